@@ -339,6 +339,148 @@ int leapquant_bf16w_decode_step(const lq_params *prm, const void *B, const lq_st
 int leapquant_bf16w_window_close(const lq_params *prm, void *B, const lq_state *st, int32_t len,
                                  hipStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Whole sequences: prompts before decode, and training.
+ *
+ * The same recurrence ([EL] Appendix Table 4) over all tokens of a packed
+ * batch of sequences, from fp32 states to fp32 states: what produces the
+ * states that leapquant_quantize_state splits for decode, and its gradient.
+ *
+ * Tokens of all sequences lie behind one another: sequence i holds tokens
+ * cu_seqlens[i] .. cu_seqlens[i + 1] - 1 (seqs + 1 int32 on the device,
+ * ascending, within [0, tokens]; a sequence may be empty).  Tokens before
+ * the first and behind the last sequence are neither read nor written.
+ * Offsets are held to [0, tokens]; offsets that do not ascend give
+ * unspecified (but in-bounds) results.  Value head h uses query and key
+ * head h / (heads_v / heads_k).  State (i, h) is block i * heads_v + h of
+ * S0 and S, [seqs * heads_v][dk][dv], the layout of leapquant_quantize_state.
+ * q and k are used as given (unit-norm keys keep the recurrence stable; the
+ * decode calls expect the same), with no scale.
+ * ------------------------------------------------------------------------- */
+
+typedef enum lq_dtype {
+  LQ_F32 = 0,
+  LQ_BF16 = 1,
+  LQ_F16 = 2
+} lq_dtype;
+
+/* A strided array [tokens][heads][128] (or [tokens][heads] for scalars):
+ * element (t, h, c) is ptr[t * token_stride + h * head_stride + c], strides
+ * in elements and not negative.  The 128 values of a head are contiguous.
+ * Arrays of heads need a 16-byte aligned ptr and strides that are whole
+ * multiples of 16 bytes; scalars need 4-byte alignment.  Inputs may repeat
+ * memory (stride 0); of an output, no two elements may be the same memory.
+ * Slices of one larger row (q, k and v out of one projection, or their
+ * gradients into one) are fine. */
+typedef struct lq_rows {
+  void *ptr;
+  int64_t token_stride;
+  int64_t head_stride;
+} lq_rows;
+
+typedef struct lq_sequence {
+  int64_t tokens;  /* rows of the token arrays, 0 .. 2^30                      */
+  int32_t seqs;    /* sequences, >= 1                                         */
+  int32_t heads_k; /* query and key heads, >= 1                               */
+  int32_t heads_v; /* value heads, a multiple of heads_k                      */
+  int32_t dk;      /* must be 128                                             */
+  int32_t dv;      /* must be 128                                             */
+  int32_t gate;    /* lq_gate                                                 */
+  uint32_t flags;  /* LQ_NO_DELTA or 0                                        */
+  int32_t dtype;   /* lq_dtype of q, k, v, o and their gradients              */
+} lq_sequence;
+
+/* Bytes of workspace that are enough for every call with these parameters
+ * and at most these tokens and seqs (0 is possible), or a negative
+ * lq_status.  save: for a forward call that a backward call follows, and for
+ * that backward call.  The workspace is 16-byte aligned device memory. */
+int64_t leapquant_sequence_workspace(const lq_sequence *sq, int32_t save);
+
+/* Forward: for every sequence and value head, from state S0 (NULL: zeros),
+ *   u_t = v_t - S_{t-1}^T b_t,  S_t = D_t S_{t-1} + k~_t u_t^T,  o_t = S_t^T q_t.
+ * Inputs: q, k [tokens][heads_k][128] and v [tokens][heads_v][128] of dtype;
+ * beta [tokens][heads_v] fp32; alpha fp32, [tokens][heads_v] (GDN) or
+ * [tokens][heads_v][128] (KDA).  Outputs: o [tokens][heads_v][128] of dtype;
+ * S the states after the last token (NULL: not wanted; may be S0 itself).
+ * Sums and states are fp32; o is rounded once.  With save != 0 the workspace
+ * afterwards holds what leapquant_sequence_backward reads.
+ *   LQ_ERR_SHAPE also: workspace_bytes too small, an output whose elements
+ *   coincide, more heads or sequences than a launch takes;
+ *   LQ_ERR_UNSUPPORTED also: save with LQ_GATE_KDA. */
+int leapquant_sequence_forward(const lq_sequence *sq, const int32_t *cu_seqlens,
+                               const lq_rows *q, const lq_rows *k, const lq_rows *v,
+                               const lq_rows *beta, const lq_rows *alpha, const lq_rows *o,
+                               const float *S0, float *S, void *workspace,
+                               int64_t workspace_bytes, int32_t save, hipStream_t stream);
+
+/* Backward (LQ_GATE_GDN): from go, the gradient of o, and dS, that of S
+ * (NULL: zeros), the gradients of q, k (summed over the value heads that
+ * share them), v, beta, alpha and S0 (dS0 NULL: not wanted).  Call with the
+ * parameters, cu_seqlens, q, k, beta and alpha of a forward call with save,
+ * and its workspace, unchanged since (backward may be called more than once
+ * on it).  Every result is summed in a fixed order. */
+int leapquant_sequence_backward(const lq_sequence *sq, const int32_t *cu_seqlens,
+                                const lq_rows *q, const lq_rows *k, const lq_rows *beta,
+                                const lq_rows *alpha, const lq_rows *go, const float *dS,
+                                const lq_rows *dq, const lq_rows *dk, const lq_rows *dv,
+                                const lq_rows *dbeta, const lq_rows *dalpha, float *dS0,
+                                void *workspace, int64_t workspace_bytes, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Norm of query and key heads, with the position rotation.
+ *
+ * What makes the unit-norm queries and keys that the calls above and the
+ * decode calls take.  For each head x of 128 values of token t:
+ *   r = (sum x^2 + eps)^-1/2 (LQ_NORM_L2) or (sum x^2 / 128 + eps)^-1/2 (LQ_NORM_RMS)
+ *   y = s * R(positions[t]) (w * x * r)
+ * with w the weight of 128 values (NULL: ones), s = q_scale for queries and 1
+ * for keys, and R the rotation of the first rot values in pairs (c, c + rot / 2),
+ * or (2c, 2c + 1) with interleaved, by the angle positions[t] * inv_freq[c],
+ * whose product is taken in 64 bits.
+ * ------------------------------------------------------------------------- */
+
+typedef enum lq_norm_kind {
+  LQ_NORM_L2 = 0,
+  LQ_NORM_RMS = 1
+} lq_norm_kind;
+
+typedef struct lq_head_norm {
+  int64_t tokens;      /* 0 .. 2^30                                            */
+  int32_t heads_q;     /* query heads, >= 0                                    */
+  int32_t heads_k;     /* key heads, >= 0; at least one head in all            */
+  int32_t dim;         /* must be 128                                          */
+  int32_t kind;        /* lq_norm_kind                                         */
+  int32_t dtype;       /* lq_dtype of q and k and of their gradients           */
+  int32_t dtype_out;   /* lq_dtype of the outputs and of their gradients       */
+  int32_t rot;         /* rotated values, 0 .. 128, a multiple of 16           */
+  int32_t interleaved; /* 0: pairs (c, c + rot / 2); 1: pairs (2c, 2c + 1)     */
+  float eps;           /* > 0                                                  */
+  float q_scale;
+  const float *q_weight;    /* [128] or NULL                                   */
+  const float *k_weight;    /* [128] or NULL                                   */
+  const int64_t *positions; /* [tokens]; NULL only with rot = 0                */
+  const double *inv_freq;   /* [rot / 2] radians per position; NULL likewise   */
+} lq_head_norm;
+
+/* q, q_out [tokens][heads_q][128], k, k_out [tokens][heads_k][128].  An
+ * output may be its own input (the same pointer, strides and dtype). */
+int leapquant_head_norm(const lq_head_norm *nm, const lq_rows *q, const lq_rows *k,
+                        const lq_rows *q_out, const lq_rows *k_out, hipStream_t stream);
+
+/* Bytes of workspace of leapquant_head_norm_backward with weight gradients,
+ * or a negative lq_status. */
+int64_t leapquant_head_norm_workspace(int64_t tokens, int32_t heads_q, int32_t heads_k);
+
+/* From the outputs' gradients gq, gk (dtype_out) and the inputs q, k, the
+ * inputs' gradients dq, dk (dtype) and the weights' dq_weight, dk_weight
+ * ([128] fp32, each NULL if not wanted; the sums over all tokens and heads in
+ * a fixed order, zeros if there are none).  The workspace is used only with a
+ * weight gradient. */
+int leapquant_head_norm_backward(const lq_head_norm *nm, const lq_rows *q, const lq_rows *k,
+                                 const lq_rows *gq, const lq_rows *gk, const lq_rows *dq,
+                                 const lq_rows *dk, float *dq_weight, float *dk_weight,
+                                 void *workspace, int64_t workspace_bytes, hipStream_t stream);
+
 /* ---- Measurement reference, no part of the method: a plain stream in
  * the decode step's launch shape.  One 64-lane wave per block of
  * read_bytes_per_wave bytes at src reads its block with 16-byte nontemporal

@@ -6,8 +6,8 @@ smoothing, as hand-written HIP kernels behind the C ABI of
 include/leapquant.h.  This package is the thin Python binding: it marshals
 torch device tensors and streams into the C calls and runs nothing itself.
 """
-from ._lib import (LQ_DENSE_BF16, LQ_DENSE_COMP, LQ_DENSE_FP32, LQ_GATE_GDN, LQ_GATE_KDA, LQ_NO_DELTA, LQ_NO_SMOOTH,
-                   LeapQuantError, LIB_PATH, load)
+from ._lib import (LQ_BF16, LQ_DENSE_BF16, LQ_DENSE_COMP, LQ_DENSE_FP32, LQ_F16, LQ_F32, LQ_GATE_GDN, LQ_GATE_KDA,
+                   LQ_NO_DELTA, LQ_NO_SMOOTH, LQ_NORM_L2, LQ_NORM_RMS, LeapQuantError, LIB_PATH, load)
 from .api import (LeapQuantState, code_offsets, codes_from_matrix, codes_to_matrix,
                   leapquant_abi_version, leapquant_bf16w_decode_step, leapquant_bf16w_window_close,
                   leapquant_decode_close, leapquant_decode_step,
@@ -15,9 +15,12 @@ from .api import (LeapQuantState, code_offsets, codes_from_matrix, codes_to_matr
                   leapquant_window_close_slots, leapquant_decode_close_list, leapquant_window_close_list,
                   leapquant_decode_step_close_list, leapquant_dequantize_state, leapquant_quantize_state,
                   leapquant_stream_reference, leapquant_status_string, leapquant_window_close)
+from .sequence import (LeapQuantSequence, leapquant_head_norm, leapquant_head_norm_backward,
+                       leapquant_head_norm_workspace, leapquant_sequence_backward, leapquant_sequence_forward)
 
 __all__ = [
-    "LQ_DENSE_BF16", "LQ_DENSE_COMP", "LQ_DENSE_FP32", "LQ_GATE_GDN", "LQ_GATE_KDA", "LQ_NO_DELTA", "LQ_NO_SMOOTH",
+    "LQ_BF16", "LQ_DENSE_BF16", "LQ_DENSE_COMP", "LQ_DENSE_FP32", "LQ_F16", "LQ_F32", "LQ_GATE_GDN", "LQ_GATE_KDA",
+    "LQ_NO_DELTA", "LQ_NO_SMOOTH", "LQ_NORM_L2", "LQ_NORM_RMS",
     "LeapQuantError", "LIB_PATH", "load",
     "LeapQuantState", "code_offsets", "codes_from_matrix", "codes_to_matrix",
     "leapquant_abi_version", "leapquant_bf16w_decode_step", "leapquant_bf16w_window_close",
@@ -26,4 +29,6 @@ __all__ = [
     "leapquant_window_close_slots", "leapquant_decode_close_list", "leapquant_window_close_list",
     "leapquant_decode_step_close_list", "leapquant_dequantize_state", "leapquant_quantize_state",
     "leapquant_stream_reference", "leapquant_status_string", "leapquant_window_close",
+    "LeapQuantSequence", "leapquant_head_norm", "leapquant_head_norm_backward", "leapquant_head_norm_workspace",
+    "leapquant_sequence_backward", "leapquant_sequence_forward",
 ]

@@ -25,6 +25,11 @@ LQ_NO_DELTA = 2
 LQ_DENSE_COMP = 4
 LQ_DENSE_FP32 = 0
 LQ_DENSE_BF16 = 1
+LQ_F32 = 0
+LQ_BF16 = 1
+LQ_F16 = 2
+LQ_NORM_L2 = 0
+LQ_NORM_RMS = 1
 
 EXPORTED = (
     "leapquant_quantize_state",
@@ -42,6 +47,12 @@ EXPORTED = (
     "leapquant_bf16w_decode_step",
     "leapquant_bf16w_window_close",
     "leapquant_stream_reference",
+    "leapquant_sequence_workspace",
+    "leapquant_sequence_forward",
+    "leapquant_sequence_backward",
+    "leapquant_head_norm",
+    "leapquant_head_norm_workspace",
+    "leapquant_head_norm_backward",
     "leapquant_status_string",
     "leapquant_abi_version",
 )
@@ -59,6 +70,24 @@ class LqState(ctypes.Structure):
                 ("comp_val", ctypes.c_void_p), ("buf_gate", ctypes.c_void_p),
                 ("buf_k", ctypes.c_void_p), ("buf_u", ctypes.c_void_p),
                 ("comp_key", ctypes.c_void_p)]
+
+
+class LqRows(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class LqSequence(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("seqs", ctypes.c_int32), ("heads_k", ctypes.c_int32),
+                ("heads_v", ctypes.c_int32), ("dk", ctypes.c_int32), ("dv", ctypes.c_int32),
+                ("gate", ctypes.c_int32), ("flags", ctypes.c_uint32), ("dtype", ctypes.c_int32)]
+
+
+class LqHeadNorm(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("heads_q", ctypes.c_int32), ("heads_k", ctypes.c_int32),
+                ("dim", ctypes.c_int32), ("kind", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("dtype_out", ctypes.c_int32), ("rot", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("q_scale", ctypes.c_float), ("q_weight", ctypes.c_void_p),
+                ("k_weight", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("inv_freq", ctypes.c_void_p)]
 
 
 class LeapQuantError(RuntimeError):
@@ -95,6 +124,17 @@ def load():
     lib.leapquant_bf16w_decode_step.argtypes = [P, vp, S, i32, vp, vp, vp, vp, vp, vp, vp]
     lib.leapquant_bf16w_window_close.argtypes = [P, vp, S, i32, vp]
     lib.leapquant_stream_reference.argtypes = [vp, ctypes.c_int64, vp, ctypes.c_int64, i32, i32, vp, vp]
+    R, Q, N, i64 = ctypes.POINTER(LqRows), ctypes.POINTER(LqSequence), ctypes.POINTER(LqHeadNorm), ctypes.c_int64
+    lib.leapquant_sequence_workspace.argtypes = [Q, i32]
+    lib.leapquant_sequence_forward.argtypes = [Q, vp, R, R, R, R, R, R, vp, vp, vp, i64, i32, vp]
+    lib.leapquant_sequence_backward.argtypes = [Q, vp, R, R, R, R, R, vp, R, R, R, R, R, vp, vp, i64, vp]
+    lib.leapquant_head_norm.argtypes = [N, R, R, R, R, vp]
+    lib.leapquant_head_norm_workspace.argtypes = [i64, i32, i32]
+    lib.leapquant_head_norm_backward.argtypes = [N, R, R, R, R, R, R, vp, vp, vp, i64, vp]
+    lib.leapquant_sequence_workspace.restype = lib.leapquant_head_norm_workspace.restype = i64
+    for f in ("leapquant_sequence_forward", "leapquant_sequence_backward", "leapquant_head_norm",
+              "leapquant_head_norm_backward"):
+        getattr(lib, f).restype = ctypes.c_int
     for f in ("leapquant_quantize_state", "leapquant_decode_step", "leapquant_window_close",
               "leapquant_decode_close", "leapquant_dense_step", "leapquant_decode_step_slots",
               "leapquant_decode_close_slots", "leapquant_window_close_slots",

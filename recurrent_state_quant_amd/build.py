@@ -7,9 +7,11 @@ PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
 LIB_PATH = os.path.join(PKG_DIR, "libleapquant.so")
 KERNEL_SOURCES = ("lq_device.h", "lq_decode_one.h", "lq_decode_body.inc", "lq_close16_body.inc", "lq_decode.hip",
-                  "lq_close.hip", "lq_baselines.hip")
+                  "lq_close.hip", "lq_baselines.hip", "lq_sequence.h", "lq_sequence_device.h", "lq_sequence.hip",
+                  "lq_sequence_grad.hip", "lq_norm.hip")
 SOURCES = [os.path.join(PKG_DIR, "csrc", f) for f in ("lq_decode.hip", "lq_close.hip", "lq_baselines.hip",
-                                                     "lq_abi.cpp")]
+                                                     "lq_sequence.hip", "lq_sequence_grad.hip", "lq_norm.hip",
+                                                     "lq_abi.cpp", "lq_sequence_abi.cpp")]
 ARCH = "gfx950"
 
 
