@@ -16,18 +16,25 @@ struct Rows {
   int64_t ts, hs;
 };
 
-// What the chunk kernels hand on, per chunk slot and value head (fp32).  A
-// slot is one chunk of one sequence: sequence i, chunk c has slot
-// cu[i] / 64 + i + c, so `slots` = tokens / 64 + seqs slots cover any split
-// of the tokens into sequences without a pass that counts them.
+// What the chunk kernels hand on, per chunk slot and head.  A slot is one
+// chunk of one sequence: sequence i, chunk c has slot cu[i] / 64 + i + c, so
+// `slots` = tokens / 64 + seqs slots cover any split of the tokens into
+// sequences without a pass that counts them.  The matrices are kept as
+// operands of the scans: bf16 parts in fragments of 16 rows x 32 contraction
+// indexes (64 lanes x 16 bytes a part; n parts: 1 of bf16 inputs, 2 of fp16,
+// 3 of fp32 ones).  P has 3 parts of room.
 struct SeqSpace {
-  float *T;    // [slots][hv][64][64]  (I + M)^-1
-  float *P;    // [slots][hv][64][64]  decayed, beta-weighted q k^T
-  float *dec;  // [slots][hv][2][64]   decay from the chunk's start; beta times decay to its end
-  float *U;    // [slots][hv][64][128] u_t
-  float *S;    // [slots][hv][dv][dk]  state at the chunk's start, transposed
-  float *X;    // [slots][hv][64][128] backward: gradient of v
-  float *G;    // [slots][hv][dv][dk]  backward: gradient of the state at the chunk's end, transposed
+  uint16_t *T, *P;        // [slots][hv][4][2][3]  (I + M)^-1; decayed, beta-weighted q k^T
+  uint16_t *K, *Q;        // [slots][hk][4][4][n]
+  uint16_t *KT;           // [slots][hk][8][2][n]
+  float *dec;             // [slots][hv][2][64]    decay from the chunk's start; beta times decay to its end
+  // kept for the backward pass (else nullptr)
+  uint16_t *TT, *PT;      // [slots][hv][4][2][3]  their transposes
+  uint16_t *QT;           // [slots][hk][8][2][n]
+  float *U;               // [slots][hv][64][128]  u_t
+  float *S;               // [slots][hv][dk][dv]   state at the chunk's start
+  float *X;               // [slots][hv][64][128]  backward: gradient of v
+  float *G;               // [slots][hv][dk][dv]   backward: gradient of the state at the chunk's end
 };
 
 struct SeqArgs {
@@ -58,6 +65,11 @@ struct NormArgs {
   float *dwq, *dwk;       // [128] or nullptr
   float *part;            // backward: [blocks][2][128] partial weight gradients
 };
+
+// Columns of the state that a workgroup of the scans takes: 32 halve the
+// reads of the operands that its column blocks share, 16 double the
+// workgroups of a few heads.
+inline bool scan_wide(const SeqArgs &a) { return (int64_t)a.seqs * a.hv * 4 >= 256; }
 
 // dtype: 0 fp32, 1 bf16, 2 fp16
 hipError_t launch_seq_recurrent(const SeqArgs &a, int dtype, bool kda, bool delta, hipStream_t stream);

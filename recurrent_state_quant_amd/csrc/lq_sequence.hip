@@ -13,10 +13,10 @@
 //                (I + M) U = V - G * (K S0),   M_ij = L_ij beta_j k_i.k_j  (j < i)
 //                O = G * (Q S0) + P U,         P_ij = L_ij beta_j q_i.k_j  (j <= i)
 //                S_C = G_C S0 + (kappa * K)^T U
-//              in three launches: prep (T = (I + M)^-1 and P of every chunk,
-//              in parallel), scan (U and S from chunk to chunk; the columns
+//              in two launches: prep (T = (I + M)^-1 and P of every chunk, in
+//              parallel) and scan (U, O and S from chunk to chunk; the columns
 //              of S are independent, so a head's scan is spread over
-//              workgroups by columns), out (O of every chunk, in parallel).
+//              workgroups by columns).
 #include "lq_sequence_device.h"
 
 namespace lq {
@@ -128,293 +128,472 @@ __global__ __launch_bounds__(256) void seq_recurrent_kernel(const SeqArgs A) {
 }
 
 // ---------------------------------------------------------------------------
-// Prep: one workgroup per (slot, key head); the value heads that share it in
-// turn.  q k^T and k k^T are taken once.  T by blocks of 16: each diagonal
-// block by forward substitution (a column per lane), then T_ab = -T_aa sum_c
-// M_ac T_cb by distance from the diagonal.
+// Prep: one workgroup per (slot, value head).  Writes, in the order in which
+// the scans load them (matrix fragments, bf16 parts): T, P, and, for the first
+// value head of a key head, K^T (and K and Q where they are not their own only
+// part); with SAVE also the transposes of T, P and Q for the backward scan.  M and T are fp32; T by blocks of 16: each diagonal block by forward
+// substitution (a column per lane), then 16 -> 32 -> 64 by T_ba = -T_b (M_ba
+// T_a) on the fp32 matrix path.
 // ---------------------------------------------------------------------------
-template <class E, bool DELTA>
+template <class E, bool DELTA, bool SAVE>
 __global__ __launch_bounds__(256) void seq_prep_kernel(const SeqArgs A) {
-  const int slot = blockIdx.x, hk = blockIdx.y;
-  const int tid = threadIdx.x, w = tid >> 6, lane = tid & 63;
+  constexpr int NP = Parts<E>::n, LDH = D + 8, kPlane = C * LDH;
+  const int slot = blockIdx.x, hv = blockIdx.y, hk = hv / A.group;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const Chunk ch = find_chunk(A, slot, lane);
   if (ch.len == 0) return;
-  __shared__ float sh_k[C * LDD];
-  __shared__ float sh_l[C * LDC];
-  __shared__ float sh_m[C * LDC];
-  __shared__ float sh_t[C * LDC];
-  __shared__ float sh_a[C], sh_b[C];
-  stage_rows<E>(sh_k, A.k, hk, ch.t0, ch.len, tid);
-  __syncthreads();
-  const int i0 = 16 * w + 4 * (lane >> 4), j0 = lane & 15;
-  floatx4 qk[4], kk[4];
+  const size_t at_ = (size_t)slot * A.hv + hv, atk = (size_t)slot * A.hk + hk;
+  const bool first = hv % A.group == 0;
+  __shared__ __align__(16) uint16_t sh_k[NP * kPlane];  // K's parts; then (as fp32 [64][LDC]) T
+  __shared__ __align__(16) float sh_l[C * LDC];         // L, then P
+  __shared__ __align__(16) float sh_m[C * LDC];         // M; above its diagonal blocks: products on their way to T
+  __shared__ __align__(16) float sh_a[C];
+  __shared__ float sh_b[C];
+  float *const sh_t = reinterpret_cast<float *>(sh_k);
+  static_assert(sizeof(sh_k) >= sizeof(float) * C * LDC, "T fits over K");
+  const int i = lane & 15, g = lane >> 4;
+
+  {
+    const int row = tid >> 2, c0 = (tid & 3) * 8;
 #pragma unroll
-  for (int n = 0; n < 4; ++n) qk[n] = kk[n] = floatx4{0.f, 0.f, 0.f, 0.f};
-  for (int x = 0; x < D / 16; ++x) {
-    const float4 fq = frag_rows<E>(A.q, hk, ch.t0, ch.len, 16 * w, x, lane);
-    const float4 fk = frag<false>(sh_k, LDD, 16 * w, x, lane);
-    for (int n = 0; n <= w; ++n) {
-      const float4 fb = frag<false>(sh_k, LDD, 16 * n, x, lane);
-      mma(qk[n], fq, fb);
-      if (DELTA) mma(kk[n], fk, fb);
+    for (int c = 0; c < 4; ++c) {
+      bf8 f[NP];
+#pragma unroll
+      for (int n = 0; n < NP; ++n) f[n] = bf8{};
+      if (row < ch.len) parts_load<E, NP>(f, at<const E>(A.k, ch.t0 + row, hk) + c0 + 32 * c);
+#pragma unroll
+      for (int n = 0; n < NP; ++n) *reinterpret_cast<bf8 *>(sh_k + n * kPlane + row * LDH + c0 + 32 * c) = f[n];
     }
   }
-  for (int g = 0; g < A.group; ++g) {
-    const int hv = hk * A.group + g;
-    const size_t at_ = (size_t)slot * A.hv + hv;
-    __syncthreads();
-    if (w == 0) {
-      const bool in = lane < ch.len;
-      const float al = in ? *at<const float>(A.alpha, ch.t0 + lane, hv) : 1.f;
-      const float be = in ? *at<const float>(A.beta, ch.t0 + lane, hv) : 0.f;
-      sh_a[lane] = al;
-      sh_b[lane] = be;
-      // decay from the chunk's start (inclusive prefix product) and to its
-      // end (exclusive suffix product)
-      float pre = al, suf = __shfl_down(al, 1);  // (every lane takes part in a shuffle)
-      suf = lane < 63 ? suf : 1.f;
+  bf8 fq[4][NP];
 #pragma unroll
-      for (int d = 1; d < 64; d <<= 1) {
-        const float x = __shfl_up(pre, d), y = __shfl_down(suf, d);
-        if (lane >= d) pre *= x;
-        if (lane + d < 64) suf *= y;
-      }
-      A.w.dec[at_ * 2 * C + lane] = pre;
-      A.w.dec[at_ * 2 * C + C + lane] = suf * be;
+  for (int x = 0; x < 4; ++x) {
+#pragma unroll
+    for (int n = 0; n < NP; ++n) fq[x][n] = bf8{};
+    if (16 * w + i < ch.len) parts_load<E, NP>(fq[x], at<const E>(A.q, ch.t0 + 16 * w + i, hk) + 32 * x + 8 * g);
+  }
+  if (w == 0) {
+    const bool in = lane < ch.len;
+    const float al = in ? *at<const float>(A.alpha, ch.t0 + lane, hv) : 1.f;
+    const float be = in ? *at<const float>(A.beta, ch.t0 + lane, hv) : 0.f;
+    sh_a[lane] = al;
+    sh_b[lane] = be;
+    // decay from the chunk's start (inclusive prefix product) and to its
+    // end (exclusive suffix product)
+    float pre = al, suf = __shfl_down(al, 1);  // (every lane takes part in a shuffle)
+    suf = lane < 63 ? suf : 1.f;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const float x = __shfl_up(pre, d), y = __shfl_down(suf, d);
+      if (lane >= d) pre *= x;
+      if (lane + d < 64) suf *= y;
     }
-    __syncthreads();
-    decay_matrix(sh_l, sh_a, tid);
-    __syncthreads();
-    float *P = A.w.P + at_ * C * C;
+    A.w.dec[at_ * 2 * C + lane] = pre;
+    A.w.dec[at_ * 2 * C + C + lane] = suf * be;
+  }
+  __syncthreads();
+  decay_matrix(sh_l, sh_a, w, lane);
+  Acc2 aq[4], ak[4];
+#pragma unroll
+  for (int n = 0; n < 4; ++n) aq[n] = ak[n] = acc2_zero();
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    bf8 fk[NP];
+    if (DELTA || first) frag16<NP>(fk, sh_k, kPlane, LDH, 16 * w, 32 * x, lane);
+    if (first) {
+      frag_store<NP>(A.w.K + ((atk * 4 + w) * 4 + x) * NP * 512, fk, lane);
+      frag_store<NP>(A.w.Q + ((atk * 4 + w) * 4 + x) * NP * 512, fq[x], lane);
+    }
 #pragma unroll
     for (int n = 0; n < 4; ++n) {
-      const int j = 16 * n + j0;
-      const float be = sh_b[j];
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int i = i0 + r;
-        const float lb = sh_l[i * LDC + j] * be;
-        P[i * C + j] = j <= i ? lb * qk[n][r] : 0.f;
-        if (DELTA) sh_m[i * LDC + j] = j < i ? lb * kk[n][r] : 0.f;
+      if (n <= w) {
+        bf8 fb[NP];
+        frag16<NP>(fb, sh_k, kPlane, LDH, 16 * n, 32 * x, lane);
+        mma_parts<NP, NP>(aq[n], fq[x], fb);
+        if (DELTA) mma_parts<NP, NP>(ak[n], fk, fb);
       }
     }
-    if (!DELTA) continue;
+  }
+  if (first) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {  // key rows 32 w .. + 31, token steps of 32
+      const int mt = 2 * w + (e >> 1), x = e & 1;
+      bf8 f[NP];
+      frag_gather<NP>(f, sh_k, kPlane, LDH, 16 * mt, 32 * x, lane);
+      frag_store<NP>(A.w.KT + ((atk * 8 + mt) * 2 + x) * NP * 512, f, lane);
+    }
+  }
+  __syncthreads();  // L is whole, K's parts are read
+#pragma unroll
+  for (int n = 0; n < 4; ++n) {
+    const int j = 16 * n + i;
+    const float be = sh_b[j];
+    const floatx4 qk = aq[n].sum(), kk = ak[n].sum();
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int row = 16 * w + 4 * g + r;
+      const float lb = sh_l[row * LDC + j] * be;
+      sh_l[row * LDC + j] = j <= row ? lb * qk[r] : 0.f;
+      if (DELTA && n <= w) sh_m[row * LDC + j] = j < row ? lb * kk[r] : 0.f;
+    }
+  }
+  if (DELTA) {
     __syncthreads();
-    // diagonal blocks: wave w, column lane & 15 (four lanes do the same)
     {
+      // diagonal block w, column i (the four groups of lanes do the same)
       const int d0 = 16 * w;
       float t[16];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        float x = i == j0 ? 1.f : 0.f;
+      for (int a = 0; a < 16; ++a) {
+        float x = a == i ? 1.f : 0.f;
 #pragma unroll
-        for (int l = 0; l < i; ++l) x = fmaf(-sh_m[(d0 + i) * LDC + d0 + l], t[l], x);
-        t[i] = x;
+        for (int l = 0; l < a; ++l) x = fmaf(-sh_m[(d0 + a) * LDC + d0 + l], t[l], x);
+        t[a] = x;
       }
+      // group g stores rows 4 g .. + 3
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        if (lane < 16) sh_t[(d0 + i) * LDC + d0 + j0] = t[i];
-      }
-    }
-    const int bi = tid >> 4, bj = tid & 15;
-    for (int dist = 1; dist < 4; ++dist) {
-      __syncthreads();
-      float x[3];
-      for (int a = dist; a < 4; ++a) {
-        const int b = a - dist;
-        float y = 0.f;
-        for (int c = b; c < a; ++c)
-#pragma unroll
-          for (int l = 0; l < 16; ++l)
-            y = fmaf(sh_m[(16 * a + bi) * LDC + 16 * c + l], sh_t[(16 * c + l) * LDC + 16 * b + bj], y);
-        // kept in the upper triangle of sh_m, which is not read
-        sh_m[(16 * b + bi) * LDC + 16 * a + bj] = y;
-      }
-      __syncthreads();
-      for (int a = dist; a < 4; ++a) {
-        const int b = a - dist;
-        float y = 0.f;
-#pragma unroll
-        for (int l = 0; l < 16; ++l)
-          y = fmaf(sh_t[(16 * a + bi) * LDC + 16 * a + l], sh_m[(16 * b + l) * LDC + 16 * a + bj], y);
-        x[a - 1] = -y;
-      }
-      for (int a = dist; a < 4; ++a) sh_t[(16 * a + bi) * LDC + 16 * (a - dist) + bj] = x[a - 1];
+      for (int a = 0; a < 16; ++a)
+        if ((a >> 2) == g) sh_t[(d0 + a) * LDC + d0 + i] = t[a];
     }
     __syncthreads();
-    float *T = A.w.T + at_ * C * C;
-    for (int e = tid; e < C * C; e += 256) {
-      const int i = e >> 6, j = e & 63;
-      T[e] = (j >> 4) <= (i >> 4) ? sh_t[i * LDC + j] : 0.f;
+    const floatx4 zero = {0.f, 0.f, 0.f, 0.f};
+    if (w < 2) {
+      const int b = 2 * w, a = b + 1;
+      floatx4 y = zero, z = zero;
+      mma(y, frag<false>(sh_m + 16 * b, LDC, 16 * a, 0, lane), frag<true>(sh_t + 16 * b * LDC, LDC, 16 * b, 0, lane));
+      // the product, transposed, to block (b, a) of sh_m
+      *reinterpret_cast<float4 *>(sh_m + (16 * b + i) * LDC + 16 * a + 4 * g) = make_float4(y[0], y[1], y[2], y[3]);
+      mma(z, frag<false>(sh_t + 16 * a, LDC, 16 * a, 0, lane), frag<false>(sh_m + 16 * a, LDC, 16 * b, 0, lane));
+#pragma unroll
+      for (int r = 0; r < 4; ++r) sh_t[(16 * a + 4 * g + r) * LDC + 16 * b + i] = -z[r];
     }
+    __syncthreads();
+    const int a = 2 + (w >> 1), b = w & 1;
+    {
+      floatx4 y = zero;
+      for (int c = b; c < 2; ++c)
+        mma(y, frag<false>(sh_m + 16 * c, LDC, 16 * a, 0, lane), frag<true>(sh_t + 16 * c * LDC, LDC, 16 * b, 0, lane));
+      *reinterpret_cast<float4 *>(sh_m + (16 * b + i) * LDC + 16 * a + 4 * g) = make_float4(y[0], y[1], y[2], y[3]);
+    }
+    __syncthreads();
+    {
+      floatx4 z = zero;
+      for (int c = 2; c <= a; ++c)
+        mma(z, frag<false>(sh_t + 16 * c, LDC, 16 * a, 0, lane), frag<false>(sh_m + 16 * c, LDC, 16 * b, 0, lane));
+#pragma unroll
+      for (int r = 0; r < 4; ++r) sh_t[(16 * a + 4 * g + r) * LDC + 16 * b + i] = -z[r];
+    }
+  }
+  __syncthreads();
+  // rows 16 w + i, columns 32 x + 8 g .. + 7 of T and P; T's block above the
+  // diagonal in a step is not written there: zeros
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    if (2 * x > w) continue;
+    const int row = 16 * w + i, col = 32 * x + 8 * g;
+    float v[8];
+    bf8 f[3];
+    if (DELTA) {
+      const bool in = (col >> 4) <= w;
+      const float4 *s = reinterpret_cast<const float4 *>(sh_t + row * LDC + col);
+      const float4 u0 = in ? s[0] : make_float4(0.f, 0.f, 0.f, 0.f), u1 = in ? s[1] : make_float4(0.f, 0.f, 0.f, 0.f);
+      v[0] = u0.x; v[1] = u0.y; v[2] = u0.z; v[3] = u0.w;
+      v[4] = u1.x; v[5] = u1.y; v[6] = u1.z; v[7] = u1.w;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = col + e <= row ? v[e] : 0.f;
+      split8<3>(v, f);
+      frag_store<3>(A.w.T + ((at_ * 4 + w) * 2 + x) * 3 * 512, f, lane);
+    }
+    const float4 *s = reinterpret_cast<const float4 *>(sh_l + row * LDC + col);
+    v[0] = s[0].x; v[1] = s[0].y; v[2] = s[0].z; v[3] = s[0].w;
+    v[4] = s[1].x; v[5] = s[1].y; v[6] = s[1].z; v[7] = s[1].w;
+    split8<3>(v, f);
+    frag_store<3>(A.w.P + ((at_ * 4 + w) * 2 + x) * 3 * 512, f, lane);
+  }
+  if (!SAVE) return;
+  // transposes for the backward scan: columns 16 w + i, rows 32 x + 8 g .. + 7
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    if (x < (w >> 1)) continue;
+    const int col = 16 * w + i, row = 32 * x + 8 * g;
+    float v[8];
+    bf8 f[3];
+    if (DELTA) {
+      const bool in = (row >> 4) >= w;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = in && row + e >= col ? sh_t[(row + e) * LDC + col] : 0.f;
+      split8<3>(v, f);
+      frag_store<3>(A.w.TT + ((at_ * 4 + w) * 2 + x) * 3 * 512, f, lane);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = sh_l[(row + e) * LDC + col];
+    split8<3>(v, f);
+    frag_store<3>(A.w.PT + ((at_ * 4 + w) * 2 + x) * 3 * 512, f, lane);
+  }
+  if (!first) return;
+  __syncthreads();
+#pragma unroll
+  for (int x = 0; x < 4; ++x)
+#pragma unroll
+    for (int n = 0; n < NP; ++n)
+      *reinterpret_cast<bf8 *>(sh_k + n * kPlane + (16 * w + i) * LDH + 32 * x + 8 * g) = fq[x][n];
+  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int mt = 2 * w + (e >> 1), x = e & 1;
+    bf8 f[NP];
+    frag_gather<NP>(f, sh_k, kPlane, LDH, 16 * mt, 32 * x, lane);
+    frag_store<NP>(A.w.QT + ((atk * 8 + mt) * 2 + x) * NP * 512, f, lane);
   }
 }
 
 // ---------------------------------------------------------------------------
-// Scan: one workgroup per (sequence, value head, block of CB columns).  Wave
-// w holds rows 32 w .. 32 w + 31 of the state block in its accumulators and
-// takes token tile w of the products with 64 rows.
+// Scan: one workgroup per (sequence, value head, block of CB columns), chunk
+// after chunk.  Wave w takes token tile w (16 rows) of the products with 64
+// rows and rows 32 w .. + 31 of the state, whose block stays in its
+// accumulators; column tile n of the block holds columns NT i + n, so that a
+// lane's NT columns are neighbours in memory.
+// The operands that do not depend on the state (K, Q, T, P, K^T) are private
+// to a wave: they come straight from global memory in fragment order (a
+// wave's load is one run of 1 KiB; rows of the inputs themselves would be
+// sixteen pieces of 64 bytes and cost the address path four times as long),
+// each reloaded for the next chunk right after its use, so the loads run
+// behind the rest of the chunk.  What the waves share (S, X, U) goes through
+// LDS as bf16 parts; three barriers a chunk.
+// The output's products take the parts that its type can hold: o in 16 bits
+// is rounded at 2^-9 or 2^-12, so parts below 2^-16 are left out of Q S and
+// P U there (never out of U and S).
 // ---------------------------------------------------------------------------
-template <class E, bool DELTA, int CB>
+template <class E, bool DELTA, bool SAVE, int CB>
 __global__ __launch_bounds__(256) void seq_scan_kernel(const SeqArgs A) {
-  constexpr int NT = CB / 16, kBlocks = D / CB;
-  const int tid = threadIdx.x, w = tid >> 6, lane = tid & 63;
+  constexpr int NT = CB / 16, kBlocks = D / CB, NP = Parts<E>::n, NO = NP == 3 ? 3 : 2;
+  constexpr int FS = 4 * NT, FX = 2 * NT;  // fragments of a part of [CB][128], [CB][64]
+  const int lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   // workgroups b, b + 8, .. run on one XCD: the column blocks of one head
-  // are placed there, so that its L2 serves their common K and T
+  // are placed there, so that its L2 serves their common operands
   const int64_t b = blockIdx.x;
   const int64_t unit = (b / (8 * kBlocks)) * 8 + (b & 7);
   if (unit >= (int64_t)A.seqs * A.hv) return;
-  const int col0 = (int)((b >> 3) % kBlocks) * CB;
   const int seq = (int)(unit / A.hv), hv = (int)(unit % A.hv), hk = hv / A.group;
   const int start = seq_start(A, seq), end = seq_end(A, seq, start);
-  __shared__ float sh_k[C * LDD];
-  __shared__ float sh_T[DELTA ? C * LDC : 1];
-  __shared__ float sh_s[CB * LDD];  // S^T
-  __shared__ float sh_x[CB * LDC];  // X^T
-  __shared__ float sh_u[CB * LDC];  // (kappa * U)^T
-  const int i = lane & 15, g = lane >> 4;
+  __shared__ __align__(16) uint16_t sh_s[3 * FS * 512];              // S, [column][key row]
+  __shared__ __align__(16) uint16_t sh_x[DELTA ? 3 * FX * 512 : 8];  // X, [column][token]
+  __shared__ __align__(16) uint16_t sh_u[NO * FX * 512];             // U
+  __shared__ __align__(16) uint16_t sh_ku[3 * FX * 512];             // kappa * U
+  __shared__ __align__(16) float sh_dec[2][2 * C];                   // decays, of this chunk and the next
+  const int i = lane & 15, g = lane >> 4, tok = 16 * w + 4 * g;
+  const int col = (int)((b >> 3) % kBlocks) * CB + NT * i;  // the lane's first column
 
   floatx4 s[2][NT];
 #pragma unroll
   for (int m = 0; m < 2; ++m)
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int r = 0; r < 4; ++r) {
+      float x[NT] = {};
+      if (A.S0) load_n<NT>(A.S0 + (unit * D + 32 * w + 16 * m + 4 * g + r) * D + col, x);
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
-        s[m][n][r] = A.S0 ? A.S0[(unit * D + 32 * w + 16 * m + 4 * g + r) * D + col0 + 16 * n + i] : 0.f;
+      for (int n = 0; n < NT; ++n) s[m][n][r] = x[n];
+    }
+  wait_loads();  // the loop below counts its own loads only
 
-  for (int t0 = start, slot = start / C + seq; t0 < end; t0 += C, ++slot) {
-    const int len = end - t0 < C ? end - t0 : C;
-    const size_t at_ = (size_t)slot * A.hv + hv;
-    const float *dec = A.w.dec + at_ * 2 * C;
-    stage_rows<E>(sh_k, A.k, hk, t0, len, tid);
-    if (DELTA) stage_f32<C>(sh_T, LDC, A.w.T + at_ * C * C, C, tid);
+  // Loads stand at fixed places: with a branch around them the compiler could
+  // not count what is in flight and would wait for all of it.  A row past the
+  // end is the chunk's first row instead; its X is set to zero and its columns
+  // of P and K^T are zero.  V's pointer moves on from chunk to chunk (`move`:
+  // 1, or 0 where there is none: then the last chunk is read again).
+  bf8 fk[4][NP], fq[4][NP], fT[2][3], fP[2][NO], fKT[2][2][NP];
+  E v[4][NT];
+  float dec;  // thread t < 128: value t of the next chunk's decays
+  const int slot0 = start / C + seq;
+  const int chunks = (end - start + C - 1) / C;
+  const E *pV = at<const E>(A.v, start + tok, hv) + col;
+  const int64_t backV = tok * A.v.ts;
+  auto load_k = [&](int c) {
+    const size_t f = (((size_t)(slot0 + c) * A.hk + hk) * 4 + w) * 4 * NP * 512;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      if (DELTA) frag_load<NP>(fk[x], A.w.K + f + x * NP * 512, lane);
+      frag_load<NP>(fq[x], A.w.Q + f + x * NP * 512, lane);
+    }
+  };
+  auto load_v = [&](int c, int move) {
+    const int len = end - start - c * C;
+    pV += move * (C * A.v.ts);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) load_raw<NT>(tok + r < len ? pV + r * A.v.ts : pV - backV, v[r]);
+    dec = A.w.dec[((size_t)(slot0 + c) * A.hv + hv) * 2 * C + (threadIdx.x & 127)];
+  };
+  auto load_T = [&](int c) {
+    const uint16_t *p = A.w.T + (((size_t)(slot0 + c) * A.hv + hv) * 4 + w) * 2 * 3 * 512;
+    if (DELTA) {
+      frag_load<3>(fT[0], p, lane);
+      if (w >= 2) frag_load<3>(fT[1], p + 3 * 512, lane);
+    }
+  };
+  auto load_P = [&](int c) {
+    const uint16_t *p = A.w.P + (((size_t)(slot0 + c) * A.hv + hv) * 4 + w) * 2 * 3 * 512;
+    frag_load<NO>(fP[0], p, lane);
+    if (w >= 2) frag_load<NO>(fP[1], p + 3 * 512, lane);
+  };
+  auto load_KT = [&](int c) {
+    const uint16_t *p = A.w.KT + (((size_t)(slot0 + c) * A.hk + hk) * 8 + 2 * w) * 2 * NP * 512;
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const float4 x = make_float4(s[m][n][0], s[m][n][1], s[m][n][2], s[m][n][3]);
-        const int row = 32 * w + 16 * m + 4 * g, col = 16 * n + i;
-        *reinterpret_cast<float4 *>(sh_s + col * LDD + row) = x;
-        *reinterpret_cast<float4 *>(A.w.S + (at_ * D + col0 + col) * D + row) = x;
-      }
-    __syncthreads();
-    const int tok = 16 * w + 4 * g;
-    floatx4 u[NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) u[n] = floatx4{0.f, 0.f, 0.f, 0.f};
-    if (DELTA) {
-      for (int x = 0; x < D / 16; ++x) {
-        const float4 fa = frag<false>(sh_k, LDD, 16 * w, x, lane);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) mma(u[n], fa, frag<false>(sh_s, LDD, 16 * n, x, lane));
-      }
-    }
-    float kap[4];
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      kap[r] = dec[C + tok + r];
-      const float gam = dec[tok + r];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const float v = tok + r < len ? to_f(at<const E>(A.v, t0 + tok + r, hv)[col0 + 16 * n + i]) : 0.f;
-        u[n][r] = v - gam * u[n][r];
-      }
-    }
-    if (DELTA) {
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        *reinterpret_cast<float4 *>(sh_x + (16 * n + i) * LDC + tok) =
-            make_float4(u[n][0], u[n][1], u[n][2], u[n][3]);
-        u[n] = floatx4{0.f, 0.f, 0.f, 0.f};
-      }
-      __syncthreads();
-      for (int x = 0; x <= w; ++x) {
-        const float4 fa = frag<false>(sh_T, LDC, 16 * w, x, lane);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) mma(u[n], fa, frag<false>(sh_x, LDC, 16 * n, x, lane));
-      }
-    }
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-#pragma unroll
-      for (int r = 0; r < 4; ++r) A.w.U[(at_ * C + tok + r) * D + col0 + 16 * n + i] = u[n][r];
-      *reinterpret_cast<float4 *>(sh_u + (16 * n + i) * LDC + tok) =
-          make_float4(kap[0] * u[n][0], kap[1] * u[n][1], kap[2] * u[n][2], kap[3] * u[n][3]);
-    }
-    const float last = dec[C - 1];
-    __syncthreads();
+      for (int x = 0; x < 2; ++x) frag_load<NP>(fKT[m][x], p + (2 * m + x) * NP * 512, lane);
+  };
+  if (chunks) {
+    load_k(0);
+    load_v(0, 0);
+    load_T(0);
+    load_KT(0);
+    load_P(0);
+    if (threadIdx.x < 2 * C) sh_dec[0][threadIdx.x] = dec;
+  }
+  for (int c = 0; c < chunks; ++c) {
+    const int t0 = start + c * C, len = end - t0;
+    const int move = c + 1 < chunks ? 1 : 0, next = c + move;
+    const size_t at_ = (size_t)(slot0 + c) * A.hv + hv;
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
 #pragma unroll
-      for (int n = 0; n < NT; ++n) s[m][n] *= last;
-      for (int x = 0; x < C / 16; ++x) {
-        const float4 fa = frag<true>(sh_k, LDD, 32 * w + 16 * m, x, lane);
+      for (int n = 0; n < NT; ++n)
+        frag_share<3, FS>(sh_s, 4 * n + w, m, lane, s[m][n][0], s[m][n][1], s[m][n][2], s[m][n][3]);
+      if (SAVE) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n) mma(s[m][n], fa, frag<false>(sh_u, LDC, 16 * n, x, lane));
+        for (int r = 0; r < 4; ++r) {
+          float x[NT];
+#pragma unroll
+          for (int n = 0; n < NT; ++n) x[n] = s[m][n][r];
+          store_n<NT>(A.w.S + (at_ * D + 32 * w + 16 * m + 4 * g + r) * D + col, x);
+        }
       }
     }
-    __syncthreads();
+    lds_barrier();
+    Acc2 yk[NT], yq[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) yk[n] = yq[n] = acc2_zero();
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        bf8 fs[3];
+        frag_get<3, FS>(fs, sh_s, 4 * n + x, lane);
+        if (DELTA) mma_parts<NP, 3>(yk[n], fk[x], fs);
+        mma_parts<NP, 3, NO>(yq[n], fq[x], fs);
+      }
+    load_k(next);
+    const float *sd = sh_dec[c & 1];
+    const float4 gm4 = *reinterpret_cast<const float4 *>(sd + tok), kp4 = *reinterpret_cast<const float4 *>(sd + C + tok);
+    const float gm[4] = {gm4.x, gm4.y, gm4.z, gm4.w}, kp[4] = {kp4.x, kp4.y, kp4.z, kp4.w};
+    const float la = sd[C - 1];
+    floatx4 u[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const floatx4 y = yk[n].sum();
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float x = to_f(v[r][n]);
+        u[n][r] = tok + r < len ? (DELTA ? x - gm[r] * y[r] : x) : 0.f;
+        yq[n].a[r] = gm[r] * (yq[n].a[r] + yq[n].b[r]);
+        yq[n].b[r] = 0.f;
+      }
+    }
+    load_v(next, move);
+    if (DELTA) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        frag_share<3, FX>(sh_x, 2 * n + (w >> 1), w & 1, lane, u[n][0], u[n][1], u[n][2], u[n][3]);
+      lds_barrier();
+      Acc2 y[NT];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) y[n] = acc2_zero();
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        if (2 * x <= w) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            bf8 fx[3];
+            frag_get<3, FX>(fx, sh_x, 2 * n + x, lane);
+            mma_parts<3, 3>(y[n], fT[x], fx);
+          }
+        }
+      }
+      load_T(next);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) u[n] = y[n].sum();
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      frag_share<3, FX>(sh_ku, 2 * n + (w >> 1), w & 1, lane, kp[0] * u[n][0], kp[1] * u[n][1], kp[2] * u[n][2],
+                        kp[3] * u[n][3]);
+      frag_share<NO, FX>(sh_u, 2 * n + (w >> 1), w & 1, lane, u[n][0], u[n][1], u[n][2], u[n][3]);
+    }
+    if (SAVE) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        float x[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) x[n] = u[n][r];
+        store_n<NT>(A.w.U + (at_ * C + tok + r) * D + col, x);
+      }
+    }
+    lds_barrier();
+    Acc2 ds[2][NT];
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) ds[m][n] = acc2_zero();
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        bf8 fu[3];
+        frag_get<3, FX>(fu, sh_ku, 2 * n + x, lane);
+#pragma unroll
+        for (int m = 0; m < 2; ++m) mma_parts<NP, 3>(ds[m][n], fKT[m][x], fu);
+      }
+    load_KT(next);
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      if (2 * x <= w) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          bf8 fu[NO];
+          frag_get<NO, FX>(fu, sh_u, 2 * n + x, lane);
+          mma_parts<NO, NO, NO>(yq[n], fP[x], fu);
+        }
+      }
+    }
+    load_P(next);
+    if (threadIdx.x < 2 * C) sh_dec[(c + 1) & 1][threadIdx.x] = dec;
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) s[m][n] = s[m][n] * la + ds[m][n].sum();
+    E *o = at<E>(A.o, t0 + tok, hv) + col;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      if (tok + r < len) {
+        E x[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) x[n] = from_f<E>(yq[n].a[r] + yq[n].b[r]);
+        store_raw<NT>(o + r * A.o.ts, x);
+      }
+    }
   }
   if (A.S) {
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int r = 0; r < 4; ++r) {
+        float x[NT];
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          A.S[(unit * D + 32 * w + 16 * m + 4 * g + r) * D + col0 + 16 * n + i] = s[m][n][r];
-  }
-}
-
-// ---------------------------------------------------------------------------
-// Out: one workgroup per (slot, value head); wave w takes token tile w.
-// ---------------------------------------------------------------------------
-template <class E>
-__global__ __launch_bounds__(256) void seq_out_kernel(const SeqArgs A) {
-  const int slot = blockIdx.x, hv = blockIdx.y, hk = hv / A.group;
-  const int tid = threadIdx.x, w = tid >> 6, lane = tid & 63;
-  const Chunk ch = find_chunk(A, slot, lane);
-  if (ch.len == 0) return;
-  const size_t at_ = (size_t)slot * A.hv + hv;
-  __shared__ float sh_b[C * LDD];
-  const int i = lane & 15, g = lane >> 4, tok = 16 * w + 4 * g;
-  floatx4 acc[8];
-#pragma unroll
-  for (int n = 0; n < 8; ++n) acc[n] = floatx4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {  // columns 64 h .. 64 h + 63 of S
-    __syncthreads();
-    stage_f32<D>(sh_b, LDD, A.w.S + (at_ * D + 64 * h) * D, 64, tid);
-    __syncthreads();
-    for (int x = 0; x < D / 16; ++x) {
-      const float4 fa = frag_rows<E>(A.q, hk, ch.t0, ch.len, 16 * w, x, lane);
-#pragma unroll
-      for (int n = 0; n < 4; ++n) mma(acc[4 * h + n], fa, frag<false>(sh_b, LDD, 16 * n, x, lane));
-    }
-  }
-#pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const float gam = A.w.dec[at_ * 2 * C + tok + r];
-#pragma unroll
-    for (int n = 0; n < 8; ++n) acc[n][r] *= gam;
-  }
-  __syncthreads();
-  stage_f32<D>(sh_b, LDD, A.w.U + at_ * C * D, C, tid);
-  __syncthreads();
-  const float *P = A.w.P + at_ * C * C;
-  for (int x = 0; x <= w; ++x) {
-    const float4 fa = frag<false>(P, C, 16 * w, x, lane);
-#pragma unroll
-    for (int n = 0; n < 8; ++n) mma(acc[n], fa, frag<true>(sh_b, LDD, 16 * n, x, lane));
-  }
-#pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    if (tok + r < ch.len) {
-      E *o = at<E>(A.o, ch.t0 + tok + r, hv);
-#pragma unroll
-      for (int n = 0; n < 8; ++n) o[16 * n + i] = from_f<E>(acc[n][r]);
-    }
+        for (int n = 0; n < NT; ++n) x[n] = s[m][n][r];
+        store_n<NT>(A.S + (unit * D + 32 * w + 16 * m + 4 * g + r) * D + col, x);
+      }
   }
 }
 
@@ -444,18 +623,21 @@ hipError_t launch_seq_recurrent(const SeqArgs &a, int dtype, bool kda, bool delt
                       : recurrent<F16>(a, kda, delta, stream);
 }
 
-template <class E, bool DELTA>
+template <class E, bool DELTA, bool SAVE>
 hipError_t chunked(const SeqArgs &a, hipStream_t stream) {
-  const dim3 slots((unsigned)a.slots, a.hk), heads((unsigned)a.slots, a.hv);
   const int64_t units = ((int64_t)a.seqs * a.hv + 7) / 8 * 8;
-  hipLaunchKernelGGL((seq_prep_kernel<E, DELTA>), slots, dim3(256), 0, stream, a);
-  hipLaunchKernelGGL((seq_scan_kernel<E, DELTA, 16>), dim3((unsigned)(units * (D / 16))), dim3(256), 0, stream, a);
-  hipLaunchKernelGGL((seq_out_kernel<E>), heads, dim3(256), 0, stream, a);
+  hipLaunchKernelGGL((seq_prep_kernel<E, DELTA, SAVE>), dim3((unsigned)a.slots, a.hv), dim3(256), 0, stream, a);
+  if (scan_wide(a))
+    hipLaunchKernelGGL((seq_scan_kernel<E, DELTA, SAVE, 32>), dim3((unsigned)(units * 4)), dim3(256), 0, stream, a);
+  else
+    hipLaunchKernelGGL((seq_scan_kernel<E, DELTA, SAVE, 16>), dim3((unsigned)(units * 8)), dim3(256), 0, stream, a);
   return hipGetLastError();
 }
 template <class E>
 hipError_t chunked(const SeqArgs &a, bool delta, hipStream_t stream) {
-  return delta ? chunked<E, true>(a, stream) : chunked<E, false>(a, stream);
+  const bool save = a.w.S != nullptr;
+  if (delta) return save ? chunked<E, true, true>(a, stream) : chunked<E, true, false>(a, stream);
+  return save ? chunked<E, false, true>(a, stream) : chunked<E, false, false>(a, stream);
 }
 hipError_t launch_seq_chunked(const SeqArgs &a, int dtype, bool delta, hipStream_t stream) {
   return dtype == 0 ? chunked<F32>(a, delta, stream)

@@ -2,12 +2,14 @@
 // validation and launches.  Semantics are documented in include/leapquant.h.
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "leapquant.h"
 #include "lq_sequence.h"
 
 namespace {
 
-constexpr int64_t kDim = 128;
+constexpr int64_t kDim = 128, kState = kDim * kDim;
 constexpr int64_t kMaxTokens = int64_t(1) << 30;
 constexpr int64_t kMaxGrid = int64_t(1) << 23;  // workgroups of a launch: 512 lanes each stay below 2^32
 constexpr int64_t kMaxHeads = 65535;            // second grid dimension
@@ -121,28 +123,39 @@ bool chunked(const lq_sequence *sq, bool save) {
   return sq->tokens > 0 && sq->gate == LQ_GATE_GDN && (save || sq->tokens > kShort * sq->seqs);
 }
 
-// fp32 values of each array of lq::SeqSpace, per slot and value head
-constexpr int64_t kTile = lq::kChunk * lq::kChunk, kRowsU = lq::kChunk * kDim, kState = kDim * kDim;
-
-int64_t space_bytes(int64_t slots, int64_t heads, bool save) {
-  const int64_t per = 2 * kTile + 2 * lq::kChunk + kRowsU + kState + (save ? kRowsU + kState : 0);
-  return slots * heads * per * 4;
+// The arrays of lq::SeqSpace, one behind another from `base`; returns the
+// bytes they take (the sizes alone with base = nullptr).
+int64_t space(const lq_sequence *sq, int64_t slots, bool save, char *base, lq::SeqSpace *w) {
+  const int64_t hk = slots * sq->heads_k, hv = slots * sq->heads_v;
+  const int64_t parts = sq->dtype == LQ_F32 ? 3 : sq->dtype == LQ_F16 ? 2 : 1;
+  const int64_t square = lq::kChunk * lq::kChunk * 3 * 2, heads = lq::kChunk * kDim * parts * 2;
+  const int64_t rows = lq::kChunk * kDim * 4, state = kDim * kDim * 4;
+  int64_t used = 0;
+  const auto take = [&](auto **p, int64_t bytes) {
+    if (base) *p = reinterpret_cast<std::remove_reference_t<decltype(*p)>>(base + used);
+    used += bytes;
+  };
+  take(&w->T, hv * square);
+  take(&w->P, hv * square);
+  take(&w->K, hk * heads);
+  take(&w->Q, hk * heads);
+  take(&w->KT, hk * heads);
+  take(&w->dec, hv * 2 * lq::kChunk * 4);
+  if (save) {
+    take(&w->TT, hv * square);
+    take(&w->PT, hv * square);
+    take(&w->QT, hk * heads);
+    take(&w->U, hv * rows);
+    take(&w->S, hv * state);
+    take(&w->X, hv * rows);
+    take(&w->G, hv * state);
+  }
+  return used;
 }
 
-lq::SeqSpace space(void *ws, int64_t slots, int64_t heads, bool save) {
-  const int64_t n = slots * heads;
-  lq::SeqSpace s{};
-  float *p = static_cast<float *>(ws);
-  s.T = p;
-  s.P = s.T + n * kTile;
-  s.dec = s.P + n * kTile;
-  s.U = s.dec + n * 2 * lq::kChunk;
-  s.S = s.U + n * kRowsU;
-  if (save) {
-    s.X = s.S + n * kState;
-    s.G = s.X + n * kRowsU;
-  }
-  return s;
+int64_t space_bytes(const lq_sequence *sq, int64_t slots, bool save) {
+  lq::SeqSpace none{};
+  return space(sq, slots, save, nullptr, &none);
 }
 
 // What forward and backward check alike: cu_seqlens, q, k, beta, alpha and
@@ -165,13 +178,13 @@ int check_common(const lq_sequence *sq, const int32_t *cu, const lq_rows *q, con
   if ((rc = check_rows(alpha, T, sq->heads_v, kda ? kDim : 1, 4, false, &b, &a->alpha))) return rc;
   bl->add_in(b);
   const int64_t slots = slots_of(T, sq->seqs);
-  const int64_t need = chunked(sq, save) ? space_bytes(slots, sq->heads_v, save) : 0;
+  const int64_t need = chunked(sq, save) ? space_bytes(sq, slots, save) : 0;
   if (need) {
     if (!ws) return LQ_ERR_NULL;
     if (!aligned(ws, 16)) return LQ_ERR_ALIGN;
     if (ws_bytes < need) return LQ_ERR_SHAPE;
     bl->add_out(dense(ws, need));
-    a->w = space(ws, slots, sq->heads_v, save);
+    space(sq, slots, save, static_cast<char *>(ws), &a->w);
   }
   a->tokens = T;
   a->slots = slots;
@@ -237,11 +250,11 @@ int64_t leapquant_sequence_workspace(const lq_sequence *sq, int32_t save) {
   const int rc = check_sequence(sq);
   if (rc) return rc;
   if (sq->gate == LQ_GATE_KDA) return save ? LQ_ERR_UNSUPPORTED : 0;
-  if (save) return sq->tokens ? space_bytes(slots_of(sq->tokens, sq->seqs), sq->heads_v, true) : 0;
+  if (save) return sq->tokens ? space_bytes(sq, slots_of(sq->tokens, sq->seqs), true) : 0;
   // the most sequences with which that many tokens are taken in chunks
   const int64_t most = sq->tokens > 0 ? (sq->tokens - 1) / kShort : 0;
   if (most < 1) return 0;
-  return space_bytes(slots_of(sq->tokens, most < sq->seqs ? most : sq->seqs), sq->heads_v, false);
+  return space_bytes(sq, slots_of(sq->tokens, most < sq->seqs ? most : sq->seqs), false);
 }
 
 int leapquant_sequence_forward(const lq_sequence *sq, const int32_t *cu_seqlens, const lq_rows *q, const lq_rows *k,
