@@ -257,45 +257,79 @@ __global__ __launch_bounds__(512) void seq_rscan_kernel(const SeqArgs A) {
 }
 
 // ---------------------------------------------------------------------------
-// Gradients inside a chunk: one workgroup per (slot, key head), the value
-// heads that share it in turn, so that dQ and dK are summed over them in a
-// fixed order.  Wave w takes one token tile (16 rows).  Products are taken
-// transposed (the token is the accumulators' column), so a lane holds four
-// neighbouring values of one token's row.  U, S0 and G go through one LDS
-// buffer as bf16 parts, 24 KiB at a time; the wave's own rows of Q, K, dO, dX
-// and U come straight from global memory, a step ahead.  LDS and registers
-// are held to what lets two workgroups share a CU: one loads while the other
-// computes (with one, loads and products took turns: 350 us for the training
-// step of 8,192 tokens and 16 heads).
+// Gradients inside a chunk: one workgroup of eight waves per (slot, key head),
+// the value heads that share it in turn, so that dQ and dK are summed over
+// them in a fixed order.  A wave takes one token tile (16 rows) and half of
+// the other axis: of the 64 x 64 products every other column tile, of the 64 x
+// 128 ones 64 key columns.  Products are taken transposed (the token is the
+// accumulators' column), so a lane holds four neighbouring values of one
+// token's row.  U, then S0 and G 32 value columns at a time, go through LDS as
+// bf16 parts; every other operand is a fragment of the wave's own.
+// One workgroup a CU: with four waves and two workgroups the accumulators of
+// 128 key columns did not fit (68 registers in scratch, no faster).
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ Raw8<F32> raw_f32(const float *p) { return raw_load(reinterpret_cast<const F32 *>(p)); }
+// A tile of 16 rows of 128 values as the fragments of its four steps: lane (i,
+// g) holds values 32 x + 8 g .. + 7 of row i.  Rows are read whole, 256 bytes a
+// quarter wave, and turned in LDS that is the wave's own (no barrier); straight
+// into fragments a load would touch sixteen rows and take four times as long.
+// Rows at or past `len` repeat the first row.
+template <class E> struct Row4 { Raw8<E> x[4]; };
+constexpr int kTileBytes = 4 * LDC;  // a row in LDS: 256 bytes and padding
+template <class E>
+__device__ __forceinline__ void tile_load(Row4<E> &f, float *lds, const E *p, int64_t ts, int r0, int len, int lane) {
+  constexpr int kHalves = sizeof(E) / 2;  // 256 bytes of a row at a time
+  const int i = lane & 15, g = lane >> 4;
+  char *const d = reinterpret_cast<char *>(lds);
+  uint4 v[kHalves][4];
+#pragma unroll
+  for (int e = 0; e < kHalves; ++e)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int r = r0 + 4 * q + g;
+      v[e][q] = reinterpret_cast<const uint4 *>(p + (r < len ? r : 0) * ts)[16 * e + i];
+    }
+#pragma unroll
+  for (int e = 0; e < kHalves; ++e) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4 *>(d + (4 * q + g) * kTileBytes + 16 * i) = v[e][q];
+#pragma unroll
+    for (int x = 0; x < 4 / kHalves; ++x)
+#pragma unroll
+      for (int n = 0; n < kHalves; ++n)
+        f.x[e * (4 / kHalves) + x].v[n] =
+            *reinterpret_cast<const uint4 *>(d + i * kTileBytes + (32 * x + 8 * g) * (int)sizeof(E) + 16 * n);
+  }
+}
 
 template <class E, bool DELTA>
-__global__ __launch_bounds__(256, 2) void seq_grad_kernel(const SeqArgs A) {
+__global__ __launch_bounds__(512) void seq_grad_kernel(const SeqArgs A) {
   // parts of E1 and E2: what dQ and dK can hold of them
   constexpr int NP = Parts<E>::n, NE = NP == 3 ? 3 : 2;
   const int slot = blockIdx.x, hk = blockIdx.y;
-  const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const Chunk ch = find_chunk(A, slot, lane);
+  const Chunk ch = find_chunk(A, slot, threadIdx.x & 63);
   if (ch.len == 0) return;
-  __shared__ __align__(16) uint16_t sh_p[24 * 512];  // parts of U, S0 or G
+  // dO's rows on their way to fragments; parts of U, then of S0 and G; then the terms of dalpha
+  __shared__ __align__(16) uint16_t sh_p[48 * 512];
+  __shared__ __align__(16) float sh_u[C * LDD];  // U
+  __shared__ __align__(16) float sh_x[DELTA ? C * LDD : 4];  // dX
   // two triangles each: E1 with its diagonal below, E2 transposed above; L
   // with its diagonal below, dL transposed above
   __shared__ __align__(16) float sh_e[C * LDC];
   __shared__ __align__(16) float sh_l[C * LDC];
-  __shared__ __align__(16) float sh_a[C], sh_be[C], sh_gam[C], sh_kap[C];
-  __shared__ __align__(16) float sh_db[4][C];
-  __shared__ float sh_dgam[C], sh_kz[C], sh_gs[4], sh_f[4][C], sh_fa[4];
-  // the tile's row of 64 x 64 products is the longer the later it is: the
-  // two workgroups of a CU give a SIMD's waves opposite tiles
-  const int wt = (blockIdx.x & 1) ? 3 - w : w;
+  __shared__ __align__(16) float sh_a[C + 4], sh_be[C], sh_gam[C], sh_kap[C];
+  __shared__ __align__(16) float sh_db[4][C], sh_f[8][C];
+  __shared__ float sh_dgam[2][C], sh_kz[2][C], sh_gs[8], sh_fa[8];
+  // waves w and w + 4 share a SIMD: their token tiles together have the same
+  // share of the triangle
+  const int h = w >> 2, wt = h ? 7 - w : w;
   const floatx4 zero = {0.f, 0.f, 0.f, 0.f};
   const size_t atk = (size_t)slot * A.hk + hk;
+  const uint16_t *const Qf = A.w.Q + (atk * 4 + wt) * 4 * NP * 512, *const Kf = A.w.K + atk * 16 * NP * 512;
 
-  floatx4 dq[8], dk[8];  // key columns 16 n + 4 g + r of token `row`
+  floatx4 dq[4], dk[4];  // key columns 64 h + 16 n + 4 g + r of token `row`
 #pragma unroll
-  for (int n = 0; n < 8; ++n) dq[n] = dk[n] = zero;
+  for (int n = 0; n < 4; ++n) dq[n] = dk[n] = zero;
 
   for (int gr = 0; gr < A.group; ++gr) {
     // the lane is opaque in every round: else the addresses and conditions of
@@ -305,114 +339,161 @@ __global__ __launch_bounds__(256, 2) void seq_grad_kernel(const SeqArgs A) {
     const int lane = tid & 63, i = lane & 15, g = lane >> 4;
     const int row = 16 * wt + i;  // the lane's token
     const bool in = row < ch.len;
-    const int rowc = in ? row : 0;
-    const E *const pq = at<const E>(A.q, ch.t0 + rowc, hk), *const pk = at<const E>(A.k, ch.t0 + rowc, hk);
     const int hv = hk * A.group + gr;
     const size_t at_ = (size_t)slot * A.hv + hv;
     const float *U = A.w.U + at_ * C * D, *X = A.w.X + at_ * C * D;
     const float *S0 = A.w.S + at_ * D * D, *G = A.w.G + at_ * D * D;
-    const E *go = at<const E>(A.go, ch.t0 + rowc, hv);
     __syncthreads();
-    // operands of a step of the products below, loaded a step ahead
-    Raw8<E> nq, nk, no;
-    Raw8<F32> nx;
-    const auto load_step = [&](int x) {
-      nq = raw_load(pq + 8 * g + 32 * x);
-      no = raw_load(go + 8 * g + 32 * x);
-      if (DELTA) {
-        nk = raw_load(pk + 8 * g + 32 * x);
-        nx = raw_f32(X + row * D + 32 * x + 8 * g);
-      }
-    };
-    load_step(0);
+    Row4<E> fo;  // dO's rows of the wave's tile
+    float al = 1.f, be = 0.f, gm = 0.f, kp = 0.f;
     if (tid < C) {
-      const bool on = tid < ch.len;
-      sh_a[tid] = on ? *at<const float>(A.alpha, ch.t0 + tid, hv) : 1.f;
-      sh_be[tid] = on ? *at<const float>(A.beta, ch.t0 + tid, hv) : 0.f;
-      sh_gam[tid] = A.w.dec[at_ * 2 * C + tid];
-      sh_kap[tid] = A.w.dec[at_ * 2 * C + C + tid];
+      const int t = ch.t0 + (tid < ch.len ? tid : 0);
+      al = *at<const float>(A.alpha, t, hv);
+      be = *at<const float>(A.beta, t, hv);
+      gm = A.w.dec[at_ * 2 * C + tid];
+      kp = A.w.dec[at_ * 2 * C + C + tid];
     }
-    // U's parts, two steps at a time: wave w stores tile w
-    Raw8<F32> nu[2];
+    {
+      float4 u[4], x[4];
 #pragma unroll
-    for (int e = 0; e < 2; ++e) nu[e] = raw_f32(U + (16 * w + i) * D + 32 * e + 8 * g);
+      for (int e = 0; e < 4; ++e) {
+        u[e] = reinterpret_cast<const float4 *>(U)[tid + 512 * e];
+        if (DELTA) x[e] = reinterpret_cast<const float4 *>(X)[tid + 512 * e];
+      }
+      tile_load(fo, reinterpret_cast<float *>(sh_p) + w * 16 * LDC, at<const E>(A.go, ch.t0, hv), A.go.ts, 16 * wt,
+                ch.len, lane);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int o = (16 * e + (tid >> 5)) * LDD + 4 * (tid & 31);
+        *reinterpret_cast<float4 *>(sh_u + o) = u[e];
+        if (DELTA) *reinterpret_cast<float4 *>(sh_x + o) = x[e];
+      }
+    }
+    if (tid < C) {
+      sh_a[tid] = tid < ch.len ? al : 1.f;
+      sh_be[tid] = tid < ch.len ? be : 0.f;
+      sh_gam[tid] = gm;
+      sh_kap[tid] = kp;
+    }
     lds_barrier();
-    decay_matrix(sh_l, sh_a, w, lane);
-    // ---- the 64 x 64 products (rows j of the accumulators, column `row`), lower tiles only
-    floatx4 a1[4], a2[4], d1[4], d2[4];
+    // U's parts: wave w stores tile w >> 1, steps 2 (w & 1), + 1
 #pragma unroll
-    for (int n = 0; n < 4; ++n) a1[n] = a2[n] = d1[n] = d2[n] = zero;
-#pragma unroll 1
-    for (int x = 0; x < 4; ++x) {
-      if (!(x & 1)) {
-        if (x) lds_barrier();
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          bf8 f[3];
-          raw_parts<F32, 3>(f, nu[e]);
-          frag_store<3>(sh_p + (w * 2 + e) * 3 * 512, f, lane);
-          nu[e] = raw_f32(U + (16 * w + i) * D + 32 * (e + 2) + 8 * g);
-        }
-        lds_barrier();
+    for (int e = 0; e < 2; ++e) {
+      const int ut = w >> 1, x = 2 * (w & 1) + e;
+      bf8 f[3];
+      raw_parts<F32, 3>(f, raw_load(reinterpret_cast<const F32 *>(sh_u + (16 * ut + i) * LDD + 32 * x + 8 * g)));
+      frag_store<3>(sh_p + (ut * 4 + x) * 3 * 512, f, lane);
+    }
+    // L: column `lane`, rows 8 w .. + 7
+    {
+      float p = 1.f;
+      for (int l = 0; l < 8 * w; l += 4) {
+        const float4 a = *reinterpret_cast<const float4 *>(sh_a + l);
+        p *= l > lane ? a.x : 1.f;
+        p *= l + 1 > lane ? a.y : 1.f;
+        p *= l + 2 > lane ? a.z : 1.f;
+        p *= l + 3 > lane ? a.w : 1.f;
       }
-      bf8 fq[NP], fk[NP], fo[NP], fx[3];
-      raw_parts<E, NP>(fq, nq);
-      raw_parts<E, NP>(fo, no);
-      if (DELTA) {
-        raw_parts<E, NP>(fk, nk);
-        raw_parts<F32, 3>(fx, nx);
-      }
-      if (x < 3) load_step(x + 1);
 #pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        if (n <= wt) {
-          bf8 bk[NP], bu[3];
-          const int j = 16 * n + i;
-          parts_load<E, NP>(bk, at<const E>(A.k, ch.t0 + (j < ch.len ? j : 0), hk) + 32 * x + 8 * g);
-          frag_load<3>(bu, sh_p + (n * 2 + (x & 1)) * 3 * 512, lane);
-          mma_into<3, NP>(d1[n], bu, fo);
-          if (DELTA) mma_into<3, 3>(d2[n], bu, fx);
-          mma_into<NP, NP>(a1[n], bk, fq);
-          if (DELTA) mma_into<NP, NP>(a2[n], bk, fk);
-        }
+      for (int e = 0; e < 8; ++e) {
+        const int r = 8 * w + e;
+        p *= r > lane ? sh_a[r] : 1.f;
+        sh_l[r * LDC + lane] = r >= lane ? p : 0.f;
       }
     }
-    lds_barrier();  // L is whole, U's parts are read
-    // S0's first 32 value columns: thread (key row, 16 columns)
-    const int srow = tid >> 1, scol = 16 * (tid & 1);
-    Raw8<F32> ns[2];
-    const auto load_state = [&](const float *p, int x) {
+    // Q's and K's fragments for the products: all ahead where there is room
+    bf8 fq[4][NP], fk[4][NP], fb[4][2][NP];
+    const auto load_qk = [&](int x) {
+      frag_load<NP>(fq[x], Qf + x * NP * 512, lane);
+      if (DELTA) frag_load<NP>(fk[x], Kf + (wt * 4 + x) * NP * 512, lane);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) ns[e] = raw_f32(p + srow * D + 32 * x + scol + 8 * e);
+      for (int n = 0; n < 2; ++n)
+        if (2 * n + h <= wt) frag_load<NP>(fb[x][n], Kf + ((2 * n + h) * 4 + x) * NP * 512, lane);
     };
-    load_state(S0, 0);
-    no = raw_load(go + 8 * g);
-    if (DELTA) nx = raw_f32(X + row * D + 8 * g);
+    if (NP == 1) {
 #pragma unroll
-    for (int n = 0; n < 4; ++n) {
-      const int j0 = 16 * n + 4 * g;
+      for (int x = 0; x < 4; ++x) load_qk(x);
+    }
+    lds_barrier();  // L is whole, U's parts are stored
+    // ---- the 64 x 64 products (rows j of the accumulators, column `row`), lower tiles only
+    floatx4 a1[2], a2[2], d1[2], d2[2];
+#pragma unroll
+    for (int n = 0; n < 2; ++n) a1[n] = a2[n] = d1[n] = d2[n] = zero;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      bf8 po[NP], px[3];
+      if (NP > 1) load_qk(x);
+      raw_parts<E, NP>(po, fo.x[x]);
+      if (DELTA) raw_parts<F32, 3>(px, raw_load(reinterpret_cast<const F32 *>(sh_x + row * LDD + 32 * x + 8 * g)));
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        const int t = 2 * n + h;
+        if (t <= wt) {
+          bf8 bu[3];
+          frag_load<3>(bu, sh_p + (t * 4 + x) * 3 * 512, lane);
+          mma_into<3, NP>(d1[n], bu, po);
+          if (DELTA) mma_into<3, 3>(d2[n], bu, px);
+          mma_into<NP, NP>(a1[n], fb[x][n], fq[x]);
+          if (DELTA) mma_into<NP, NP>(a2[n], fb[x][n], fk[x]);
+        }
+      }
+      if (NP > 1) __builtin_amdgcn_sched_barrier(0);
+    }
+    // 32 value columns of S0 and G: eight threads a key row, four columns each
+    float4 xs[2], xg[2];
+    const auto load_states = [&](int x) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int o = (64 * e + (tid >> 3)) * D + 32 * x + 4 * (tid & 7);
+        xs[e] = *reinterpret_cast<const float4 *>(S0 + o);
+        xg[e] = *reinterpret_cast<const float4 *>(G + o);
+      }
+    };
+    float gs = 0.f;
+    const auto share_states = [&]() {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = 64 * e + (tid >> 3), c = tid & 7;
+        uint16_t *d = sh_p + (r >> 4) * 3 * 512 + ((r & 15) + 16 * (c >> 1)) * 8 + 4 * (c & 1);
+        uint32_t p0[3], p1[3];
+        split_pair<3>(xs[e].x, xs[e].y, p0);
+        split_pair<3>(xs[e].z, xs[e].w, p1);
+#pragma unroll
+        for (int n = 0; n < 3; ++n) *reinterpret_cast<uint2 *>(d + n * 512) = make_uint2(p0[n], p1[n]);
+        split_pair<3>(xg[e].x, xg[e].y, p0);
+        split_pair<3>(xg[e].z, xg[e].w, p1);
+#pragma unroll
+        for (int n = 0; n < 3; ++n) *reinterpret_cast<uint2 *>(d + (24 + n) * 512) = make_uint2(p0[n], p1[n]);
+        gs += (xs[e].x * xg[e].x + xs[e].y * xg[e].y) + (xs[e].z * xg[e].z + xs[e].w * xg[e].w);
+      }
+    };
+    load_states(0);
+    lds_barrier();  // U's parts are read
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      const int t = 2 * n + h, j0 = 16 * t + 4 * g;
       float db[4] = {0.f, 0.f, 0.f, 0.f};
-      if (n <= wt) {
+      if (t <= wt) {
         const float4 b4 = *reinterpret_cast<const float4 *>(sh_be + j0);
         const float4 l4 = *reinterpret_cast<const float4 *>(sh_l + row * LDC + j0);
-        const float be[4] = {b4.x, b4.y, b4.z, b4.w}, l[4] = {l4.x, l4.y, l4.z, l4.w};
+        const float be4[4] = {b4.x, b4.y, b4.z, b4.w}, l[4] = {l4.x, l4.y, l4.z, l4.w};
         float e1[4], e2[4], dl[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          // a token past the end took the first one's rows: nothing of it counts
+          // a token past the end took the first one's dO: nothing of it counts
           const float o = in ? d1[n][r] : 0.f, d = DELTA && in ? -d2[n][r] : 0.f;
-          e1[r] = l[r] * be[r] * o;
-          e2[r] = l[r] * be[r] * d;
+          e1[r] = l[r] * be4[r] * o;
+          e2[r] = l[r] * be4[r] * d;
           const float w1 = o * a1[n][r], wv = DELTA ? fmaf(d, a2[n][r], w1) : w1;
-          dl[r] = be[r] * wv;
+          dl[r] = be4[r] * wv;
           db[r] = l[r] * wv;
-          if (n == wt) {  // the diagonal: E1 alone; behind it: nothing
+          if (t == wt) {  // the diagonal: E1 alone; behind it: nothing
             const int j = j0 + r;
             db[r] = j < row ? db[r] : (j == row ? w1 : 0.f);
           }
           db[r] = row16_sum(db[r]);
         }
-        if (n < wt) {
+        if (t < wt) {
           *reinterpret_cast<float4 *>(sh_e + row * LDC + j0) = make_float4(e1[0], e1[1], e1[2], e1[3]);
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
@@ -431,115 +512,84 @@ __global__ __launch_bounds__(256, 2) void seq_grad_kernel(const SeqArgs A) {
       }
       if (i == 0) *reinterpret_cast<float4 *>(&sh_db[wt][j0]) = make_float4(db[0], db[1], db[2], db[3]);
     }
-    // ---- Z1, Z2 with S0, then Z3 with G, transposed: rows 16 n + 4 g + r are key columns
+    // ---- Z1, Z2 with S0, Z3 with G, transposed: rows 64 h + 16 n + 4 g + r are key columns
+    floatx4 z1[4], z2[4], z3[4];
+#pragma unroll
+    for (int n = 0; n < 4; ++n) z1[n] = z2[n] = z3[n] = zero;
+    // the products' last operands: K^T and Q^T of the first 32 tokens
+    bf8 bk[4][NP], bq[4][NP];
+    const auto load_kq = [&](int x) {
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        const size_t f = ((atk * 8 + 4 * h + n) * 2 + x) * NP * 512;
+        frag_load<NP>(bk[n], A.w.KT + f, lane);
+        frag_load<NP>(bq[n], A.w.QT + f, lane);
+      }
+    };
+    // Q's and K's rows, for the sums along them
+    float rq[4][4], rk[4][4];
+    const auto load_rows = [&]() {
+      const int tc = ch.t0 + (in ? row : 0);
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        load4(at<const E>(A.q, tc, hk) + 64 * h + 16 * n + 4 * g, rq[n]);
+        load4(at<const E>(A.k, tc, hk) + 64 * h + 16 * n + 4 * g, rk[n]);
+      }
+    };
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      if (x) lds_barrier();
+      share_states();
+      if (x < 3) load_states(x + 1);
+      if (NP == 1 && x == 2) load_rows();
+      if (NP == 1 && x == 3) load_kq(0);
+      lds_barrier();
+      bf8 po[NP], px[3], pu[3];
+      raw_parts<E, NP>(po, fo.x[x]);
+      if (DELTA) raw_parts<F32, 3>(px, raw_load(reinterpret_cast<const F32 *>(sh_x + row * LDD + 32 * x + 8 * g)));
+      raw_parts<F32, 3>(pu, raw_load(reinterpret_cast<const F32 *>(sh_u + row * LDD + 32 * x + 8 * g)));
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        bf8 bs[3], bg[3];
+        frag_load<3>(bs, sh_p + (4 * h + n) * 3 * 512, lane);
+        frag_load<3>(bg, sh_p + (8 + 4 * h + n) * 3 * 512, lane);
+        mma_into<3, NP>(z1[n], bs, po);
+        if (DELTA) mma_into<3, 3>(z2[n], bs, px);
+        mma_into<3, 3>(z3[n], bg, pu);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if (NP > 1) load_rows();
     const float gam = sh_gam[row], kap = sh_kap[row];
-    const int st = (srow >> 4) * 3 * 512, sl = (srow & 15) + 16 * 2 * (tid & 1);
     float dg = 0.f, kz = 0.f;
     {
-      floatx4 z1[8], z2[8];
 #pragma unroll
-      for (int n = 0; n < 8; ++n) z1[n] = z2[n] = zero;
-#pragma unroll 1
-      for (int x = 0; x < 4; ++x) {
-        if (x) lds_barrier();
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          bf8 f[3];
-          raw_parts<F32, 3>(f, ns[e]);
-          frag_store<3>(sh_p + st, f, sl + 16 * e);
-        }
-        if (x < 3) load_state(S0, x + 1); else load_state(G, 0);
-        lds_barrier();
-        bf8 fo[NP], fx[3];
-        raw_parts<E, NP>(fo, no);
-        if (DELTA) raw_parts<F32, 3>(fx, nx);
-        if (x < 3) {
-          no = raw_load(go + 8 * g + 32 * (x + 1));
-          if (DELTA) nx = raw_f32(X + row * D + 32 * (x + 1) + 8 * g);
-        }
-#pragma unroll
-        for (int n = 0; n < 8; ++n) {
-          bf8 bs[3];
-          frag_load<3>(bs, sh_p + n * 3 * 512, lane);
-          mma_into<3, NP>(z1[n], bs, fo);
-          if (DELTA) mma_into<3, 3>(z2[n], bs, fx);
-        }
-      }
-      nu[0] = raw_f32(U + row * D + 8 * g);
-#pragma unroll
-      for (int n = 0; n < 8; ++n) {
-        float q[4], k[4];
-        load4(pq + 16 * n + 4 * g, q);
-        load4(pk + 16 * n + 4 * g, k);
+      for (int n = 0; n < 4; ++n)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          dg = fmaf(q[r], z1[n][r], dg);
+          dg = fmaf(rq[n][r], z1[n][r], dg);
+          kz = fmaf(rk[n][r], z3[n][r], kz);
           dq[n][r] = fmaf(gam, z1[n][r], dq[n][r]);
+          dk[n][r] = fmaf(kap, z3[n][r], dk[n][r]);
           if (DELTA) {
-            dg = fmaf(-k[r], z2[n][r], dg);
+            dg = fmaf(-rk[n][r], z2[n][r], dg);
             dk[n][r] = fmaf(-gam, z2[n][r], dk[n][r]);
           }
         }
-      }
-    }
-    float gs = 0.f;
-    {
-      floatx4 z3[8];
-#pragma unroll
-      for (int n = 0; n < 8; ++n) z3[n] = zero;
-#pragma unroll 1
-      for (int x = 0; x < 4; ++x) {
-        lds_barrier();
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          // <G, S0>: S0's values come again, out of the cache
-          float xs[8], xg[8];
-          load8(reinterpret_cast<const F32 *>(S0 + srow * D + 32 * x + scol + 8 * e), xs);
-          const float4 u0 = __builtin_bit_cast(float4, ns[e].v[0]), u1 = __builtin_bit_cast(float4, ns[e].v[1]);
-          xg[0] = u0.x; xg[1] = u0.y; xg[2] = u0.z; xg[3] = u0.w;
-          xg[4] = u1.x; xg[5] = u1.y; xg[6] = u1.z; xg[7] = u1.w;
-#pragma unroll
-          for (int y = 0; y < 8; ++y) gs = fmaf(xs[y], xg[y], gs);
-          bf8 f[3];
-          split8<3>(xg, f);
-          frag_store<3>(sh_p + st, f, sl + 16 * e);
-        }
-        if (x < 3) load_state(G, x + 1);
-        lds_barrier();
-        bf8 fu[3];
-        raw_parts<F32, 3>(fu, nu[0]);
-        if (x < 3) nu[0] = raw_f32(U + row * D + 32 * (x + 1) + 8 * g);
-#pragma unroll
-        for (int n = 0; n < 8; ++n) {
-          bf8 bg[3];
-          frag_load<3>(bg, sh_p + n * 3 * 512, lane);
-          mma_into<3, 3>(z3[n], bg, fu);
-        }
-      }
-#pragma unroll
-      for (int n = 0; n < 8; ++n) {
-        float k[4];
-        load4(pk + 16 * n + 4 * g, k);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          kz = fmaf(k[r], z3[n][r], kz);
-          dk[n][r] = fmaf(kap, z3[n][r], dk[n][r]);
-        }
-      }
     }
     gs = wave_sum(gs);
-    if (lane == 0) sh_gs[w] = gs;
     dg += __shfl_xor(dg, 16);
     kz += __shfl_xor(kz, 16);
     dg += __shfl_xor(dg, 32);
     kz += __shfl_xor(kz, 32);
     if (g == 0) {
-      sh_dgam[row] = in ? dg : 0.f;
-      sh_kz[row] = in ? kz : 0.f;
+      sh_dgam[h][row] = in ? dg : 0.f;
+      sh_kz[h][row] = in ? kz : 0.f;
     }
+    if (lane == 0) sh_gs[w] = gs;
     lds_barrier();
     // ---- E1 K, E1^T Q, (E2 + E2^T) K
-#pragma unroll 1
+#pragma unroll
     for (int x = 0; x < 2; ++x) {
       const float *pr = sh_e + row * LDC + 32 * x + 8 * g;    // the token's row: E1 up to the diagonal, E2^T behind
       const float *pc = sh_e + (32 * x + 8 * g) * LDC + row;  // its column: E2^T above the diagonal, E1 from there
@@ -552,70 +602,82 @@ __global__ __launch_bounds__(256, 2) void seq_grad_kernel(const SeqArgs A) {
         vc[e] = j >= row ? b : 0.f;
         if (DELTA) v2[e] = j < row ? b : (j > row ? a : 0.f);
       }
+      if (NP > 1) load_kq(x);
       bf8 fr[NE], fc[NE], f2[NE];
       split8<NE>(vr, fr);
       split8<NE>(vc, fc);
       if (DELTA) split8<NE>(v2, f2);
 #pragma unroll
-      for (int n = 0; n < 8; ++n) {
-        const size_t f = ((atk * 8 + n) * 2 + x) * NP * 512;
-        bf8 bk[NP], bq[NP];
-        frag_load<NP>(bk, A.w.KT + f, lane);
-        frag_load<NP>(bq, A.w.QT + f, lane);
-        if (2 * x <= wt) mma_into<NP, NE, NE>(dq[n], bk, fr);
-        if (2 * x + 1 >= wt) mma_into<NP, NE, NE>(dk[n], bq, fc);
-        if (DELTA) mma_into<NP, NE, NE>(dk[n], bk, f2);
+      for (int n = 0; n < 4; ++n) {
+        mma_into<NP, NE, NE>(dq[n], bk[n], fr);
+        mma_into<NP, NE, NE>(dk[n], bq[n], fc);
+        if (DELTA) mma_into<NP, NE, NE>(dk[n], bk[n], f2);
       }
+      if (NP == 1 && x == 0) load_kq(1);
     }
     // ---- dalpha: lane 0 has the state's column, lane j that of token j - 1;
-    // wave w has tokens 16 w .. + 15, and what comes in from later ones is
-    // added through the product of the decays between
+    // wave w has tokens 8 w .. + 7, and what comes in from later ones is added
+    // through the product of the decays between
+    float *const sh_c = reinterpret_cast<float *>(sh_p);  // [64][LDC]
     {
-      const int j = lane - 1;
-      float f[16], run = 0.f, pa = 1.f;
+      const int j = lane ? lane - 1 : 0;
+      const float all = ((sh_gs[0] + sh_gs[1]) + (sh_gs[2] + sh_gs[3])) + ((sh_gs[4] + sh_gs[5]) + (sh_gs[6] + sh_gs[7]));
+      const float end = lane ? sh_be[j] * (sh_kz[0][j] + sh_kz[1][j]) : all;  // into the last token
+      float f[8], a[8], wg[8], run = 0.f, pa = 1.f;
 #pragma unroll
-      for (int e = 15; e >= 0; --e) {
-        const int t = 16 * w + e;
-        float dl;
-        if (lane == 0) {
-          dl = sh_dgam[t];
-          if (t == C - 1) dl += (sh_gs[0] + sh_gs[1]) + (sh_gs[2] + sh_gs[3]);
-        } else {
-          dl = t > j ? sh_l[j * LDC + t] : 0.f;
-          if (t == C - 1) dl = fmaf(sh_be[j], sh_kz[j], dl);
-        }
-        const float a = t < C - 1 ? sh_a[t + 1] : 0.f;  // from the token behind
-        run = fmaf(e < 15 ? a : 0.f, run, dl);
-        pa *= a;
+      for (int e = 0; e < 8; ++e) {
+        const int t = 8 * w + e;
+        const float s0 = sh_dgam[0][t] + sh_dgam[1][t], s1 = sh_l[j * LDC + t];
+        const float g0 = t > 0 ? sh_gam[t > 0 ? t - 1 : 0] : 1.f, l0 = sh_l[(t > 0 ? t - 1 : 0) * LDC + j];
+        f[e] = lane ? (t > j ? s1 : 0.f) : s0;
+        wg[e] = lane ? (t > j ? l0 : 0.f) : g0;
+        a[e] = t < C - 1 ? sh_a[t + 1] : 0.f;  // from the token behind
+      }
+      if (w == 7) f[7] += end;
+#pragma unroll
+      for (int e = 7; e >= 0; --e) {
+        run = fmaf(e < 7 ? a[e] : 0.f, run, f[e]);
         f[e] = run;
+        pa *= a[e];
       }
       sh_f[w][lane] = run;
       if (lane == 0) sh_fa[w] = pa;
       lds_barrier();
       float carry = 0.f;
-      for (int s = 3; s > w; --s) carry = fmaf(sh_fa[s], carry, sh_f[s][lane]);
+      for (int s = 7; s > w; --s) carry = fmaf(sh_fa[s], carry, sh_f[s][lane]);
 #pragma unroll
-      for (int e = 15; e >= 0; --e) {
-        const int t = 16 * w + e;
-        carry *= t < C - 1 ? sh_a[t + 1] : 0.f;
-        const float wg = lane == 0 ? (t > 0 ? sh_gam[t - 1] : 1.f) : (t > j ? sh_l[(t - 1) * LDC + j] : 0.f);
-        const float x = wave_sum((f[e] + carry) * wg);
-        if (lane == 0 && t < ch.len) *at<float>(A.dalpha, ch.t0 + t, hv) = x;
+      for (int e = 7; e >= 0; --e) {
+        carry *= a[e];
+        sh_c[(8 * w + e) * LDC + lane] = (f[e] + carry) * wg[e];
       }
-      if (w == 0 && lane < ch.len) {
-        float x = sh_l[(C - 1) * LDC + lane] * sh_kz[lane];
-        for (int t = lane >> 4; t < 4; ++t) x += sh_db[t][lane];
-        *at<float>(A.dbeta, ch.t0 + lane, hv) = x;
+    }
+    // a wave sums its own eight tokens' terms, eight lanes a token
+    {
+      const int t = 8 * w + (lane >> 3);
+      const float4 c0 = *reinterpret_cast<const float4 *>(sh_c + t * LDC + 8 * (lane & 7));
+      const float4 c1 = *reinterpret_cast<const float4 *>(sh_c + t * LDC + 8 * (lane & 7) + 4);
+      float x = ((c0.x + c0.y) + (c0.z + c0.w)) + ((c1.x + c1.y) + (c1.z + c1.w));
+      x += dpp<0xB1>(x);
+      x += dpp<0x4E>(x);
+      x += dpp<0x141>(x);
+      const float kzt = sh_kz[0][t] + sh_kz[1][t];
+      float y = sh_l[(C - 1) * LDC + t] * kzt;
+      const int first = t >> 4;  // tiles before the token's have no terms
+#pragma unroll
+      for (int n = 0; n < 4; ++n) y += n >= first ? sh_db[n][t] : 0.f;
+      if ((lane & 7) == 0 && t < ch.len) {
+        *at<float>(A.dalpha, ch.t0 + t, hv) = x;
+        *at<float>(A.dbeta, ch.t0 + t, hv) = y;
       }
     }
   }
-  const int row = 16 * wt + (lane & 15), g = lane >> 4;
+  const int row = 16 * wt + (threadIdx.x & 15), g = (threadIdx.x & 63) >> 4;
   if (row < ch.len) {
-    E *oq = at<E>(A.dq, ch.t0 + row, hk) + 4 * g, *ok = at<E>(A.dk, ch.t0 + row, hk) + 4 * g;
+    E *pq = at<E>(A.dq, ch.t0 + row, hk) + 64 * h + 4 * g, *pk = at<E>(A.dk, ch.t0 + row, hk) + 64 * h + 4 * g;
 #pragma unroll
-    for (int n = 0; n < 8; ++n) {
-      store4(oq + 16 * n, dq[n]);
-      store4(ok + 16 * n, dk[n]);
+    for (int n = 0; n < 4; ++n) {
+      store4(pq + 16 * n, dq[n]);
+      store4(pk + 16 * n, dk[n]);
     }
   }
 }
@@ -630,7 +692,7 @@ hipError_t backward(const SeqArgs &a, hipStream_t stream) {
     hipLaunchKernelGGL((seq_rscan_kernel<E, DELTA, 32>), dim3((unsigned)(units * 4)), dim3(512), 0, stream, a);
   else
     hipLaunchKernelGGL((seq_rscan_kernel<E, DELTA, 16>), dim3((unsigned)(units * 8)), dim3(512), 0, stream, a);
-  hipLaunchKernelGGL((seq_grad_kernel<E, DELTA>), dim3((unsigned)a.slots, a.hk), dim3(256), 0, stream, a);
+  hipLaunchKernelGGL((seq_grad_kernel<E, DELTA>), dim3((unsigned)a.slots, a.hk), dim3(512), 0, stream, a);
   return hipGetLastError();
 }
 template <class E>
