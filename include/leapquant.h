@@ -456,8 +456,8 @@ typedef struct lq_head_norm {
   int32_t interleaved; /* 0: pairs (c, c + rot / 2); 1: pairs (2c, 2c + 1)     */
   float eps;           /* > 0                                                  */
   float q_scale;
-  const float *q_weight;    /* [128] or NULL                                   */
-  const float *k_weight;    /* [128] or NULL                                   */
+  const float *q_weight;    /* [128], 16-byte aligned, or NULL                 */
+  const float *k_weight;    /* [128], 16-byte aligned, or NULL                 */
   const int64_t *positions; /* [tokens]; NULL only with rot = 0                */
   const double *inv_freq;   /* [rot / 2] radians per position; NULL likewise   */
 } lq_head_norm;

@@ -79,85 +79,119 @@ __device__ __forceinline__ void norm_rotate(const NormArgs &A, float (&x)[8], co
   for (int e = 0; e < 8; ++e) x[e] = fmaf(sign * s[e], p[e], c[e] * x[e]);
 }
 
+// The weight's eight values of a lane (queries or keys)
+__device__ __forceinline__ void norm_weights(const float *w, int first, float (&x)[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] = 1.f;
+  if (w) load8(reinterpret_cast<const F32 *>(w + first), x);
+}
+
 template <class EI, class EO>
 __global__ __launch_bounds__(256) void norm_kernel(const NormArgs A) {
   __shared__ float2 sh_turn[4][64];
   const int w = threadIdx.x >> 6, lane = threadIdx.x & 63, first = (lane & 15) * 8;
   const NormWork n = norm_work(A, (int64_t)blockIdx.x * 4 + w);
   const bool on = n.t < A.tokens;
-  float c[8], s[8];
+  if (!on) return;  // whole waves; the waves share nothing
+  // every load first: the run's heads, four a quarter wave (past the run's end: its last head again)
+  Raw8<EI> raw[kNormHeads / 4];
+#pragma unroll
+  for (int k = 0; k < kNormHeads / 4; ++k) {
+    int h = n.h0 + (lane >> 4) + 4 * k;
+    h = h < n.h1 ? h : n.h1 - 1;
+    const bool isq = h < A.hq;
+    raw[k] = raw_load(at<const EI>(isq ? A.q : A.k, n.t, isq ? h : h - A.hq) + first);
+  }
+  float wq[8], wk[8], c[8], s[8];
+  norm_weights(A.wq, first, wq);
+  norm_weights(A.wk, first, wk);
   if (A.rot) {
-    if (on) sh_turn[w][lane] = norm_turn(A, n.t, lane);
-    __syncthreads();
+    sh_turn[w][lane] = norm_turn(A, n.t, lane);
+    __builtin_amdgcn_wave_barrier();  // a wave's LDS accesses stay in order
     norm_pairs(A, sh_turn[w], first, c, s);
   }
-  if (!on) return;
-  for (int h = n.h0 + (lane >> 4); h < n.h1; h += 4) {
+#pragma unroll
+  for (int k = 0; k < kNormHeads / 4; ++k) {
+    const int h = n.h0 + (lane >> 4) + 4 * k;
+    if (n.h0 + 4 * k >= n.h1) break;
     const bool isq = h < A.hq;
-    const int hh = isq ? h : h - A.hq;
     float x[8], ss = 0.f;
-    load8(at<const EI>(isq ? A.q : A.k, n.t, hh) + first, x);
+    raw_floats(x, raw[k]);
 #pragma unroll
     for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
     ss = row16_sum(ss);
     const float r = 1.f / sqrtf(ss * (A.rms ? 1.f / D : 1.f) + A.eps) * (isq ? A.q_scale : 1.f);
-    const float *wt = isq ? A.wq : A.wk;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] *= r * (wt ? wt[first + e] : 1.f);
+    for (int e = 0; e < 8; ++e) x[e] *= r * (isq ? wq[e] : wk[e]);
     norm_rotate(A, x, c, s, 1.f, lane);
-    store8(at<EO>(isq ? A.yq : A.yk, n.t, hh) + first, x);
+    if (h < n.h1) store8(at<EO>(isq ? A.yq : A.yk, n.t, isq ? h : h - A.hq) + first, x);
   }
 }
 
 // Backward.  Weight gradients: a lane sums its eight values over the wave's
 // tokens and heads, the workgroup's waves meet in LDS, and the workgroups'
 // sums in `part` are added by a second launch, all in a fixed order.
+constexpr int kNormBackWaves = 8, kNormBackBlocks = 512;
+
 template <class EI, class EO>
-__global__ __launch_bounds__(256) void norm_backward_kernel(const NormArgs A) {
-  __shared__ float2 sh_turn[4][64];
-  __shared__ float sh_dw[4][2][D];
+__global__ __launch_bounds__(64 * kNormBackWaves, 4) void norm_backward_kernel(const NormArgs A) {
+  __shared__ float2 sh_turn[kNormBackWaves][64];
+  __shared__ float sh_dw[kNormBackWaves][2][D];
   const int w = threadIdx.x >> 6, lane = threadIdx.x & 63, first = (lane & 15) * 8;
   const int heads = A.hq + A.hk, runs = (heads + kNormHeads - 1) / kNormHeads;
-  const int64_t waves = A.tokens * runs, step = (int64_t)gridDim.x * 4;
-  float dw[2][8];
+  const int64_t waves = A.tokens * runs, step = (int64_t)gridDim.x * kNormBackWaves;
+  float dw[2][8], wq[8], wk[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) dw[0][e] = dw[1][e] = 0.f;
-  const int64_t rounds = (waves + step - 1) / step;
-  for (int64_t k = 0; k < rounds; ++k) {
-    const NormWork n = norm_work(A, k * step + (int64_t)blockIdx.x * 4 + w);
-    const bool on = n.t < A.tokens;
+  norm_weights(A.wq, first, wq);
+  norm_weights(A.wk, first, wk);
+  for (int64_t wave = (int64_t)blockIdx.x * kNormBackWaves + w; wave < waves; wave += step) {
+    const NormWork n = norm_work(A, wave);
     float c[8], s[8];
     if (A.rot) {
-      __syncthreads();
-      if (on) sh_turn[w][lane] = norm_turn(A, n.t, lane);
-      __syncthreads();
+      __builtin_amdgcn_wave_barrier();
+      sh_turn[w][lane] = norm_turn(A, n.t, lane);
+      __builtin_amdgcn_wave_barrier();
       norm_pairs(A, sh_turn[w], first, c, s);
     }
-    if (!on) continue;
-    for (int h = n.h0 + (lane >> 4); h < n.h1; h += 4) {
-      const bool isq = h < A.hq;
-      const int hh = isq ? h : h - A.hq;
-      float x[8], gy[8], ss = 0.f, xg = 0.f;
-      load8(at<const EI>(isq ? A.q : A.k, n.t, hh) + first, x);
-      load8(at<const EO>(isq ? A.yq : A.yk, n.t, hh) + first, gy);
-      norm_rotate(A, gy, c, s, -1.f, lane);
+#pragma unroll 1
+    for (int k0 = 0; k0 < kNormHeads / 4; k0 += 2) {  // two heads a quarter wave in flight
+      if (n.h0 + 4 * k0 >= n.h1) break;
+      Raw8<EI> rx[2];
+      Raw8<EO> rg[2];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-      ss = row16_sum(ss);
-      const float r = 1.f / sqrtf(ss * (A.rms ? 1.f / D : 1.f) + A.eps), sc = isq ? A.q_scale : 1.f;
-      const float *wt = isq ? A.wq : A.wk;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float ge = sc * gy[e], t = ge * x[e] * r;
-        dw[0][e] += isq ? t : 0.f;
-        dw[1][e] += isq ? 0.f : t;
-        gy[e] = ge * (wt ? wt[first + e] : 1.f);
-        xg = fmaf(x[e], gy[e], xg);
+      for (int k = 0; k < 2; ++k) {
+        int h = n.h0 + (lane >> 4) + 4 * (k0 + k);
+        h = h < n.h1 ? h : n.h1 - 1;
+        const bool isq = h < A.hq;
+        rx[k] = raw_load(at<const EI>(isq ? A.q : A.k, n.t, isq ? h : h - A.hq) + first);
+        rg[k] = raw_load(at<const EO>(isq ? A.yq : A.yk, n.t, isq ? h : h - A.hq) + first);
       }
-      xg = row16_sum(xg) * (A.rms ? 1.f / D : 1.f) * r * r;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = r * (gy[e] - x[e] * xg);
-      store8(at<EI>(isq ? A.dq : A.dk, n.t, hh) + first, x);
+      for (int k = 0; k < 2; ++k) {
+        const int h = n.h0 + (lane >> 4) + 4 * (k0 + k);
+        const bool isq = h < A.hq, mine = h < n.h1;
+        float x[8], gy[8], ss = 0.f, xg = 0.f;
+        raw_floats(x, rx[k]);
+        raw_floats(gy, rg[k]);
+        norm_rotate(A, gy, c, s, -1.f, lane);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+        ss = row16_sum(ss);
+        const float r = 1.f / sqrtf(ss * (A.rms ? 1.f / D : 1.f) + A.eps), sc = isq ? A.q_scale : 1.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float ge = sc * gy[e], t = mine ? ge * x[e] * r : 0.f;
+          dw[0][e] += isq ? t : 0.f;
+          dw[1][e] += isq ? 0.f : t;
+          gy[e] = ge * (isq ? wq[e] : wk[e]);
+          xg = fmaf(x[e], gy[e], xg);
+        }
+        xg = row16_sum(xg) * (A.rms ? 1.f / D : 1.f) * r * r;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = r * (gy[e] - x[e] * xg);
+        if (mine) store8(at<EI>(isq ? A.dq : A.dk, n.t, isq ? h : h - A.hq) + first, x);
+      }
     }
   }
   if (!A.dwq && !A.dwk) return;
@@ -171,31 +205,42 @@ __global__ __launch_bounds__(256) void norm_backward_kernel(const NormArgs A) {
       if (lane < 16) sh_dw[w][p][first + e] = x;
     }
   __syncthreads();
-  const int p = threadIdx.x >> 7, d = threadIdx.x & 127;
-  A.part[(int64_t)blockIdx.x * 2 * D + threadIdx.x] = (sh_dw[0][p][d] + sh_dw[1][p][d]) + (sh_dw[2][p][d] + sh_dw[3][p][d]);
+  if (threadIdx.x < 2 * D) {
+    const int p = threadIdx.x >> 7, d = threadIdx.x & 127;
+    float x = 0.f;
+#pragma unroll
+    for (int v = 0; v < kNormBackWaves; ++v) x += sh_dw[v][p][d];
+    A.part[(int64_t)blockIdx.x * 2 * D + threadIdx.x] = x;
+  }
 }
 
-// dw: workgroup (queries or keys), thread (value d, eighth of the partial sums)
+// dw: workgroup (queries or keys, 32 values), thread (value, one of 32 shares
+// of the partial sums)
 __global__ __launch_bounds__(1024) void norm_weight_kernel(const NormArgs A, int blocks) {
-  __shared__ float sh[8][D];
-  const int p = blockIdx.x, d = threadIdx.x & (D - 1), e = threadIdx.x >> 7;
+  __shared__ float sh[32][33];
+  const int p = blockIdx.x >> 2, d = (blockIdx.x & 3) * 32 + (threadIdx.x & 31), e = threadIdx.x >> 5;
   float x = 0.f;
-  for (int b = e; b < blocks; b += 8) x += A.part[((int64_t)b * 2 + p) * D + d];
-  sh[e][d] = x;
+#pragma unroll 8
+  for (int b = e; b < blocks; b += 32) x += A.part[((int64_t)b * 2 + p) * D + d];
+  sh[e][threadIdx.x & 31] = x;
   __syncthreads();
   float *out = p ? A.dwk : A.dwq;
-  if (e == 0 && out)
-    out[d] = ((sh[0][d] + sh[1][d]) + (sh[2][d] + sh[3][d])) + ((sh[4][d] + sh[5][d]) + (sh[6][d] + sh[7][d]));
+  if (e == 0 && out) {
+    float y = 0.f;
+#pragma unroll
+    for (int v = 0; v < 32; ++v) y += sh[v][threadIdx.x];
+    out[d] = y;
+  }
 }
 
 static int64_t norm_waves(int64_t tokens, int hq, int hk) {
   return tokens * ((hq + hk + kNormHeads - 1) / kNormHeads);
 }
 // The backward pass holds its partial weight gradients in registers, so its
-// workgroups stay and take waves in turn; 1,024 of them fill the chip.
+// workgroups stay and take waves in turn; 512 of eight waves fill the chip.
 int64_t norm_blocks(int64_t tokens, int hq, int hk) {
-  const int64_t b = (norm_waves(tokens, hq, hk) + 3) / 4;
-  return b < 1024 ? b : 1024;
+  const int64_t b = (norm_waves(tokens, hq, hk) + kNormBackWaves - 1) / kNormBackWaves;
+  return b < kNormBackBlocks ? b : kNormBackBlocks;
 }
 
 template <class EI, class EO>
@@ -206,8 +251,8 @@ hipError_t norm_run(const NormArgs &a, bool back, hipStream_t stream) {
     return hipGetLastError();
   }
   const int64_t b = norm_blocks(a.tokens, a.hq, a.hk);
-  if (b) hipLaunchKernelGGL((norm_backward_kernel<EI, EO>), dim3((unsigned)b), dim3(256), 0, stream, a);
-  if (a.dwq || a.dwk) hipLaunchKernelGGL(norm_weight_kernel, dim3(2), dim3(1024), 0, stream, a, (int)b);
+  if (b) hipLaunchKernelGGL((norm_backward_kernel<EI, EO>), dim3((unsigned)b), dim3(64 * kNormBackWaves), 0, stream, a);
+  if (a.dwq || a.dwk) hipLaunchKernelGGL(norm_weight_kernel, dim3(8), dim3(1024), 0, stream, a, (int)b);
   return hipGetLastError();
 }
 template <class EI>

@@ -22,7 +22,9 @@ struct Rows {
 // sequences without a pass that counts them.  The matrices are kept as
 // operands of the scans: bf16 parts in fragments of 16 rows x 32 contraction
 // indexes (64 lanes x 16 bytes a part; n parts: 1 of bf16 inputs, 2 of fp16,
-// 3 of fp32 ones).  P has 3 parts of room.
+// 3 of fp32 ones).  With a decay for every channel K, Q and K^T hold decays:
+// they are kept per value head, in 3 parts, and dec is the chunk's decay of
+// every key row.
 struct SeqSpace {
   uint16_t *T, *P;        // [slots][hv][4][2][3]  (I + M)^-1; decayed, beta-weighted q k^T
   uint16_t *K, *Q;        // [slots][hk][4][4][n]
@@ -73,7 +75,7 @@ inline bool scan_wide(const SeqArgs &a) { return (int64_t)a.seqs * a.hv * 4 >= 2
 
 // dtype: 0 fp32, 1 bf16, 2 fp16
 hipError_t launch_seq_recurrent(const SeqArgs &a, int dtype, bool kda, bool delta, hipStream_t stream);
-hipError_t launch_seq_chunked(const SeqArgs &a, int dtype, bool delta, hipStream_t stream);
+hipError_t launch_seq_chunked(const SeqArgs &a, int dtype, bool kda, bool delta, hipStream_t stream);
 hipError_t launch_seq_backward(const SeqArgs &a, int dtype, bool delta, hipStream_t stream);
 int64_t norm_blocks(int64_t tokens, int hq, int hk);  // workgroups of the backward pass
 hipError_t launch_norm(const NormArgs &a, int in, int out, hipStream_t stream);

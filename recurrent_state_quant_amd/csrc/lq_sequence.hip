@@ -128,10 +128,90 @@ __global__ __launch_bounds__(256) void seq_recurrent_kernel(const SeqArgs A) {
 }
 
 // ---------------------------------------------------------------------------
+// T = (I + M)^-1 for the unit lower triangle I + M (M fp32 [64][LDC], below the
+// diagonal; its blocks above are used on the way), by blocks of 16: each
+// diagonal block by forward substitution (a column per lane), then 16 -> 32 ->
+// 64 by T_ba = -T_b (M_ba T_a) on the fp32 matrix path.  Four waves; ends with
+// a barrier.  T's blocks above the diagonal are not written.
+__device__ __forceinline__ void invert_unit_lower(float *sh_t, float *sh_m, int w, int lane) {
+  const int i = lane & 15, g = lane >> 4;
+  const floatx4 zero = {0.f, 0.f, 0.f, 0.f};
+  {
+    // diagonal block w, column i (the four groups of lanes do the same)
+    const int d0 = 16 * w;
+    float t[16];
+#pragma unroll
+    for (int a = 0; a < 16; ++a) {
+      float x = a == i ? 1.f : 0.f;
+#pragma unroll
+      for (int l = 0; l < a; ++l) x = fmaf(-sh_m[(d0 + a) * LDC + d0 + l], t[l], x);
+      t[a] = x;
+    }
+    // group g stores rows 4 g .. + 3
+#pragma unroll
+    for (int a = 0; a < 16; ++a)
+      if ((a >> 2) == g) sh_t[(d0 + a) * LDC + d0 + i] = t[a];
+  }
+  __syncthreads();
+  if (w < 2) {
+    const int b = 2 * w, a = b + 1;
+    floatx4 y = zero, z = zero;
+    mma(y, frag<false>(sh_m + 16 * b, LDC, 16 * a, 0, lane), frag<true>(sh_t + 16 * b * LDC, LDC, 16 * b, 0, lane));
+    // the product, transposed, to block (b, a) of sh_m
+    *reinterpret_cast<float4 *>(sh_m + (16 * b + i) * LDC + 16 * a + 4 * g) = make_float4(y[0], y[1], y[2], y[3]);
+    mma(z, frag<false>(sh_t + 16 * a, LDC, 16 * a, 0, lane), frag<false>(sh_m + 16 * a, LDC, 16 * b, 0, lane));
+#pragma unroll
+    for (int r = 0; r < 4; ++r) sh_t[(16 * a + 4 * g + r) * LDC + 16 * b + i] = -z[r];
+  }
+  __syncthreads();
+  const int a = 2 + (w >> 1), b = w & 1;
+  {
+    floatx4 y = zero;
+    for (int c = b; c < 2; ++c)
+      mma(y, frag<false>(sh_m + 16 * c, LDC, 16 * a, 0, lane), frag<true>(sh_t + 16 * c * LDC, LDC, 16 * b, 0, lane));
+    *reinterpret_cast<float4 *>(sh_m + (16 * b + i) * LDC + 16 * a + 4 * g) = make_float4(y[0], y[1], y[2], y[3]);
+  }
+  __syncthreads();
+  {
+    floatx4 z = zero;
+    for (int c = 2; c <= a; ++c)
+      mma(z, frag<false>(sh_t + 16 * c, LDC, 16 * a, 0, lane), frag<false>(sh_m + 16 * c, LDC, 16 * b, 0, lane));
+#pragma unroll
+    for (int r = 0; r < 4; ++r) sh_t[(16 * a + 4 * g + r) * LDC + 16 * b + i] = -z[r];
+  }
+  __syncthreads();
+}
+
+// T and P as the scan's fragments: rows 16 w + i, columns 32 x + 8 g .. + 7;
+// T's block above the diagonal in a step is not written in sh_t: zeros.
+template <bool DELTA>
+__device__ __forceinline__ void store_triangles(const SeqArgs &A, size_t at_, const float *sh_t, const float *sh_p, int w,
+                                                int lane) {
+  const int i = lane & 15, g = lane >> 4;
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    if (2 * x > w) continue;
+    const int row = 16 * w + i, col = 32 * x + 8 * g;
+    float v[8];
+    bf8 f[3];
+    if (DELTA) {
+      const bool in = (col >> 4) <= w;
+      load8(reinterpret_cast<const F32 *>(sh_t + row * LDC + col), v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = in && col + e <= row ? v[e] : 0.f;
+      split8<3>(v, f);
+      frag_store<3>(A.w.T + ((at_ * 4 + w) * 2 + x) * 3 * 512, f, lane);
+    }
+    load8(reinterpret_cast<const F32 *>(sh_p + row * LDC + col), v);
+    split8<3>(v, f);
+    frag_store<3>(A.w.P + ((at_ * 4 + w) * 2 + x) * 3 * 512, f, lane);
+  }
+}
+
+// ---------------------------------------------------------------------------
 // Prep: one workgroup per (slot, value head).  Writes, in the order in which
 // the scans load them (matrix fragments, bf16 parts): T, P, and, for the first
-// value head of a key head, K^T (and K and Q where they are not their own only
-// part); with SAVE also the transposes of T, P and Q for the backward scan.  M and T are fp32; T by blocks of 16: each diagonal block by forward
+// value head of a key head, K, Q and K^T; with SAVE also the transposes of T, P and Q for the backward scan.  M and T are fp32; T by blocks of 16: each diagonal block by forward
 // substitution (a column per lane), then 16 -> 32 -> 64 by T_ba = -T_b (M_ba
 // T_a) on the fp32 matrix path.
 // ---------------------------------------------------------------------------
@@ -238,79 +318,9 @@ __global__ __launch_bounds__(256) void seq_prep_kernel(const SeqArgs A) {
       if (DELTA && n <= w) sh_m[row * LDC + j] = j < row ? lb * kk[r] : 0.f;
     }
   }
-  if (DELTA) {
-    __syncthreads();
-    {
-      // diagonal block w, column i (the four groups of lanes do the same)
-      const int d0 = 16 * w;
-      float t[16];
-#pragma unroll
-      for (int a = 0; a < 16; ++a) {
-        float x = a == i ? 1.f : 0.f;
-#pragma unroll
-        for (int l = 0; l < a; ++l) x = fmaf(-sh_m[(d0 + a) * LDC + d0 + l], t[l], x);
-        t[a] = x;
-      }
-      // group g stores rows 4 g .. + 3
-#pragma unroll
-      for (int a = 0; a < 16; ++a)
-        if ((a >> 2) == g) sh_t[(d0 + a) * LDC + d0 + i] = t[a];
-    }
-    __syncthreads();
-    const floatx4 zero = {0.f, 0.f, 0.f, 0.f};
-    if (w < 2) {
-      const int b = 2 * w, a = b + 1;
-      floatx4 y = zero, z = zero;
-      mma(y, frag<false>(sh_m + 16 * b, LDC, 16 * a, 0, lane), frag<true>(sh_t + 16 * b * LDC, LDC, 16 * b, 0, lane));
-      // the product, transposed, to block (b, a) of sh_m
-      *reinterpret_cast<float4 *>(sh_m + (16 * b + i) * LDC + 16 * a + 4 * g) = make_float4(y[0], y[1], y[2], y[3]);
-      mma(z, frag<false>(sh_t + 16 * a, LDC, 16 * a, 0, lane), frag<false>(sh_m + 16 * a, LDC, 16 * b, 0, lane));
-#pragma unroll
-      for (int r = 0; r < 4; ++r) sh_t[(16 * a + 4 * g + r) * LDC + 16 * b + i] = -z[r];
-    }
-    __syncthreads();
-    const int a = 2 + (w >> 1), b = w & 1;
-    {
-      floatx4 y = zero;
-      for (int c = b; c < 2; ++c)
-        mma(y, frag<false>(sh_m + 16 * c, LDC, 16 * a, 0, lane), frag<true>(sh_t + 16 * c * LDC, LDC, 16 * b, 0, lane));
-      *reinterpret_cast<float4 *>(sh_m + (16 * b + i) * LDC + 16 * a + 4 * g) = make_float4(y[0], y[1], y[2], y[3]);
-    }
-    __syncthreads();
-    {
-      floatx4 z = zero;
-      for (int c = 2; c <= a; ++c)
-        mma(z, frag<false>(sh_t + 16 * c, LDC, 16 * a, 0, lane), frag<false>(sh_m + 16 * c, LDC, 16 * b, 0, lane));
-#pragma unroll
-      for (int r = 0; r < 4; ++r) sh_t[(16 * a + 4 * g + r) * LDC + 16 * b + i] = -z[r];
-    }
-  }
   __syncthreads();
-  // rows 16 w + i, columns 32 x + 8 g .. + 7 of T and P; T's block above the
-  // diagonal in a step is not written there: zeros
-#pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    if (2 * x > w) continue;
-    const int row = 16 * w + i, col = 32 * x + 8 * g;
-    float v[8];
-    bf8 f[3];
-    if (DELTA) {
-      const bool in = (col >> 4) <= w;
-      const float4 *s = reinterpret_cast<const float4 *>(sh_t + row * LDC + col);
-      const float4 u0 = in ? s[0] : make_float4(0.f, 0.f, 0.f, 0.f), u1 = in ? s[1] : make_float4(0.f, 0.f, 0.f, 0.f);
-      v[0] = u0.x; v[1] = u0.y; v[2] = u0.z; v[3] = u0.w;
-      v[4] = u1.x; v[5] = u1.y; v[6] = u1.z; v[7] = u1.w;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = col + e <= row ? v[e] : 0.f;
-      split8<3>(v, f);
-      frag_store<3>(A.w.T + ((at_ * 4 + w) * 2 + x) * 3 * 512, f, lane);
-    }
-    const float4 *s = reinterpret_cast<const float4 *>(sh_l + row * LDC + col);
-    v[0] = s[0].x; v[1] = s[0].y; v[2] = s[0].z; v[3] = s[0].w;
-    v[4] = s[1].x; v[5] = s[1].y; v[6] = s[1].z; v[7] = s[1].w;
-    split8<3>(v, f);
-    frag_store<3>(A.w.P + ((at_ * 4 + w) * 2 + x) * 3 * 512, f, lane);
-  }
+  if (DELTA) invert_unit_lower(sh_t, sh_m, w, lane);
+  store_triangles<DELTA>(A, at_, sh_t, sh_l, w, lane);
   if (!SAVE) return;
   // transposes for the backward scan: columns 16 w + i, rows 32 x + 8 g .. + 7
 #pragma unroll
@@ -349,6 +359,209 @@ __global__ __launch_bounds__(256) void seq_prep_kernel(const SeqArgs A) {
 }
 
 // ---------------------------------------------------------------------------
+// Prep with a decay for every key channel c: the decays do not factor out of
+// the products along c,
+//   M_ij = beta_j sum_c k_ic k_jc alpha_{j+1,c} .. alpha_{i,c},
+// so K, Q and K^T are written with their decays, per value head, in three
+// parts.  A quotient of prefix products would overflow; instead, by blocks of
+// 16 tokens: with a_i the decays from block I's start to token i, b_j those
+// from token j to the end of block J, m those of the blocks between,
+//   M_ij = beta_j sum_c (k a)_ic (m (k b))_jc
+// are matrix products of factors that are all at most 1 (for alpha <= 1), and
+// inside a block the sums are taken directly, the decay running from token to
+// token (a lane has a token and 32 channels).  Decays of zero are exact.
+// The direct sums are about half of the kernel's time.
+// ---------------------------------------------------------------------------
+template <class E, bool DELTA>
+__global__ __launch_bounds__(256) void seq_prep_kda_kernel(const SeqArgs A) {
+  const int slot = blockIdx.x, hv = blockIdx.y, hk = hv / A.group;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const Chunk ch = find_chunk(A, slot, lane);
+  if (ch.len == 0) return;
+  const size_t at_ = (size_t)slot * A.hv + hv;
+  __shared__ __align__(16) float sh_k[C * LDD];  // k, then k a; then T
+  __shared__ __align__(16) float sh_q[C * LDD];  // q, then q a
+  __shared__ __align__(16) float sh_a[C * LDD];  // alpha, then k b
+  __shared__ __align__(16) float sh_p[C * LDC];  // P
+  __shared__ __align__(16) float sh_m[C * LDC];  // M
+  __shared__ __align__(16) float sh_bp[4][D];    // decays of the blocks
+  __shared__ __align__(16) float sh_b[C];        // beta
+  const int i = lane & 15, g = lane >> 4;
+  stage_rows<E>(sh_k, A.k, hk, ch.t0, ch.len, tid);
+  stage_rows<E>(sh_q, A.q, hk, ch.t0, ch.len, tid);
+  {
+    const int row = tid >> 2, c0 = (tid & 3) * 4;
+    const float *p = at<const float>(A.alpha, ch.t0 + (row < ch.len ? row : 0), hv) + c0;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      float4 x = *reinterpret_cast<const float4 *>(p + 16 * c);
+      if (row >= ch.len) x = make_float4(1.f, 1.f, 1.f, 1.f);
+      *reinterpret_cast<float4 *>(sh_a + row * LDD + c0 + 16 * c) = x;
+    }
+  }
+  if (tid < C) sh_b[tid] = tid < ch.len ? *at<const float>(A.beta, ch.t0 + tid, hv) : 0.f;
+  __syncthreads();
+  // ---- block w's own products: lane (token i, channels 32 g .. + 31), token j = i - o
+  {
+    const int row = 16 * w + i;
+    float d[32], ki[32], qi[32];
+#pragma unroll
+    for (int c = 0; c < 32; c += 4) {
+      const float4 x = *reinterpret_cast<const float4 *>(sh_k + row * LDD + 32 * g + c);
+      const float4 y = *reinterpret_cast<const float4 *>(sh_q + row * LDD + 32 * g + c);
+      ki[c] = x.x; ki[c + 1] = x.y; ki[c + 2] = x.z; ki[c + 3] = x.w;
+      qi[c] = y.x; qi[c + 1] = y.y; qi[c + 2] = y.z; qi[c + 3] = y.w;
+      d[c] = d[c + 1] = d[c + 2] = d[c + 3] = 1.f;
+    }
+#pragma unroll 1
+    for (int o = 0; o < 16; ++o) {
+      const int j = i - o < 0 ? 0 : i - o;  // (tokens before the block: computed, not stored)
+      const float *pk = sh_k + (16 * w + j) * LDD + 32 * g;
+      float sk = 0.f, sq = 0.f;
+#pragma unroll
+      for (int c = 0; c < 32; c += 4) {
+        const float4 x = *reinterpret_cast<const float4 *>(pk + c);
+        const float kj[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float t = d[c + e] * kj[e];
+          if (DELTA) sk = fmaf(ki[c + e], t, sk);
+          sq = fmaf(qi[c + e], t, sq);
+        }
+      }
+      if (DELTA) {
+        sk += __shfl_xor(sk, 16);
+        sk += __shfl_xor(sk, 32);
+      }
+      sq += __shfl_xor(sq, 16);
+      sq += __shfl_xor(sq, 32);
+      if (g == 0 && o <= i) {
+        const int col = 16 * w + j;
+        const float be = sh_b[col];
+        sh_p[row * LDC + col] = be * sq;
+        if (DELTA && o) sh_m[row * LDC + col] = be * sk;
+      }
+      const float *pa = sh_a + (16 * w + j) * LDD + 32 * g;  // on to the token before
+#pragma unroll
+      for (int c = 0; c < 32; c += 4) {
+        const float4 x = *reinterpret_cast<const float4 *>(pa + c);
+        d[c] *= x.x; d[c + 1] *= x.y; d[c + 2] *= x.z; d[c + 3] *= x.w;
+      }
+    }
+    // the rest of the diagonal block: zeros
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int col = 4 * g + e;
+      if (col > i) sh_p[row * LDC + 16 * w + col] = 0.f;
+      if (DELTA && col >= i) sh_m[row * LDC + 16 * w + col] = 0.f;
+    }
+  }
+  __syncthreads();
+  // ---- k a, q a, k b and the blocks' decays: thread (channel, block pair)
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int c = tid & 127, b = 2 * (tid >> 7) + e;
+    float *pk = sh_k + 16 * b * LDD + c, *pq = sh_q + 16 * b * LDD + c, *pa = sh_a + 16 * b * LDD + c;
+    float al[16], x = 1.f;
+#pragma unroll
+    for (int t = 0; t < 16; ++t) al[t] = pa[t * LDD];
+#pragma unroll
+    for (int t = 15; t >= 0; --t) {
+      pa[t * LDD] = pk[t * LDD] * x;  // decays of the tokens behind t
+      x *= al[t];
+    }
+    sh_bp[b][c] = x;
+    x = 1.f;
+#pragma unroll
+    for (int t = 0; t < 16; ++t) {
+      x *= al[t];
+      pk[t * LDD] *= x;
+      pq[t * LDD] *= x;
+    }
+  }
+  __syncthreads();
+  // ---- products between blocks, and K and Q with the decays from the chunk's start: wave w has rows 16 w ..
+  {
+    floatx4 qk[3], kk[3];
+#pragma unroll
+    for (int n = 0; n < 3; ++n) qk[n] = kk[n] = floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+    for (int x = 0; x < 4; ++x) {
+      const int c0 = 32 * x + 8 * g;
+      float k[8], q[8], m[8], v[8];
+      bf8 fk[3], fq[3], f[3];
+      load8(reinterpret_cast<const F32 *>(sh_k + (16 * w + i) * LDD + c0), k);
+      load8(reinterpret_cast<const F32 *>(sh_q + (16 * w + i) * LDD + c0), q);
+      split8<3>(k, fk);
+      split8<3>(q, fq);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) m[e] = 1.f;  // decays of the blocks between
+#pragma unroll
+      for (int n = 2; n >= 0; --n) {
+        if (n >= w) continue;
+        load8(reinterpret_cast<const F32 *>(sh_a + (16 * n + i) * LDD + c0), v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] *= m[e];
+        split8<3>(v, f);
+        mma_into<3, 3>(qk[n], fq, f);
+        if (DELTA) mma_into<3, 3>(kk[n], fk, f);
+        load8(reinterpret_cast<const F32 *>(&sh_bp[n][c0]), v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m[e] *= v[e];
+      }
+      // m: now the decays of all blocks before w
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        k[e] *= m[e];
+        q[e] *= m[e];
+      }
+      split8<3>(k, fk);
+      split8<3>(q, fq);
+      if (DELTA) frag_store<3>(A.w.K + ((at_ * 4 + w) * 4 + x) * 3 * 512, fk, lane);
+      frag_store<3>(A.w.Q + ((at_ * 4 + w) * 4 + x) * 3 * 512, fq, lane);
+    }
+#pragma unroll
+    for (int n = 0; n < 3; ++n) {
+      if (n >= w) continue;
+      const int j = 16 * n + i;
+      const float be = sh_b[j];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int row = 16 * w + 4 * g + r;
+        sh_p[row * LDC + j] = be * qk[n][r];
+        if (DELTA) sh_m[row * LDC + j] = be * kk[n][r];
+      }
+    }
+    // P's blocks above the diagonal in the steps that are stored: zeros
+    for (int n = w + 1; n < 4; ++n)
+      *reinterpret_cast<float4 *>(sh_p + (16 * w + i) * LDC + 16 * n + 4 * g) = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  // ---- K^T with beta and the decays to the chunk's end: key rows 32 w .. + 31
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int mt = 2 * w + (e >> 1), x = e & 1, c = 16 * mt + i;
+    // tokens 32 x + 8 g .. + 7 lie in block 2 x + (g >> 1)
+    const float b1 = sh_bp[1][c], b2 = sh_bp[2][c], b3 = sh_bp[3][c];
+    const int blk = 2 * x + (g >> 1);
+    const float rest = blk == 0 ? b1 * b2 * b3 : (blk == 1 ? b2 * b3 : (blk == 2 ? b3 : 1.f));
+    float v[8];
+    bf8 f[3];
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+      const int tok = 32 * x + 8 * g + t;
+      v[t] = sh_b[tok] * rest * sh_a[tok * LDD + c];
+    }
+    split8<3>(v, f);
+    frag_store<3>(A.w.KT + ((at_ * 8 + mt) * 2 + x) * 3 * 512, f, lane);
+  }
+  if (tid < D) A.w.dec[at_ * 2 * C + tid] = (sh_bp[0][tid] * sh_bp[1][tid]) * (sh_bp[2][tid] * sh_bp[3][tid]);
+  __syncthreads();
+  if (DELTA) invert_unit_lower(sh_k, sh_m, w, lane);
+  store_triangles<DELTA>(A, at_, sh_k, sh_p, w, lane);
+}
+
+// ---------------------------------------------------------------------------
 // Scan: one workgroup per (sequence, value head, block of CB columns), chunk
 // after chunk.  Wave w takes token tile w (16 rows) of the products with 64
 // rows and rows 32 w .. + 31 of the state, whose block stays in its
@@ -365,9 +578,11 @@ __global__ __launch_bounds__(256) void seq_prep_kernel(const SeqArgs A) {
 // is rounded at 2^-9 or 2^-12, so parts below 2^-16 are left out of Q S and
 // P U there (never out of U and S).
 // ---------------------------------------------------------------------------
-template <class E, bool DELTA, bool SAVE, int CB>
+template <class E, bool KDA, bool DELTA, bool SAVE, int CB>
 __global__ __launch_bounds__(256) void seq_scan_kernel(const SeqArgs A) {
-  constexpr int NT = CB / 16, kBlocks = D / CB, NP = Parts<E>::n, NO = NP == 3 ? 3 : 2;
+  constexpr int NT = CB / 16, kBlocks = D / CB, NO = Parts<E>::n == 3 ? 3 : 2;
+  // parts of K and K^T, and of Q; with a decay a channel they hold decays, per value head
+  constexpr int NP = KDA ? 3 : Parts<E>::n, NQ = KDA ? NO : NP;
   constexpr int FS = 4 * NT, FX = 2 * NT;  // fragments of a part of [CB][128], [CB][64]
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -376,12 +591,13 @@ __global__ __launch_bounds__(256) void seq_scan_kernel(const SeqArgs A) {
   const int64_t b = blockIdx.x;
   const int64_t unit = (b / (8 * kBlocks)) * 8 + (b & 7);
   if (unit >= (int64_t)A.seqs * A.hv) return;
-  const int seq = (int)(unit / A.hv), hv = (int)(unit % A.hv), hk = hv / A.group;
+  const int seq = (int)(unit / A.hv), hv = (int)(unit % A.hv);
+  const int hk = KDA ? hv : hv / A.group, heads_k = KDA ? A.hv : A.hk;
   const int start = seq_start(A, seq), end = seq_end(A, seq, start);
   __shared__ __align__(16) uint16_t sh_s[3 * FS * 512];              // S, [column][key row]
   __shared__ __align__(16) uint16_t sh_x[DELTA ? 3 * FX * 512 : 8];  // X, [column][token]
-  __shared__ __align__(16) uint16_t sh_u[NO * FX * 512];             // U
-  __shared__ __align__(16) uint16_t sh_ku[3 * FX * 512];             // kappa * U
+  __shared__ __align__(16) uint16_t sh_u[KDA ? 8 : NO * FX * 512];   // U
+  __shared__ __align__(16) uint16_t sh_ku[3 * FX * 512];             // kappa * U; with a decay a channel U
   __shared__ __align__(16) float sh_dec[2][2 * C];                   // decays, of this chunk and the next
   const int i = lane & 15, g = lane >> 4, tok = 16 * w + 4 * g;
   const int col = (int)((b >> 3) % kBlocks) * CB + NT * i;  // the lane's first column
@@ -403,7 +619,7 @@ __global__ __launch_bounds__(256) void seq_scan_kernel(const SeqArgs A) {
   // end is the chunk's first row instead; its X is set to zero and its columns
   // of P and K^T are zero.  V's pointer moves on from chunk to chunk (`move`:
   // 1, or 0 where there is none: then the last chunk is read again).
-  bf8 fk[4][NP], fq[4][NP], fT[2][3], fP[2][NO], fKT[2][2][NP];
+  bf8 fk[4][NP], fq[4][NQ], fT[2][3], fP[2][NO], fKT[2][2][NP];
   E v[4][NT];
   float dec;  // thread t < 128: value t of the next chunk's decays
   const int slot0 = start / C + seq;
@@ -411,11 +627,11 @@ __global__ __launch_bounds__(256) void seq_scan_kernel(const SeqArgs A) {
   const E *pV = at<const E>(A.v, start + tok, hv) + col;
   const int64_t backV = tok * A.v.ts;
   auto load_k = [&](int c) {
-    const size_t f = (((size_t)(slot0 + c) * A.hk + hk) * 4 + w) * 4 * NP * 512;
+    const size_t f = (((size_t)(slot0 + c) * heads_k + hk) * 4 + w) * 4 * NP * 512;
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
       if (DELTA) frag_load<NP>(fk[x], A.w.K + f + x * NP * 512, lane);
-      frag_load<NP>(fq[x], A.w.Q + f + x * NP * 512, lane);
+      frag_load<NQ>(fq[x], A.w.Q + f + x * NP * 512, lane);
     }
   };
   auto load_v = [&](int c, int move) {
@@ -438,7 +654,7 @@ __global__ __launch_bounds__(256) void seq_scan_kernel(const SeqArgs A) {
     if (w >= 2) frag_load<NO>(fP[1], p + 3 * 512, lane);
   };
   auto load_KT = [&](int c) {
-    const uint16_t *p = A.w.KT + (((size_t)(slot0 + c) * A.hk + hk) * 8 + 2 * w) * 2 * NP * 512;
+    const uint16_t *p = A.w.KT + (((size_t)(slot0 + c) * heads_k + hk) * 8 + 2 * w) * 2 * NP * 512;
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -482,13 +698,22 @@ __global__ __launch_bounds__(256) void seq_scan_kernel(const SeqArgs A) {
         bf8 fs[3];
         frag_get<3, FS>(fs, sh_s, 4 * n + x, lane);
         if (DELTA) mma_parts<NP, 3>(yk[n], fk[x], fs);
-        mma_parts<NP, 3, NO>(yq[n], fq[x], fs);
+        mma_parts<NQ, 3, NO>(yq[n], fq[x], fs);
       }
     load_k(next);
     const float *sd = sh_dec[c & 1];
-    const float4 gm4 = *reinterpret_cast<const float4 *>(sd + tok), kp4 = *reinterpret_cast<const float4 *>(sd + C + tok);
-    const float gm[4] = {gm4.x, gm4.y, gm4.z, gm4.w}, kp[4] = {kp4.x, kp4.y, kp4.z, kp4.w};
-    const float la = sd[C - 1];
+    float gm[4], kp[4], la[2][4];
+    if (KDA) {  // a decay for every row of the state, none for the tokens
+#pragma unroll
+      for (int r = 0; r < 4; ++r) gm[r] = kp[r] = 1.f;
+#pragma unroll
+      for (int m = 0; m < 2; ++m) load4(reinterpret_cast<const F32 *>(sd + 32 * w + 16 * m + 4 * g), la[m]);
+    } else {
+      load4(reinterpret_cast<const F32 *>(sd + tok), gm);
+      load4(reinterpret_cast<const F32 *>(sd + C + tok), kp);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) la[0][r] = la[1][r] = sd[C - 1];
+    }
     floatx4 u[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -529,7 +754,7 @@ __global__ __launch_bounds__(256) void seq_scan_kernel(const SeqArgs A) {
     for (int n = 0; n < NT; ++n) {
       frag_share<3, FX>(sh_ku, 2 * n + (w >> 1), w & 1, lane, kp[0] * u[n][0], kp[1] * u[n][1], kp[2] * u[n][2],
                         kp[3] * u[n][3]);
-      frag_share<NO, FX>(sh_u, 2 * n + (w >> 1), w & 1, lane, u[n][0], u[n][1], u[n][2], u[n][3]);
+      if (!KDA) frag_share<NO, FX>(sh_u, 2 * n + (w >> 1), w & 1, lane, u[n][0], u[n][1], u[n][2], u[n][3]);
     }
     if (SAVE) {
 #pragma unroll
@@ -562,7 +787,7 @@ __global__ __launch_bounds__(256) void seq_scan_kernel(const SeqArgs A) {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           bf8 fu[NO];
-          frag_get<NO, FX>(fu, sh_u, 2 * n + x, lane);
+          frag_get<NO, FX>(fu, KDA ? sh_ku : sh_u, 2 * n + x, lane);
           mma_parts<NO, NO, NO>(yq[n], fP[x], fu);
         }
       }
@@ -572,7 +797,11 @@ __global__ __launch_bounds__(256) void seq_scan_kernel(const SeqArgs A) {
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
-      for (int n = 0; n < NT; ++n) s[m][n] = s[m][n] * la + ds[m][n].sum();
+      for (int n = 0; n < NT; ++n) {
+        const floatx4 d = ds[m][n].sum();
+#pragma unroll
+        for (int r = 0; r < 4; ++r) s[m][n][r] = fmaf(s[m][n][r], la[m][r], d[r]);
+      }
     E *o = at<E>(A.o, t0 + tok, hv) + col;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
@@ -623,26 +852,31 @@ hipError_t launch_seq_recurrent(const SeqArgs &a, int dtype, bool kda, bool delt
                       : recurrent<F16>(a, kda, delta, stream);
 }
 
-template <class E, bool DELTA, bool SAVE>
+template <class E, bool KDA, bool DELTA, bool SAVE>
 hipError_t chunked(const SeqArgs &a, hipStream_t stream) {
   const int64_t units = ((int64_t)a.seqs * a.hv + 7) / 8 * 8;
-  hipLaunchKernelGGL((seq_prep_kernel<E, DELTA, SAVE>), dim3((unsigned)a.slots, a.hv), dim3(256), 0, stream, a);
-  if (scan_wide(a))
-    hipLaunchKernelGGL((seq_scan_kernel<E, DELTA, SAVE, 32>), dim3((unsigned)(units * 4)), dim3(256), 0, stream, a);
+  const dim3 slots((unsigned)a.slots, a.hv);
+  if constexpr (KDA)
+    hipLaunchKernelGGL((seq_prep_kda_kernel<E, DELTA>), slots, dim3(256), 0, stream, a);
   else
-    hipLaunchKernelGGL((seq_scan_kernel<E, DELTA, SAVE, 16>), dim3((unsigned)(units * 8)), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL((seq_prep_kernel<E, DELTA, SAVE>), slots, dim3(256), 0, stream, a);
+  if (scan_wide(a))
+    hipLaunchKernelGGL((seq_scan_kernel<E, KDA, DELTA, SAVE, 32>), dim3((unsigned)(units * 4)), dim3(256), 0, stream, a);
+  else
+    hipLaunchKernelGGL((seq_scan_kernel<E, KDA, DELTA, SAVE, 16>), dim3((unsigned)(units * 8)), dim3(256), 0, stream, a);
   return hipGetLastError();
 }
 template <class E>
-hipError_t chunked(const SeqArgs &a, bool delta, hipStream_t stream) {
+hipError_t chunked(const SeqArgs &a, bool kda, bool delta, hipStream_t stream) {
   const bool save = a.w.S != nullptr;
-  if (delta) return save ? chunked<E, true, true>(a, stream) : chunked<E, true, false>(a, stream);
-  return save ? chunked<E, false, true>(a, stream) : chunked<E, false, false>(a, stream);
+  if (kda) return delta ? chunked<E, true, true, false>(a, stream) : chunked<E, true, false, false>(a, stream);
+  if (delta) return save ? chunked<E, false, true, true>(a, stream) : chunked<E, false, true, false>(a, stream);
+  return save ? chunked<E, false, false, true>(a, stream) : chunked<E, false, false, false>(a, stream);
 }
-hipError_t launch_seq_chunked(const SeqArgs &a, int dtype, bool delta, hipStream_t stream) {
-  return dtype == 0 ? chunked<F32>(a, delta, stream)
-         : dtype == 1 ? chunked<BF16>(a, delta, stream)
-                      : chunked<F16>(a, delta, stream);
+hipError_t launch_seq_chunked(const SeqArgs &a, int dtype, bool kda, bool delta, hipStream_t stream) {
+  return dtype == 0 ? chunked<F32>(a, kda, delta, stream)
+         : dtype == 1 ? chunked<BF16>(a, kda, delta, stream)
+                      : chunked<F16>(a, kda, delta, stream);
 }
 
 }  // namespace lq

@@ -120,14 +120,15 @@ int check_sequence(const lq_sequence *sq) {
 }
 
 bool chunked(const lq_sequence *sq, bool save) {
-  return sq->tokens > 0 && sq->gate == LQ_GATE_GDN && (save || sq->tokens > kShort * sq->seqs);
+  return sq->tokens > 0 && (save || sq->tokens > kShort * sq->seqs);
 }
 
 // The arrays of lq::SeqSpace, one behind another from `base`; returns the
 // bytes they take (the sizes alone with base = nullptr).
 int64_t space(const lq_sequence *sq, int64_t slots, bool save, char *base, lq::SeqSpace *w) {
-  const int64_t hk = slots * sq->heads_k, hv = slots * sq->heads_v;
-  const int64_t parts = sq->dtype == LQ_F32 ? 3 : sq->dtype == LQ_F16 ? 2 : 1;
+  const bool kda = sq->gate == LQ_GATE_KDA;  // K and Q with decays: per value head, as fp32 values
+  const int64_t hv = slots * sq->heads_v, hk = kda ? hv : slots * sq->heads_k;
+  const int64_t parts = kda || sq->dtype == LQ_F32 ? 3 : sq->dtype == LQ_F16 ? 2 : 1;
   const int64_t square = lq::kChunk * lq::kChunk * 3 * 2, heads = lq::kChunk * kDim * parts * 2;
   const int64_t rows = lq::kChunk * kDim * 4, state = kDim * kDim * 4;
   int64_t used = 0;
@@ -211,7 +212,7 @@ int check_norm(const lq_head_norm *nm) {
     if (!nm->positions || !nm->inv_freq) return LQ_ERR_NULL;
     if (!aligned(nm->positions, 8) || !aligned(nm->inv_freq, 8)) return LQ_ERR_ALIGN;
   }
-  if (!aligned(nm->q_weight, 4) || !aligned(nm->k_weight, 4)) return LQ_ERR_ALIGN;
+  if (!aligned(nm->q_weight, 16) || !aligned(nm->k_weight, 16)) return LQ_ERR_ALIGN;
   // four runs of sixteen heads a workgroup
   if (nm->tokens * ((nm->heads_q + nm->heads_k + 15) / 16) > kMaxGrid * 4) return LQ_ERR_SHAPE;
   return LQ_OK;
@@ -249,7 +250,7 @@ extern "C" {
 int64_t leapquant_sequence_workspace(const lq_sequence *sq, int32_t save) {
   const int rc = check_sequence(sq);
   if (rc) return rc;
-  if (sq->gate == LQ_GATE_KDA) return save ? LQ_ERR_UNSUPPORTED : 0;
+  if (save && sq->gate == LQ_GATE_KDA) return LQ_ERR_UNSUPPORTED;
   if (save) return sq->tokens ? space_bytes(sq, slots_of(sq->tokens, sq->seqs), true) : 0;
   // the most sequences with which that many tokens are taken in chunks
   const int64_t most = sq->tokens > 0 ? (sq->tokens - 1) / kShort : 0;
@@ -282,7 +283,7 @@ int leapquant_sequence_forward(const lq_sequence *sq, const int32_t *cu_seqlens,
   a.S0 = S0;
   a.S = S;
   if (!chunked(sq, save != 0)) return hip_status(lq::launch_seq_recurrent(a, sq->dtype, kda, delta, stream));
-  return hip_status(lq::launch_seq_chunked(a, sq->dtype, delta, stream));
+  return hip_status(lq::launch_seq_chunked(a, sq->dtype, kda, delta, stream));
 }
 
 int leapquant_sequence_backward(const lq_sequence *sq, const int32_t *cu_seqlens, const lq_rows *q, const lq_rows *k,

@@ -410,19 +410,31 @@ __device__ __forceinline__ Raw8<E> raw_load(const E *p) {
   for (int n = 0; n < (int)(sizeof(E) / 2); ++n) r.v[n] = reinterpret_cast<const uint4 *>(p)[n];
   return r;
 }
+__device__ __forceinline__ void raw_floats(float (&x)[8], const Raw8<F32> &r) {
+  const float4 a = __builtin_bit_cast(float4, r.v[0]), b = __builtin_bit_cast(float4, r.v[1]);
+  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+}
+__device__ __forceinline__ void raw_floats(float (&x)[8], const Raw8<BF16> &r) {
+  const uint32_t w[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    x[2 * e] = __uint_as_float(w[e] << 16);
+    x[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ void raw_floats(float (&x)[8], const Raw8<F16> &r) {
+  const f16x8 h = __builtin_bit_cast(f16x8, r.v[0]);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] = (float)h[e];
+}
 template <class E, int N>
 __device__ __forceinline__ void raw_parts(bf8 (&f)[N], const Raw8<E> &r) {
   if constexpr (N == 1) {
     f[0] = __builtin_bit_cast(bf8, r.v[0]);
-  } else if constexpr (sizeof(E) == 2) {
-    const f16x8 h = __builtin_bit_cast(f16x8, r.v[0]);
-    float x[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = (float)h[e];
-    split8<N>(x, f);
   } else {
-    const float4 a = __builtin_bit_cast(float4, r.v[0]), b = __builtin_bit_cast(float4, r.v[1]);
-    const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    float x[8];
+    raw_floats(x, r);
     split8<N>(x, f);
   }
 }

@@ -23,17 +23,28 @@ def _rows(x, dtype, shape, name, device):
     """A strided [tokens, heads(, 128)] tensor as lq_rows."""
     if not isinstance(x, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if x.device.type != "cuda":
-        raise ValueError(f"{name} must be in device memory")
     if x.device != device:
-        raise ValueError(f"{name} is on {x.device}, the call on {device}")
+        raise ValueError(f"{name} must be in device memory" if x.device.type != "cuda" else
+                         f"{name} is on {x.device}, the call on {device}")
     if x.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {x.dtype}")
-    if tuple(x.shape) != tuple(shape):
+    if x.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(x.shape)}")
-    if x.dim() == 3 and x.numel() and x.stride(2) != 1:
+    strides = x.stride()
+    if len(strides) == 3 and strides[2] != 1 and x.numel():
         raise ValueError(f"{name}: the values of a head must be contiguous")
-    return ctypes.byref(L.LqRows(x.data_ptr() or None, x.stride(0), x.stride(1)))
+    return L.LqRows(x.data_ptr() or None, strides[0], strides[1])
+
+
+def _launch(fn, device, stream, *args):
+    """The call on its device, with the stream's handle as the last argument."""
+    if device.type != "cuda":
+        raise ValueError("the call's tensors must be in device memory")
+    handle = _stream(stream, device)
+    if torch.cuda.current_device() == device.index:
+        return L.check(fn(*args, handle))
+    with torch.cuda.device(device):
+        L.check(fn(*args, handle))
 
 
 def _states(x, n, name, device):
@@ -104,9 +115,7 @@ def leapquant_sequence_forward(plan, cu_seqlens, q, k, v, beta, alpha, o, S0=Non
             _rows(v, dt, (T, hv, 128), "v", d), _rows(beta, _F32, (T, hv), "beta", d),
             _rows(alpha, _F32, ashape, "alpha", d), _rows(o, dt, (T, hv, 128), "o", d),
             _states(S0, seqs * hv, "S0", d), _states(S, seqs * hv, "S", d)]
-    with torch.cuda.device(d):
-        L.check(L.load().leapquant_sequence_forward(ctypes.byref(prm), cu, *args, *plan._space(), int(plan.save),
-                                                    _stream(stream, d)))
+    _launch(L.load().leapquant_sequence_forward, d, stream, prm, cu, *args, *plan._space(), int(plan.save))
 
 
 def leapquant_sequence_backward(plan, cu_seqlens, q, k, beta, alpha, do, dq, dk, dv, dbeta, dalpha, dS=None,
@@ -125,9 +134,7 @@ def leapquant_sequence_backward(plan, cu_seqlens, q, k, beta, alpha, do, dq, dk,
             _rows(dq, dt, (T, hk, 128), "dq", d), _rows(dk, dt, (T, hk, 128), "dk", d),
             _rows(dv, dt, (T, hv, 128), "dv", d), _rows(dbeta, _F32, (T, hv), "dbeta", d),
             _rows(dalpha, _F32, (T, hv), "dalpha", d), _states(dS0, seqs * hv, "dS0", d)]
-    with torch.cuda.device(d):
-        L.check(L.load().leapquant_sequence_backward(ctypes.byref(prm), cu, *args, *plan._space(),
-                                                     _stream(stream, d)))
+    _launch(L.load().leapquant_sequence_backward, d, stream, prm, cu, *args, *plan._space())
 
 
 def _norm_params(q, k, out, norm, eps, q_weight, k_weight, q_scale, positions, inv_freq, interleaved):
@@ -164,8 +171,7 @@ def leapquant_head_norm(q, k, q_out, k_out, norm="l2", eps=1e-6, q_weight=None, 
     d, T, shape_q, shape_k = q.device, q.shape[0], (q.shape[0], q.shape[1], 128), (q.shape[0], k.shape[1], 128)
     args = [_rows(q, q.dtype, shape_q, "q", d), _rows(k, q.dtype, shape_k, "k", d),
             _rows(q_out, q_out.dtype, shape_q, "q_out", d), _rows(k_out, q_out.dtype, shape_k, "k_out", d)]
-    with torch.cuda.device(d):
-        L.check(L.load().leapquant_head_norm(ctypes.byref(prm), *args, _stream(stream, d)))
+    _launch(L.load().leapquant_head_norm, d, stream, prm, *args)
 
 
 def leapquant_head_norm_workspace(tokens, heads_q, heads_k, device="cuda"):
@@ -192,5 +198,4 @@ def leapquant_head_norm_backward(q, k, dq_out, dk_out, dq, dk, norm="l2", eps=1e
         args += [None, 0]
     else:
         args += [_ptr(workspace, torch.uint8, (workspace.numel(),), "workspace", d), workspace.numel()]
-    with torch.cuda.device(d):
-        L.check(L.load().leapquant_head_norm_backward(ctypes.byref(prm), *args, _stream(stream, d)))
+    _launch(L.load().leapquant_head_norm_backward, d, stream, prm, *args)
