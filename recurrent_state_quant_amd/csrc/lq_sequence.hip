@@ -131,12 +131,12 @@ __global__ __launch_bounds__(256) void seq_recurrent_kernel(const SeqArgs A) {
 // T = (I + M)^-1 for the unit lower triangle I + M (M fp32 [64][LDC], below the
 // diagonal; its blocks above are used on the way), by blocks of 16: each
 // diagonal block by forward substitution (a column per lane), then 16 -> 32 ->
-// 64 by T_ba = -T_b (M_ba T_a) on the fp32 matrix path.  Four waves; ends with
-// a barrier.  T's blocks above the diagonal are not written.
+// 64 by T_ba = -T_b (M_ba T_a) on the fp32 matrix path.  Waves 0 .. 3 work;
+// ends with a barrier.  T's blocks above the diagonal are not written.
 __device__ __forceinline__ void invert_unit_lower(float *sh_t, float *sh_m, int w, int lane) {
   const int i = lane & 15, g = lane >> 4;
   const floatx4 zero = {0.f, 0.f, 0.f, 0.f};
-  {
+  if (w < 4) {
     // diagonal block w, column i (the four groups of lanes do the same)
     const int d0 = 16 * w;
     float t[16];
@@ -165,14 +165,14 @@ __device__ __forceinline__ void invert_unit_lower(float *sh_t, float *sh_m, int 
   }
   __syncthreads();
   const int a = 2 + (w >> 1), b = w & 1;
-  {
+  if (w < 4) {
     floatx4 y = zero;
     for (int c = b; c < 2; ++c)
       mma(y, frag<false>(sh_m + 16 * c, LDC, 16 * a, 0, lane), frag<true>(sh_t + 16 * c * LDC, LDC, 16 * b, 0, lane));
     *reinterpret_cast<float4 *>(sh_m + (16 * b + i) * LDC + 16 * a + 4 * g) = make_float4(y[0], y[1], y[2], y[3]);
   }
   __syncthreads();
-  {
+  if (w < 4) {
     floatx4 z = zero;
     for (int c = 2; c <= a; ++c)
       mma(z, frag<false>(sh_t + 16 * c, LDC, 16 * a, 0, lane), frag<false>(sh_m + 16 * c, LDC, 16 * b, 0, lane));
@@ -369,11 +369,10 @@ __global__ __launch_bounds__(256) void seq_prep_kernel(const SeqArgs A) {
 //   M_ij = beta_j sum_c (k a)_ic (m (k b))_jc
 // are matrix products of factors that are all at most 1 (for alpha <= 1), and
 // inside a block the sums are taken directly, the decay running from token to
-// token (a lane has a token and 32 channels).  Decays of zero are exact.
-// The direct sums are about half of the kernel's time.
+// token (a lane has a token and 16 channels).  Decays of zero are exact.
 // ---------------------------------------------------------------------------
 template <class E, bool DELTA>
-__global__ __launch_bounds__(256) void seq_prep_kda_kernel(const SeqArgs A) {
+__global__ __launch_bounds__(512) void seq_prep_kda_kernel(const SeqArgs A) {
   const int slot = blockIdx.x, hv = blockIdx.y, hk = hv / A.group;
   const int tid = threadIdx.x, lane = tid & 63;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -388,80 +387,86 @@ __global__ __launch_bounds__(256) void seq_prep_kda_kernel(const SeqArgs A) {
   __shared__ __align__(16) float sh_bp[4][D];    // decays of the blocks
   __shared__ __align__(16) float sh_b[C];        // beta
   const int i = lane & 15, g = lane >> 4;
-  stage_rows<E>(sh_k, A.k, hk, ch.t0, ch.len, tid);
-  stage_rows<E>(sh_q, A.q, hk, ch.t0, ch.len, tid);
   {
-    const int row = tid >> 2, c0 = (tid & 3) * 4;
-    const float *p = at<const float>(A.alpha, ch.t0 + (row < ch.len ? row : 0), hv) + c0;
+    const int row = tid >> 3, c0 = (tid & 7) * 8, src = ch.t0 + (row < ch.len ? row : 0);
+    const float *pa = at<const float>(A.alpha, src, hv) + c0;
+    const E *pk = at<const E>(A.k, src, hk) + c0, *pq = at<const E>(A.q, src, hk) + c0;
+    const bool on = row < ch.len;
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      float4 x = *reinterpret_cast<const float4 *>(p + 16 * c);
-      if (row >= ch.len) x = make_float4(1.f, 1.f, 1.f, 1.f);
-      *reinterpret_cast<float4 *>(sh_a + row * LDD + c0 + 16 * c) = x;
+    for (int c = 0; c < 2; ++c) {
+      float x[8], y[8], z[8];
+      load8(pk + 64 * c, x);
+      load8(pq + 64 * c, y);
+      load8(reinterpret_cast<const F32 *>(pa + 64 * c), z);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        x[e] = on ? x[e] : 0.f;
+        y[e] = on ? y[e] : 0.f;
+        z[e] = on ? z[e] : 1.f;
+      }
+      const int o = row * LDD + c0 + 64 * c;
+      store8(reinterpret_cast<F32 *>(sh_k + o), x);
+      store8(reinterpret_cast<F32 *>(sh_q + o), y);
+      store8(reinterpret_cast<F32 *>(sh_a + o), z);
     }
   }
-  if (tid < C) sh_b[tid] = tid < ch.len ? *at<const float>(A.beta, ch.t0 + tid, hv) : 0.f;
+  if (tid < C) {
+    const float be = *at<const float>(A.beta, ch.t0 + (tid < ch.len ? tid : 0), hv);
+    sh_b[tid] = tid < ch.len ? be : 0.f;
+  }
   __syncthreads();
-  // ---- block w's own products: lane (token i, channels 32 g .. + 31), token j = i - o
+  // ---- the products inside a block: a wave has half of one's tokens, a lane
+  // (token i = lane >> 3, channels 16 (lane & 7) .. + 15), token j = i - o
   {
-    const int row = 16 * w + i;
-    float d[32], ki[32], qi[32];
+    const int blk = 16 * (w >> 1), ti = 8 * (w & 1) + (lane >> 3), row = blk + ti, c0 = 16 * (lane & 7);
+    float d[16], ki[16], qi[16];
 #pragma unroll
-    for (int c = 0; c < 32; c += 4) {
-      const float4 x = *reinterpret_cast<const float4 *>(sh_k + row * LDD + 32 * g + c);
-      const float4 y = *reinterpret_cast<const float4 *>(sh_q + row * LDD + 32 * g + c);
+    for (int c = 0; c < 16; c += 4) {
+      const float4 x = *reinterpret_cast<const float4 *>(sh_k + row * LDD + c0 + c);
+      const float4 y = *reinterpret_cast<const float4 *>(sh_q + row * LDD + c0 + c);
       ki[c] = x.x; ki[c + 1] = x.y; ki[c + 2] = x.z; ki[c + 3] = x.w;
       qi[c] = y.x; qi[c + 1] = y.y; qi[c + 2] = y.z; qi[c + 3] = y.w;
       d[c] = d[c + 1] = d[c + 2] = d[c + 3] = 1.f;
     }
-#pragma unroll 1
-    for (int o = 0; o < 16; ++o) {
-      const int j = i - o < 0 ? 0 : i - o;  // (tokens before the block: computed, not stored)
-      const float *pk = sh_k + (16 * w + j) * LDD + 32 * g;
+    const int most = 8 * (w & 1) + 8;
+#pragma unroll 2
+    for (int o = 0; o < most; ++o) {
+      const int j = ti - o < 0 ? 0 : ti - o;  // (tokens before the block: computed, not stored)
+      const float *pk = sh_k + (blk + j) * LDD + c0, *pa = sh_a + (blk + j) * LDD + c0;
       float sk = 0.f, sq = 0.f;
 #pragma unroll
-      for (int c = 0; c < 32; c += 4) {
-        const float4 x = *reinterpret_cast<const float4 *>(pk + c);
-        const float kj[4] = {x.x, x.y, x.z, x.w};
+      for (int c = 0; c < 16; c += 4) {
+        const float4 x = *reinterpret_cast<const float4 *>(pk + c), y = *reinterpret_cast<const float4 *>(pa + c);
+        const float kj[4] = {x.x, x.y, x.z, x.w}, aj[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float t = d[c + e] * kj[e];
           if (DELTA) sk = fmaf(ki[c + e], t, sk);
           sq = fmaf(qi[c + e], t, sq);
+          d[c + e] *= aj[e];  // on to the token before
         }
       }
-      if (DELTA) {
-        sk += __shfl_xor(sk, 16);
-        sk += __shfl_xor(sk, 32);
-      }
-      sq += __shfl_xor(sq, 16);
-      sq += __shfl_xor(sq, 32);
-      if (g == 0 && o <= i) {
-        const int col = 16 * w + j;
+      if (DELTA) sk = row8_sum(sk);
+      sq = row8_sum(sq);
+      if ((lane & 7) == 0 && o <= ti) {
+        const int col = blk + j;
         const float be = sh_b[col];
         sh_p[row * LDC + col] = be * sq;
         if (DELTA && o) sh_m[row * LDC + col] = be * sk;
       }
-      const float *pa = sh_a + (16 * w + j) * LDD + 32 * g;  // on to the token before
-#pragma unroll
-      for (int c = 0; c < 32; c += 4) {
-        const float4 x = *reinterpret_cast<const float4 *>(pa + c);
-        d[c] *= x.x; d[c + 1] *= x.y; d[c + 2] *= x.z; d[c + 3] *= x.w;
-      }
     }
     // the rest of the diagonal block: zeros
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int col = 4 * g + e;
-      if (col > i) sh_p[row * LDC + 16 * w + col] = 0.f;
-      if (DELTA && col >= i) sh_m[row * LDC + 16 * w + col] = 0.f;
+    for (int e = 0; e < 2; ++e) {
+      const int col = 2 * (lane & 7) + e;
+      if (col > ti) sh_p[row * LDC + blk + col] = 0.f;
+      if (DELTA && col >= ti) sh_m[row * LDC + blk + col] = 0.f;
     }
   }
   __syncthreads();
-  // ---- k a, q a, k b and the blocks' decays: thread (channel, block pair)
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const int c = tid & 127, b = 2 * (tid >> 7) + e;
+  // ---- k a, q a, k b and the blocks' decays: thread (channel, block)
+  {
+    const int c = tid & 127, b = tid >> 7;
     float *pk = sh_k + 16 * b * LDD + c, *pq = sh_q + 16 * b * LDD + c, *pa = sh_a + 16 * b * LDD + c;
     float al[16], x = 1.f;
 #pragma unroll
@@ -481,66 +486,60 @@ __global__ __launch_bounds__(256) void seq_prep_kda_kernel(const SeqArgs A) {
     }
   }
   __syncthreads();
-  // ---- products between blocks, and K and Q with the decays from the chunk's start: wave w has rows 16 w ..
-  {
-    floatx4 qk[3], kk[3];
+  // ---- products between blocks, and K or Q with the decays from the chunk's
+  // start: waves 0 .. 3 take K's rows 16 w .., waves 4 .. 7 Q's
+  const int wt = w & 3;
+  const bool kwave = w < 4;
+  if (DELTA || !kwave) {
+    const float *mine = (kwave ? sh_k : sh_q) + (16 * wt + i) * LDD;
+    uint16_t *to = (kwave ? A.w.K : A.w.Q) + (at_ * 4 + wt) * 4 * 3 * 512;
+    floatx4 acc[3];
 #pragma unroll
-    for (int n = 0; n < 3; ++n) qk[n] = kk[n] = floatx4{0.f, 0.f, 0.f, 0.f};
+    for (int n = 0; n < 3; ++n) acc[n] = floatx4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
     for (int x = 0; x < 4; ++x) {
       const int c0 = 32 * x + 8 * g;
-      float k[8], q[8], m[8], v[8];
-      bf8 fk[3], fq[3], f[3];
-      load8(reinterpret_cast<const F32 *>(sh_k + (16 * w + i) * LDD + c0), k);
-      load8(reinterpret_cast<const F32 *>(sh_q + (16 * w + i) * LDD + c0), q);
+      float k[8], m[8], v[8];
+      bf8 fk[3], f[3];
+      load8(reinterpret_cast<const F32 *>(mine + c0), k);
       split8<3>(k, fk);
-      split8<3>(q, fq);
 #pragma unroll
       for (int e = 0; e < 8; ++e) m[e] = 1.f;  // decays of the blocks between
 #pragma unroll
       for (int n = 2; n >= 0; --n) {
-        if (n >= w) continue;
+        if (n >= wt) continue;
         load8(reinterpret_cast<const F32 *>(sh_a + (16 * n + i) * LDD + c0), v);
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] *= m[e];
         split8<3>(v, f);
-        mma_into<3, 3>(qk[n], fq, f);
-        if (DELTA) mma_into<3, 3>(kk[n], fk, f);
+        mma_into<3, 3>(acc[n], fk, f);
         load8(reinterpret_cast<const F32 *>(&sh_bp[n][c0]), v);
 #pragma unroll
         for (int e = 0; e < 8; ++e) m[e] *= v[e];
       }
-      // m: now the decays of all blocks before w
+      // m: now the decays of all blocks before the wave's
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        k[e] *= m[e];
-        q[e] *= m[e];
-      }
+      for (int e = 0; e < 8; ++e) k[e] *= m[e];
       split8<3>(k, fk);
-      split8<3>(q, fq);
-      if (DELTA) frag_store<3>(A.w.K + ((at_ * 4 + w) * 4 + x) * 3 * 512, fk, lane);
-      frag_store<3>(A.w.Q + ((at_ * 4 + w) * 4 + x) * 3 * 512, fq, lane);
+      frag_store<3>(to + x * 3 * 512, fk, lane);
     }
+    float *const out = kwave ? sh_m : sh_p;
 #pragma unroll
     for (int n = 0; n < 3; ++n) {
-      if (n >= w) continue;
-      const int j = 16 * n + i;
-      const float be = sh_b[j];
+      if (n >= wt) continue;
+      const float be = sh_b[16 * n + i];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int row = 16 * w + 4 * g + r;
-        sh_p[row * LDC + j] = be * qk[n][r];
-        if (DELTA) sh_m[row * LDC + j] = be * kk[n][r];
-      }
+      for (int r = 0; r < 4; ++r) out[(16 * wt + 4 * g + r) * LDC + 16 * n + i] = be * acc[n][r];
     }
     // P's blocks above the diagonal in the steps that are stored: zeros
-    for (int n = w + 1; n < 4; ++n)
-      *reinterpret_cast<float4 *>(sh_p + (16 * w + i) * LDC + 16 * n + 4 * g) = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (!kwave)
+      for (int n = wt + 1; n < 4; ++n)
+        *reinterpret_cast<float4 *>(sh_p + (16 * wt + i) * LDC + 16 * n + 4 * g) = make_float4(0.f, 0.f, 0.f, 0.f);
   }
-  // ---- K^T with beta and the decays to the chunk's end: key rows 32 w .. + 31
+  // ---- K^T with beta and the decays to the chunk's end: key rows 16 w .. + 15
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const int mt = 2 * w + (e >> 1), x = e & 1, c = 16 * mt + i;
+  for (int x = 0; x < 2; ++x) {
+    const int mt = w, c = 16 * mt + i;
     // tokens 32 x + 8 g .. + 7 lie in block 2 x + (g >> 1)
     const float b1 = sh_bp[1][c], b2 = sh_bp[2][c], b3 = sh_bp[3][c];
     const int blk = 2 * x + (g >> 1);
@@ -558,7 +557,7 @@ __global__ __launch_bounds__(256) void seq_prep_kda_kernel(const SeqArgs A) {
   if (tid < D) A.w.dec[at_ * 2 * C + tid] = (sh_bp[0][tid] * sh_bp[1][tid]) * (sh_bp[2][tid] * sh_bp[3][tid]);
   __syncthreads();
   if (DELTA) invert_unit_lower(sh_k, sh_m, w, lane);
-  store_triangles<DELTA>(A, at_, sh_k, sh_p, w, lane);
+  if (kwave) store_triangles<DELTA>(A, at_, sh_k, sh_p, w, lane);
 }
 
 // ---------------------------------------------------------------------------
@@ -857,7 +856,7 @@ hipError_t chunked(const SeqArgs &a, hipStream_t stream) {
   const int64_t units = ((int64_t)a.seqs * a.hv + 7) / 8 * 8;
   const dim3 slots((unsigned)a.slots, a.hv);
   if constexpr (KDA)
-    hipLaunchKernelGGL((seq_prep_kda_kernel<E, DELTA>), slots, dim3(256), 0, stream, a);
+    hipLaunchKernelGGL((seq_prep_kda_kernel<E, DELTA>), slots, dim3(512), 0, stream, a);
   else
     hipLaunchKernelGGL((seq_prep_kernel<E, DELTA, SAVE>), slots, dim3(256), 0, stream, a);
   if (scan_wide(a))
