@@ -14,9 +14,13 @@ constexpr int64_t kMaxTokens = int64_t(1) << 30;
 constexpr int64_t kMaxGrid = int64_t(1) << 23;  // workgroups of a launch: 512 lanes each stay below 2^32
 constexpr int64_t kMaxHeads = 65535;            // second grid dimension
 
-// Sequences of up to this many tokens on average run token by token in one
-// launch; longer ones are taken in chunks (lq_sequence.hip).
-constexpr int64_t kShort = 16;
+// Sequences of few tokens on average run token by token in one launch, longer
+// ones in chunks (lq_sequence.hip).  Measured where the two meet, in tokens a
+// sequence: with operands of one or two parts at 22 (8 sequences x 32 heads),
+// 28 (64 x 32) and 30 (1 x 32); with three parts (fp32, or a decay a channel)
+// at 22 .. 34 for up to 32 states and at 52 .. 64 from 256 states on, where
+// the chunks' operands outweigh the states.
+constexpr int64_t kShort = 24, kShortParts = 56, kManyStates = 256;
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
@@ -120,7 +124,9 @@ int check_sequence(const lq_sequence *sq) {
 }
 
 bool chunked(const lq_sequence *sq, bool save) {
-  return sq->tokens > 0 && (save || sq->tokens > kShort * sq->seqs);
+  const bool three = sq->gate == LQ_GATE_KDA || sq->dtype == LQ_F32;
+  const bool many = int64_t(sq->seqs) * sq->heads_v >= kManyStates;
+  return sq->tokens > 0 && (save || sq->tokens > (three && many ? kShortParts : kShort) * sq->seqs);
 }
 
 // The arrays of lq::SeqSpace, one behind another from `base`; returns the
