@@ -70,8 +70,8 @@ struct NormArgs {
 
 // Columns of the state that a workgroup of the scans takes: 32 halve the
 // reads of the operands that its column blocks share, 16 double the
-// workgroups of a few heads.
-inline bool scan_wide(const SeqArgs &a) { return (int64_t)a.seqs * a.hv * 4 >= 256; }
+// workgroups of a few heads.  Wide once that gives `least` workgroups.
+inline bool scan_wide(const SeqArgs &a, int least) { return (int64_t)a.seqs * a.hv * 4 >= least; }
 
 // dtype: 0 fp32, 1 bf16, 2 fp16
 hipError_t launch_seq_recurrent(const SeqArgs &a, int dtype, bool kda, bool delta, hipStream_t stream);

@@ -183,8 +183,9 @@ __device__ __forceinline__ void invert_unit_lower(float *sh_t, float *sh_m, int 
 }
 
 // T and P as the scan's fragments: rows 16 w + i, columns 32 x + 8 g .. + 7;
-// T's block above the diagonal in a step is not written in sh_t: zeros.
-template <bool DELTA>
+// T's block above the diagonal in a step is not written in sh_t: zeros.  NO: the
+// parts of P that the output takes.
+template <bool DELTA, int NO>
 __device__ __forceinline__ void store_triangles(const SeqArgs &A, size_t at_, const float *sh_t, const float *sh_p, int w,
                                                 int lane) {
   const int i = lane & 15, g = lane >> 4;
@@ -203,8 +204,9 @@ __device__ __forceinline__ void store_triangles(const SeqArgs &A, size_t at_, co
       frag_store<3>(A.w.T + ((at_ * 4 + w) * 2 + x) * 3 * 512, f, lane);
     }
     load8(reinterpret_cast<const F32 *>(sh_p + row * LDC + col), v);
-    split8<3>(v, f);
-    frag_store<3>(A.w.P + ((at_ * 4 + w) * 2 + x) * 3 * 512, f, lane);
+    bf8 fp[NO];
+    split8<NO>(v, fp);
+    frag_store<NO>(A.w.P + ((at_ * 4 + w) * 2 + x) * 3 * 512, fp, lane);
   }
 }
 
@@ -320,7 +322,7 @@ __global__ __launch_bounds__(256) void seq_prep_kernel(const SeqArgs A) {
   }
   __syncthreads();
   if (DELTA) invert_unit_lower(sh_t, sh_m, w, lane);
-  store_triangles<DELTA>(A, at_, sh_t, sh_l, w, lane);
+  store_triangles<DELTA, kOutParts<E>>(A, at_, sh_t, sh_l, w, lane);
   if (!SAVE) return;
   // transposes for the backward scan: columns 16 w + i, rows 32 x + 8 g .. + 7
 #pragma unroll
@@ -557,7 +559,7 @@ __global__ __launch_bounds__(512) void seq_prep_kda_kernel(const SeqArgs A) {
   if (tid < D) A.w.dec[at_ * 2 * C + tid] = (sh_bp[0][tid] * sh_bp[1][tid]) * (sh_bp[2][tid] * sh_bp[3][tid]);
   __syncthreads();
   if (DELTA) invert_unit_lower(sh_k, sh_m, w, lane);
-  if (kwave) store_triangles<DELTA>(A, at_, sh_k, sh_p, w, lane);
+  if (kwave) store_triangles<DELTA, kOutParts<E>>(A, at_, sh_k, sh_p, w, lane);
 }
 
 // ---------------------------------------------------------------------------
@@ -579,7 +581,7 @@ __global__ __launch_bounds__(512) void seq_prep_kda_kernel(const SeqArgs A) {
 // ---------------------------------------------------------------------------
 template <class E, bool KDA, bool DELTA, bool SAVE, int CB>
 __global__ __launch_bounds__(256) void seq_scan_kernel(const SeqArgs A) {
-  constexpr int NT = CB / 16, kBlocks = D / CB, NO = Parts<E>::n == 3 ? 3 : 2;
+  constexpr int NT = CB / 16, kBlocks = D / CB, NO = kOutParts<E>;
   // parts of K and K^T, and of Q; with a decay a channel they hold decays, per value head
   constexpr int NP = KDA ? 3 : Parts<E>::n, NQ = KDA ? NO : NP;
   constexpr int FS = 4 * NT, FX = 2 * NT;  // fragments of a part of [CB][128], [CB][64]
@@ -802,14 +804,18 @@ __global__ __launch_bounds__(256) void seq_scan_kernel(const SeqArgs A) {
         for (int r = 0; r < 4; ++r) s[m][n][r] = fmaf(s[m][n][r], la[m][r], d[r]);
       }
     E *o = at<E>(A.o, t0 + tok, hv) + col;
+    E x[4][NT];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      if (tok + r < len) {
-        E x[NT];
+    for (int r = 0; r < 4; ++r)
 #pragma unroll
-        for (int n = 0; n < NT; ++n) x[n] = from_f<E>(yq[n].a[r] + yq[n].b[r]);
-        store_raw<NT>(o + r * A.o.ts, x);
-      }
+      for (int n = 0; n < NT; ++n) x[r][n] = from_f<E>(yq[n].a[r] + yq[n].b[r]);
+    if (len >= C) {  // a whole chunk: no branch for every row
+#pragma unroll
+      for (int r = 0; r < 4; ++r) store_raw<NT>(o + r * A.o.ts, x[r]);
+    } else {
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (tok + r < len) store_raw<NT>(o + r * A.o.ts, x[r]);
     }
   }
   if (A.S) {
@@ -861,7 +867,9 @@ hipError_t chunked(const SeqArgs &a, hipStream_t stream) {
     hipLaunchKernelGGL((seq_prep_kda_kernel<E, DELTA>), slots, dim3(512), 0, stream, a);
   else
     hipLaunchKernelGGL((seq_prep_kernel<E, DELTA, SAVE>), slots, dim3(256), 0, stream, a);
-  if (scan_wide(a))
+  // (prompt of 4,096 tokens x 32 heads, 128 wide or 256 narrow workgroups: 197
+  // and 148 us; 16,384 ragged tokens x 32 heads, 3,072 or 6,144: 385 and 574)
+  if (scan_wide(a, 256))
     hipLaunchKernelGGL((seq_scan_kernel<E, KDA, DELTA, SAVE, 32>), dim3((unsigned)(units * 4)), dim3(256), 0, stream, a);
   else
     hipLaunchKernelGGL((seq_scan_kernel<E, KDA, DELTA, SAVE, 16>), dim3((unsigned)(units * 8)), dim3(256), 0, stream, a);

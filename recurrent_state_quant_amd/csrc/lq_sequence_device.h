@@ -273,6 +273,10 @@ template <> struct Parts<BF16> { static constexpr int n = 1; };
 template <> struct Parts<F16> { static constexpr int n = 2; };
 template <> struct Parts<F32> { static constexpr int n = 3; };
 
+// Parts that a result of type E can hold of its operands: what is rounded at
+// 2^-9 or 2^-12 takes no parts below 2^-16.
+template <class E> constexpr int kOutParts = Parts<E>::n == 3 ? 3 : 2;
+
 __device__ __forceinline__ uint32_t pair_bf16(float x, float y) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector((fl2){x, y}, bf2));
 }

@@ -38,7 +38,6 @@ __global__ __launch_bounds__(512) void seq_rscan_kernel(const SeqArgs A) {
   const int64_t b = blockIdx.x;  // column blocks of a head on one XCD, as in the forward scan
   const int64_t unit = (b / (8 * kBlocks)) * 8 + (b & 7);
   if (unit >= (int64_t)A.seqs * A.hv) return;
-  const int col0 = (int)((b >> 3) % kBlocks) * CB;
   const int seq = (int)(unit / A.hv), hv = (int)(unit % A.hv), hk = hv / A.group;
   const int start = seq_start(A, seq), end = seq_end(A, seq, start);
   __shared__ __align__(16) uint16_t sh_g[3 * FS * 512];               // G, [column][key row]
@@ -48,26 +47,29 @@ __global__ __launch_bounds__(512) void seq_rscan_kernel(const SeqArgs A) {
   __shared__ __align__(16) uint16_t sh_x[DELTA ? 3 * FX * 512 : 8];   // -Gam * dX
   __shared__ floatx4 sh_pd[4 * NT * 64];                              // P^T dO, as the accumulators hold it
   const int i = lane & 15, g = lane >> 4, tok = 16 * wt + 4 * g;
+  const int col = (int)((b >> 3) % kBlocks) * CB + NT * i;  // the lane's first column
 
   floatx4 s[NT];
 #pragma unroll
-  for (int n = 0; n < NT; ++n)
+  for (int r = 0; r < 4; ++r) {
+    float x[NT] = {};
+    if (A.dS) load_n<NT>(A.dS + (unit * D + 16 * w + 4 * g + r) * D + col, x);
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
-      s[n][r] = A.dS ? A.dS[(unit * D + 16 * w + 4 * g + r) * D + col0 + 16 * n + i] : 0.f;
+    for (int n = 0; n < NT; ++n) s[n][r] = x[n];
+  }
   wait_loads();  // the loop below counts its own loads only
 
   // Loads as in the forward scan: at fixed places in the code, a row past the
   // end replaced by the chunk's first; dO is zero there, and so are its rows
   // of P^T and T^T and its columns of Q^T and K^T.  Pointers move back a chunk.
   bf8 fA[4][NP], fB[2][3], fQT[2][NP], fKT[2][NP];  // K; T^T or P^T
-  E raw[NT][4] = {};
+  E raw[4][NT] = {};
   float cur[NT][4], last;
   float4 gam, kap;
   const int slot0 = start / C + seq;
   const int chunks = (end - start + C - 1) / C;
   const int tl = start + (chunks - 1) * C;  // the last chunk's first token
-  const E *pO = at<const E>(A.go, tl + tok, hv) + col0 + i;
+  const E *pO = at<const E>(A.go, tl + tok, hv) + col;
   const int64_t backO = tok * A.go.ts;
   auto load_A = [&](int c) {
     if (kwave) {
@@ -81,11 +83,7 @@ __global__ __launch_bounds__(512) void seq_rscan_kernel(const SeqArgs A) {
     if (!kwave) {
       pO -= move * (C * A.go.ts);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const E *p = tok + r < len ? pO + r * A.go.ts : pO - backO;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) raw[n][r] = p[16 * n];
-      }
+      for (int r = 0; r < 4; ++r) load_raw<NT>(tok + r < len ? pO + r * A.go.ts : pO - backO, raw[r]);
     }
   };
   auto load_dec = [&](int c) {
@@ -114,7 +112,7 @@ __global__ __launch_bounds__(512) void seq_rscan_kernel(const SeqArgs A) {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
-      for (int r = 0; r < 4; ++r) cur[n][r] = tok + r < len ? to_f(raw[n][r]) : 0.f;
+      for (int r = 0; r < 4; ++r) cur[n][r] = tok + r < len ? to_f(raw[r][n]) : 0.f;
       frag_share<NP, FX>(sh_o, 2 * n + (wt >> 1), wt & 1, lane, cur[n][0], cur[n][1], cur[n][2], cur[n][3]);
     }
   };
@@ -157,8 +155,13 @@ __global__ __launch_bounds__(512) void seq_rscan_kernel(const SeqArgs A) {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       frag_share<3, FS>(sh_g, 4 * n + (w >> 1), w & 1, lane, s[n][0], s[n][1], s[n][2], s[n][3]);
+    }
 #pragma unroll
-      for (int r = 0; r < 4; ++r) A.w.G[(at_ * D + 16 * w + 4 * g + r) * D + col0 + 16 * n + i] = s[n][r];
+    for (int r = 0; r < 4; ++r) {
+      float x[NT];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) x[n] = s[n][r];
+      store_n<NT>(A.w.G + (at_ * D + 16 * w + 4 * g + r) * D + col, x);
     }
     lds_barrier();
     const float gm[4] = {gam.x, gam.y, gam.z, gam.w}, kp[4] = {kap.x, kap.y, kap.z, kap.w};
@@ -217,13 +220,6 @@ __global__ __launch_bounds__(512) void seq_rscan_kernel(const SeqArgs A) {
                             -gm[3] * u[n][3]);
         }
       }
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          A.w.X[(at_ * C + tok + r) * D + col0 + 16 * n + i] = u[n][r];
-          if (tok + r < len) at<E>(A.dv, t0 + tok + r, hv)[col0 + 16 * n + i] = from_f<E>(u[n][r]);
-        }
     } else {
       product_do();
     }
@@ -244,15 +240,40 @@ __global__ __launch_bounds__(512) void seq_rscan_kernel(const SeqArgs A) {
           mma_parts<NP, 3>(ds[n], fKT[x], fx);
         }
       }
+    load_QK(next);
+    if (kwave) {  // dX's and dV's stores, behind the products
+      E *out = at<E>(A.dv, t0 + tok, hv) + col;
+      E o[4][NT];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        float x[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          x[n] = u[n][r];
+          o[r][n] = from_f<E>(x[n]);
+        }
+        store_n<NT>(A.w.X + (at_ * C + tok + r) * D + col, x);
+      }
+      if (len >= C) {  // a whole chunk: no branch for every row
+#pragma unroll
+        for (int r = 0; r < 4; ++r) store_raw<NT>(out + r * A.dv.ts, o[r]);
+      } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (tok + r < len) store_raw<NT>(out + r * A.dv.ts, o[r]);
+      }
+    }
 #pragma unroll
     for (int n = 0; n < NT; ++n) s[n] = s[n] * la + ds[n].sum();
-    load_QK(next);
   }
   if (A.dS0) {
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int r = 0; r < 4; ++r) {
+      float x[NT];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) A.dS0[(unit * D + 16 * w + 4 * g + r) * D + col0 + 16 * n + i] = s[n][r];
+      for (int n = 0; n < NT; ++n) x[n] = s[n][r];
+      store_n<NT>(A.dS0 + (unit * D + 16 * w + 4 * g + r) * D + col, x);
+    }
   }
 }
 
@@ -304,7 +325,7 @@ __device__ __forceinline__ void tile_load(Row4<E> &f, float *lds, const E *p, in
 template <class E, bool DELTA>
 __global__ __launch_bounds__(512) void seq_grad_kernel(const SeqArgs A) {
   // parts of E1 and E2: what dQ and dK can hold of them
-  constexpr int NP = Parts<E>::n, NE = NP == 3 ? 3 : 2;
+  constexpr int NP = Parts<E>::n, NE = kOutParts<E>;
   const int slot = blockIdx.x, hk = blockIdx.y;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const Chunk ch = find_chunk(A, slot, threadIdx.x & 63);
@@ -688,7 +709,9 @@ __global__ __launch_bounds__(512) void seq_grad_kernel(const SeqArgs A) {
 template <class E, bool DELTA>
 hipError_t backward(const SeqArgs &a, hipStream_t stream) {
   const int64_t units = ((int64_t)a.seqs * a.hv + 7) / 8 * 8;
-  if (scan_wide(a))
+  // (both scans of 8,192 tokens x 16 heads, 256 wide or 512 narrow workgroups:
+  // forward 234 and 257 us, backward 290 and 275)
+  if (scan_wide(a, 512))
     hipLaunchKernelGGL((seq_rscan_kernel<E, DELTA, 32>), dim3((unsigned)(units * 4)), dim3(512), 0, stream, a);
   else
     hipLaunchKernelGGL((seq_rscan_kernel<E, DELTA, 16>), dim3((unsigned)(units * 8)), dim3(512), 0, stream, a);
