@@ -183,7 +183,7 @@ const char *leapquant_status_string(int status) {
     case LQ_OK: return "ok";
     case LQ_ERR_NULL: return "a required pointer is NULL";
     case LQ_ERR_SHAPE: return "invalid size or parameter (n, p, r, gate, flags, t or len)";
-    case LQ_ERR_UNSUPPORTED: return "unsupported head size (dk and dv must be 128)";
+    case LQ_ERR_UNSUPPORTED: return "unsupported head size (dk and dv must be 128), or no gradient for this gate";
     case LQ_ERR_ALIGN: return "pointer is not aligned as required";
     case LQ_ERR_ALIAS: return "an output overlaps an input, or two arrays of the state overlap";
     case LQ_ERR_HIP: return "HIP kernel launch failed";

@@ -11,7 +11,7 @@ namespace {
 
 constexpr int64_t kDim = 128, kState = kDim * kDim;
 constexpr int64_t kMaxTokens = int64_t(1) << 30;
-constexpr int64_t kMaxGrid = int64_t(1) << 23;  // workgroups of a launch: 512 lanes each stay below 2^32
+constexpr int64_t kMaxGrid = (int64_t(1) << 23) - 1;  // workgroups of a launch: 512 lanes each stay below 2^32
 constexpr int64_t kMaxHeads = 65535;            // second grid dimension
 
 // Sequences of few tokens on average run token by token in one launch, longer

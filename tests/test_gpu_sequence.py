@@ -478,3 +478,115 @@ def test_training_chain():
     for got, want, more, name in ((dqr, ref[0], 0, "q"), (dkr, ref[1], 0, "k"), (dwq, ref[2], T * hk, "wq"),
                                   (dwk, ref[3], T * hk, "wk")):
         R.check(got, want, n + more, name)
+
+
+@pytest.mark.parametrize("gate", ["gdn", "kda"])
+def test_long_sequence(gate):
+    """Thousands of tokens from a state: errors do not pile up beyond the bound (reference on the GPU, 64 bits)."""
+    T, hk, hv = 2500, 1, 2
+    cu, x = make([T], hk, hv, F32, gate, seed=90, shift=4.0)
+    _, _, o, S = forward(cu, x, hk, hv, gate)
+    names = ("q", "k", "v", "beta", "alpha", "S0")
+    ro, rS = R.recurrence(cu, *[x[m].double().to(DEV) for m in names])
+    check_forward(cu, x, o, S, (ro, rS))
+
+
+def test_long_backward():
+    T, hk, hv = 1000, 1, 2
+    cu, x = make([T], hk, hv, F32, seed=91, shift=4.0)
+    g = torch.Generator().manual_seed(92)
+    do, dS = torch.randn(x["v"].shape, generator=g), torch.randn(x["S0"].shape, generator=g)
+    plan, d, _, _ = forward(cu, x, hk, hv, save=True)
+    got = backward(plan, cu, d, do.to(DEV), dS.to(DEV))
+    leaves = [x[m].double().to(DEV).requires_grad_(True) for m in GRADS]
+    o, S = R.recurrence(cu, *leaves)
+    ref = torch.autograd.grad((o * do.double().to(DEV)).sum() + (S * dS.double().to(DEV)).sum(), leaves)
+    check_backward(cu, got, ref)
+
+
+@pytest.mark.parametrize("lengths", [[70], [2, 3]])
+def test_offsets_past_32_bits(lengths):
+    """v and o with tokens 2^26 elements apart: offsets of more than 2^32 bytes."""
+    T, step = sum(lengths), 1 << 26
+    cu, x = make(lengths, 1, 1, BF16, seed=93)
+    far = torch.empty(T * step, dtype=BF16, device=DEV)
+    v, o = (far.as_strided((T, 1, 128), (step, 128, 1), at) for at in (0, 1024))
+    v.copy_(x["v"])
+    plan = lq.LeapQuantSequence(T, len(lengths), 1, 1, device=DEV)
+    d = {m: y.to(DEV) for m, y in x.items()}
+    S = torch.empty_like(d["S0"])
+    lq.leapquant_sequence_forward(plan, offsets(cu), d["q"], d["k"], v, d["beta"], d["alpha"], o, S0=d["S0"], S=S)
+    check_forward(cu, x, o, S, reference(cu, x))
+
+
+@pytest.mark.parametrize("gate", ["gdn", "kda"])
+@pytest.mark.parametrize("lengths", [[80, 7], [5, 4]])
+def test_head_major_arrays(gate, lengths):
+    """[heads, tokens, 128] arrays, seen as [tokens, heads, 128]."""
+    hk, hv, T = 2, 4, sum(lengths)
+    cu, x = make(lengths, hk, hv, F16, gate, seed=94)
+    turn = lambda t: t.to(DEV).transpose(0, 1).contiguous().transpose(0, 1)  # noqa: E731
+    d = {m: (y.to(DEV) if m == "S0" else turn(y)) for m, y in x.items()}
+    plan = lq.LeapQuantSequence(T, 2, hk, hv, gate, F16, DEV)
+    o, S = turn(torch.full((T, hv, 128), 7.0, dtype=F16)), torch.empty_like(d["S0"])
+    lq.leapquant_sequence_forward(plan, offsets(cu), *[d[m] for m in ("q", "k", "v", "beta", "alpha")], o, S0=d["S0"],
+                                  S=S)
+    check_forward(cu, x, o, S, reference(cu, x))
+
+
+def test_one_plan_for_calls_of_many_sizes():
+    """A plan's workspace serves every smaller call, whichever form it takes."""
+    plan = lq.LeapQuantSequence(300, 40, 1, 2, dtype=F32, device=DEV)
+    for i, lengths in enumerate(([300], [1] * 40, [7] * 40, [30] * 10, [25], [24], [0, 25, 0], [150, 150], [26] * 11)):
+        cu, x = make(lengths, 1, 2, F32, seed=100 + i)
+        _, _, o, S = forward(cu, x, 1, 2, plan=plan)
+        check_forward(cu, x, o, S, reference(cu, x))
+
+
+def test_many_value_heads_for_a_key_head():
+    cu, x = make([66, 30], 1, 8, BF16, seed=110)
+    do = torch.randn(x["v"].shape, generator=torch.Generator().manual_seed(111)).to(BF16)
+    plan, d, o, S = forward(cu, x, 1, 8, save=True)
+    ref = reference(cu, x, grads=(do, None))
+    check_forward(cu, x, o, S, ref[:2])
+    check_backward(cu, backward(plan, cu, d, do.to(DEV)), ref[2:])
+
+
+def test_gradients_of_values_that_are_not_finite_stay_in_their_sequence():
+    cu, x = make([70, 5, 90], 1, 2, F32, seed=112)
+    do = torch.randn(x["v"].shape, generator=torch.Generator().manual_seed(113)).to(DEV)
+    runs = []
+    for bad in (False, True):
+        if bad:
+            x["v"][71] = float("nan")
+        plan, d, _, _ = forward(cu, x, 1, 2, save=True)
+        y = do.clone()
+        if bad:
+            y[73] = float("inf")
+        runs.append(backward(plan, cu, d, y))
+    keep = torch.ones(165, dtype=torch.bool)
+    keep[70:75] = False
+    for m in GRADS[:5]:
+        assert torch.equal(runs[0][m][keep], runs[1][m][keep]), m
+    assert torch.equal(runs[0]["S0"][:2], runs[1]["S0"][:2]) and torch.equal(runs[0]["S0"][4:], runs[1]["S0"][4:])
+
+
+def test_refusals_on_the_device():
+    plan = lq.LeapQuantSequence(10, 2, 2, 4, dtype=F32, device=DEV)
+    z = lambda *s: torch.zeros(s, device=DEV)  # noqa: E731
+    q, v, b, cu = z(10, 2, 128), z(10, 4, 128), z(10, 4), offsets([0, 4, 10])
+    ok = dict(cu_seqlens=cu, q=q, k=q, v=v, beta=b, alpha=b, o=z(10, 4, 128))
+    lq.leapquant_sequence_forward(plan, **ok)
+    bad = [dict(cu_seqlens=cu.long()), dict(cu_seqlens=cu.cpu()), dict(q=z(10, 2, 64)), dict(k=z(9, 2, 128)),
+           dict(v=v.half()), dict(alpha=z(10, 4, 128)), dict(beta=z(10, 2)), dict(o=z(10, 4, 128).cpu()),
+           dict(q=z(10, 128, 2).transpose(1, 2)), dict(S=z(3, 128, 128)), dict(S0=z(8, 128, 128).double()),
+           dict(cu_seqlens=offsets([0, 1, 2, 10])), dict(q=z(11, 2, 128))]
+    for kw in bad:
+        with pytest.raises(ValueError):
+            lq.leapquant_sequence_forward(plan, **{**ok, **kw})
+    with pytest.raises(lq.LeapQuantError):
+        lq.leapquant_sequence_forward(plan, **{**ok, "o": v})
+    S = z(8 * 128 * 128 + 64)
+    with pytest.raises(lq.LeapQuantError):  # states that overlap in part
+        lq.leapquant_sequence_forward(plan, **ok, S0=S[:8 * 128 * 128].view(8, 128, 128),
+                                      S=S[64:].view(8, 128, 128))
