@@ -47,10 +47,15 @@ __global__ __launch_bounds__(256) void seq_recurrent_kernel(const SeqArgs A) {
 
   float s[16][CC];
 #pragma unroll
-  for (int i = 0; i < 16; ++i)
-#pragma unroll
-    for (int c = 0; c < CC; ++c)
-      s[i][c] = A.S0 ? A.S0[(unit * D + row0 + i) * D + col0 + c] : 0.f;
+  for (int i = 0; i < 16; ++i) {
+    const float *p = A.S0 + (unit * D + row0 + i) * D + col0;
+    if constexpr (CC == 4) {  // states pass once: streaming accesses
+      const float4 x = A.S0 ? ld4(p) : make_float4(0.f, 0.f, 0.f, 0.f);
+      s[i][0] = x.x; s[i][1] = x.y; s[i][2] = x.z; s[i][3] = x.w;
+    } else {
+      s[i][0] = A.S0 ? *p : 0.f;
+    }
+  }
 
   float k[16], q[16], a[KDA ? 16 : 1], v[CC], b = 0.f;
   auto fetch = [&](int t) {
@@ -121,9 +126,13 @@ __global__ __launch_bounds__(256) void seq_recurrent_kernel(const SeqArgs A) {
   }
   if (A.S) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-#pragma unroll
-      for (int c = 0; c < CC; ++c) A.S[(unit * D + row0 + i) * D + col0 + c] = s[i][c];
+    for (int i = 0; i < 16; ++i) {
+      float *p = A.S + (unit * D + row0 + i) * D + col0;
+      if constexpr (CC == 4)
+        st4(p, make_float4(s[i][0], s[i][1], s[i][2], s[i][3]));
+      else
+        *p = s[i][0];
+    }
   }
 }
 

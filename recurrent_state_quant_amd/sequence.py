@@ -40,11 +40,11 @@ def _launch(fn, device, stream, *args):
     """The call on its device, with the stream's handle as the last argument."""
     if device.type != "cuda":
         raise ValueError("the call's tensors must be in device memory")
-    handle = _stream(stream, device)
     if torch.cuda.current_device() == device.index:
+        handle = _stream(stream, device) if stream is not None else torch.cuda.current_stream().cuda_stream
         return L.check(fn(*args, handle))
     with torch.cuda.device(device):
-        L.check(fn(*args, handle))
+        L.check(fn(*args, _stream(stream, device)))
 
 
 def _states(x, n, name, device):
