@@ -104,12 +104,14 @@ __device__ __forceinline__ void load_n(const float *p, float (&x)[N]) {
     x[1] = a.y;
   }
 }
+// (streaming stores: what the scans keep for the backward pass outgrows the
+// caches; the reverse scan of 5,000 tokens x 16 heads 144 -> 130 us)
 template <int N>
 __device__ __forceinline__ void store_n(float *p, const float (&x)[N]) {
   if constexpr (N == 1)
-    p[0] = x[0];
+    __builtin_nontemporal_store(x[0], p);
   else
-    *reinterpret_cast<float2 *>(p) = make_float2(x[0], x[1]);
+    __builtin_nontemporal_store(vf2{x[0], x[1]}, reinterpret_cast<vf2 *>(p));
 }
 // four values at p (aligned to four elements)
 __device__ __forceinline__ void load4(const F32 *p, float (&x)[4]) {

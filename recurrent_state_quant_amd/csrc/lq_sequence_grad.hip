@@ -715,6 +715,7 @@ hipError_t backward(const SeqArgs &a, hipStream_t stream) {
     hipLaunchKernelGGL((seq_rscan_kernel<E, DELTA, 32>), dim3((unsigned)(units * 4)), dim3(512), 0, stream, a);
   else
     hipLaunchKernelGGL((seq_rscan_kernel<E, DELTA, 16>), dim3((unsigned)(units * 8)), dim3(512), 0, stream, a);
+  if (a.tokens == 0) return hipGetLastError();  // (then there is no workspace either)
   hipLaunchKernelGGL((seq_grad_kernel<E, DELTA>), dim3((unsigned)a.slots, a.hk), dim3(512), 0, stream, a);
   return hipGetLastError();
 }
