@@ -356,6 +356,11 @@ int leapquant_bf16w_window_close(const lq_params *prm, void *B, const lq_state *
  * S0 and S, [seqs * heads_v][dk][dv], the layout of leapquant_quantize_state.
  * q and k are used as given (unit-norm keys keep the recurrence stable; the
  * decode calls expect the same), with no scale.
+ * Values are finite, below 2^127, and decays from 0 to 1 (both inclusive).
+ * 64 tokens of a sequence may be computed together: a value that is not
+ * finite reaches the outputs of tokens at and behind it, as the formulas say,
+ * and may reach those of up to 63 tokens before it; never another sequence
+ * nor, in the forward pass, another head's states.
  * ------------------------------------------------------------------------- */
 
 typedef enum lq_dtype {
@@ -379,7 +384,7 @@ typedef struct lq_rows {
 } lq_rows;
 
 typedef struct lq_sequence {
-  int64_t tokens;  /* rows of the token arrays, 0 .. 2^30                      */
+  int64_t tokens;  /* rows of the token arrays, >= 0, below about 2^29        */
   int32_t seqs;    /* sequences, >= 1                                         */
   int32_t heads_k; /* query and key heads, >= 1                               */
   int32_t heads_v; /* value heads, a multiple of heads_k                      */
@@ -405,7 +410,7 @@ int64_t leapquant_sequence_workspace(const lq_sequence *sq, int32_t save);
  * Sums and states are fp32; o is rounded once.  With save != 0 the workspace
  * afterwards holds what leapquant_sequence_backward reads.
  *   LQ_ERR_SHAPE also: workspace_bytes too small, an output whose elements
- *   coincide, more heads or sequences than a launch takes;
+ *   coincide, more tokens, heads or sequences than a launch takes;
  *   LQ_ERR_UNSUPPORTED also: save with LQ_GATE_KDA. */
 int leapquant_sequence_forward(const lq_sequence *sq, const int32_t *cu_seqlens,
                                const lq_rows *q, const lq_rows *k, const lq_rows *v,
@@ -436,7 +441,8 @@ int leapquant_sequence_backward(const lq_sequence *sq, const int32_t *cu_seqlens
  * with w the weight of 128 values (NULL: ones), s = q_scale for queries and 1
  * for keys, and R the rotation of the first rot values in pairs (c, c + rot / 2),
  * or (2c, 2c + 1) with interleaved, by the angle positions[t] * inv_freq[c],
- * whose product is taken in 64 bits.
+ * whose product is taken in 64 bits.  Sums of squares are fp32: values below
+ * 2^60.
  * ------------------------------------------------------------------------- */
 
 typedef enum lq_norm_kind {
@@ -445,7 +451,7 @@ typedef enum lq_norm_kind {
 } lq_norm_kind;
 
 typedef struct lq_head_norm {
-  int64_t tokens;      /* 0 .. 2^30                                            */
+  int64_t tokens;      /* >= 0; times runs of 16 heads below 2^25              */
   int32_t heads_q;     /* query heads, >= 0                                    */
   int32_t heads_k;     /* key heads, >= 0; at least one head in all            */
   int32_t dim;         /* must be 128                                          */

@@ -3,20 +3,23 @@
 //   u_t = v_t - S_{t-1}^T b_t,  S_t = D_t S_{t-1} + k~_t u_t^T,  o_t = S_t^T q_t
 //
 // Two forms:
-//   recurrent  token by token, the state in registers: every gate, any
-//              length; one launch, so it also serves a few tokens per
-//              sequence.
-//   chunked    64 tokens at a time on the matrix path (scalar gate).  With
+//   recurrent  token by token, the state in registers, one launch: for few
+//              tokens a sequence, where reading and writing the states is
+//              the work.
+//   chunked    64 tokens at a time on the matrix path.  With a scalar gate,
 //              the decays L_ij = alpha_{j+1} .. alpha_i, G_i = alpha_1 ..
 //              alpha_i and kappa_j = L_Cj beta_j of a chunk that starts at
 //              state S0,
 //                (I + M) U = V - G * (K S0),   M_ij = L_ij beta_j k_i.k_j  (j < i)
 //                O = G * (Q S0) + P U,         P_ij = L_ij beta_j q_i.k_j  (j <= i)
 //                S_C = G_C S0 + (kappa * K)^T U
+//              (a decay for every key channel: at the prep kernel for it)
 //              in two launches: prep (T = (I + M)^-1 and P of every chunk, in
 //              parallel) and scan (U, O and S from chunk to chunk; the columns
 //              of S are independent, so a head's scan is spread over
 //              workgroups by columns).
+// Every decay is a running product: no logarithm and no quotient, so alpha = 0
+// (a state forgotten within a chunk) is exact.
 #include "lq_sequence_device.h"
 
 namespace lq {
@@ -27,6 +30,9 @@ namespace lq {
 // 16 rg .. 16 rg + 15 of CC columns.  Per token it needs S^T (D k) and S^T (D q)
 // from the same S_{t-1} (o_t = S_{t-1}^T (D q) + (k~.q) u_t), so both sums are
 // taken in one pass and reduced over the 8 row groups by DPP.
+// With few tokens bound by the states' bytes: 201 tokens in 64 sequences x 32
+// heads 52 us, 5.2 TB/s.  With many, by a token's chain (about 0.4 us), for
+// which the chunked form is there.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ float row8_sum(float x) {
   x += dpp<0xB1>(x);   // quad_perm [1,0,3,2]
@@ -222,9 +228,13 @@ __device__ __forceinline__ void store_triangles(const SeqArgs &A, size_t at_, co
 // ---------------------------------------------------------------------------
 // Prep: one workgroup per (slot, value head).  Writes, in the order in which
 // the scans load them (matrix fragments, bf16 parts): T, P, and, for the first
-// value head of a key head, K, Q and K^T; with SAVE also the transposes of T, P and Q for the backward scan.  M and T are fp32; T by blocks of 16: each diagonal block by forward
-// substitution (a column per lane), then 16 -> 32 -> 64 by T_ba = -T_b (M_ba
-// T_a) on the fp32 matrix path.
+// value head of a key head, K, Q and K^T; with SAVE also the transposes of T,
+// P and Q for the backward scan.  M and T are fp32 (T's rounding enters every
+// later chunk).  Four waves, a tile of 16 rows of M and P each.
+// 4,096 tokens x 32 heads (2,048 workgroups) 52 us; with SAVE and 16 heads and
+// 8,192 tokens 64 us.  Bound by the latency of a workgroup's steps (load, decays,
+// products, the inverse's five barriers), which the workgroups that share a CU
+// hide from one another in part.
 // ---------------------------------------------------------------------------
 template <class E, bool DELTA, bool SAVE>
 __global__ __launch_bounds__(256) void seq_prep_kernel(const SeqArgs A) {
@@ -381,6 +391,9 @@ __global__ __launch_bounds__(256) void seq_prep_kernel(const SeqArgs A) {
 // are matrix products of factors that are all at most 1 (for alpha <= 1), and
 // inside a block the sums are taken directly, the decay running from token to
 // token (a lane has a token and 16 channels).  Decays of zero are exact.
+// Eight waves, as LDS leaves room for one workgroup a CU (217 us with four):
+// 3,001 tokens x 32 heads in fp32 155 us, of which the direct sums are the
+// larger part.
 // ---------------------------------------------------------------------------
 template <class E, bool DELTA>
 __global__ __launch_bounds__(512) void seq_prep_kda_kernel(const SeqArgs A) {
@@ -585,8 +598,12 @@ __global__ __launch_bounds__(512) void seq_prep_kda_kernel(const SeqArgs A) {
 // behind the rest of the chunk.  What the waves share (S, X, U) goes through
 // LDS as bf16 parts; three barriers a chunk.
 // The output's products take the parts that its type can hold: o in 16 bits
-// is rounded at 2^-9 or 2^-12, so parts below 2^-16 are left out of Q S and
-// P U there (never out of U and S).
+// is rounded by up to 2^-8 or 2^-11, so parts below 2^-16 are left out of Q S
+// and P U there (never out of U and S).
+// Bound by the chain of a chunk (K S, T X, K^T U and the barriers between), 1.9
+// us with 16 columns: a prompt of 4,096 tokens x 32 heads 123 us; 16,384 tokens
+// in 24 sequences x 32 heads, where workgroups share the CUs, 327 to 388 us.
+// Eight waves, four of them for the output, were no faster (142 us).
 // ---------------------------------------------------------------------------
 template <class E, bool KDA, bool DELTA, bool SAVE, int CB>
 __global__ __launch_bounds__(256) void seq_scan_kernel(const SeqArgs A) {
@@ -876,8 +893,9 @@ hipError_t chunked(const SeqArgs &a, hipStream_t stream) {
     hipLaunchKernelGGL((seq_prep_kda_kernel<E, DELTA>), slots, dim3(512), 0, stream, a);
   else
     hipLaunchKernelGGL((seq_prep_kernel<E, DELTA, SAVE>), slots, dim3(256), 0, stream, a);
-  // (prompt of 4,096 tokens x 32 heads, 128 wide or 256 narrow workgroups: 197
-  // and 148 us; 16,384 ragged tokens x 32 heads, 3,072 or 6,144: 385 and 574)
+  // (wide and narrow: a prompt of 4,096 tokens x 32 heads, 128 or 256
+  // workgroups, 197 and 148 us; 24 ragged sequences x 32 heads, many times
+  // what the chip holds, 385 and 574)
   if (scan_wide(a, 256))
     hipLaunchKernelGGL((seq_scan_kernel<E, KDA, DELTA, SAVE, 32>), dim3((unsigned)(units * 4)), dim3(256), 0, stream, a);
   else

@@ -1,6 +1,6 @@
 // Device-side helpers shared by the sequence kernels (lq_sequence.hip,
 // lq_sequence_grad.hip): element types, chunk lookup, decays of a chunk, and
-// fp32 matrix tiles out of LDS.
+// matrix fragments in fp32 and in bf16 parts.
 #pragma once
 #include "lq_device.h"
 #include "lq_sequence.h"
@@ -105,7 +105,7 @@ __device__ __forceinline__ void load_n(const float *p, float (&x)[N]) {
   }
 }
 // (streaming stores: what the scans keep for the backward pass outgrows the
-// caches; the reverse scan of 5,000 tokens x 16 heads 144 -> 130 us)
+// caches; the reverse scan of 5,000 tokens x 16 heads 130 us, 144 without)
 template <int N>
 __device__ __forceinline__ void store_n(float *p, const float (&x)[N]) {
   if constexpr (N == 1)
@@ -182,31 +182,6 @@ __device__ __forceinline__ Chunk find_chunk(const SeqArgs &A, int slot, int lane
   return Chunk{t0, len < 0 ? 0 : (len > C ? C : len)};
 }
 
-// rows t0 .. t0 + 63 of head h as fp32 into lds [64][LDD], zeros past len;
-// 256 threads
-template <class E>
-__device__ __forceinline__ void stage_rows(float *lds, const Rows &r, int h, int t0, int len, int tid) {
-  const int row = tid >> 2, c0 = (tid & 3) * 8;
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (row < len) load8(at<const E>(r, t0 + row, h) + c0 + 32 * c, x);
-    float4 *d = reinterpret_cast<float4 *>(lds + row * LDD + c0 + 32 * c);
-    d[0] = make_float4(x[0], x[1], x[2], x[3]);
-    d[1] = make_float4(x[4], x[5], x[6], x[7]);
-  }
-}
-
-// a dense fp32 [rows][cols] block into lds rows of ld; 256 threads
-template <int COLS>
-__device__ __forceinline__ void stage_f32(float *lds, int ld, const float *src, int rows, int tid) {
-  constexpr int Q = COLS / 4;
-  for (int e = tid; e < rows * Q; e += 256) {
-    const int r = e / Q, c = e % Q;
-    *reinterpret_cast<float4 *>(lds + r * ld + 4 * c) = reinterpret_cast<const float4 *>(src)[e];
-  }
-}
-
 // Operand of a 16x16 tile of v_mfma_f32_16x16x4_f32 for sixteen steps of the
 // contraction: lane (i = lane & 15, g = lane >> 4) holds row (or column) r0 +
 // i at contraction indexes 16 kk + 4 g .. + 3.  The order of the contraction
@@ -226,15 +201,6 @@ __device__ __forceinline__ void mma(floatx4 &acc, float4 a, float4 b) {
   acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a.y, b.y, acc, 0, 0, 0);
   acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a.z, b.z, acc, 0, 0, 0);
   acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a.w, b.w, acc, 0, 0, 0);
-}
-
-// The same operand straight from row t0 + r0 + i of a strided array.
-template <class E>
-__device__ __forceinline__ float4 frag_rows(const Rows &r, int h, int t0, int len, int r0, int kk, int lane) {
-  const int i = r0 + (lane & 15), g = lane >> 4;
-  if (i >= len) return make_float4(0.f, 0.f, 0.f, 0.f);
-  const E *p = at<const E>(r, t0 + i, h) + 16 * kk + 4 * g;
-  return make_float4(to_f(p[0]), to_f(p[1]), to_f(p[2]), to_f(p[3]));
 }
 
 // L[i][j] = product of al[j + 1 .. i] (1 on the diagonal, 0 above) into lds
@@ -275,8 +241,8 @@ template <> struct Parts<BF16> { static constexpr int n = 1; };
 template <> struct Parts<F16> { static constexpr int n = 2; };
 template <> struct Parts<F32> { static constexpr int n = 3; };
 
-// Parts that a result of type E can hold of its operands: what is rounded at
-// 2^-9 or 2^-12 takes no parts below 2^-16.
+// Parts that a result of type E can hold of its operands: what is rounded by
+// up to 2^-8 (bf16) or 2^-11 (fp16) takes no parts below 2^-16.
 template <class E> constexpr int kOutParts = Parts<E>::n == 3 ? 3 : 2;
 
 __device__ __forceinline__ uint32_t pair_bf16(float x, float y) {

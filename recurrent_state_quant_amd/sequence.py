@@ -66,7 +66,8 @@ class LeapQuantSequence:
     save: for forward calls that a backward call follows; the workspace then
     holds what the backward call reads, so a plan serves one forward and its
     backward calls at a time.  Calls that may run at the same time, and
-    captured graphs that may, need a plan each.
+    captured graphs that may, need a plan each; a plan outlives the work that
+    was launched with it, and every replay of a graph that holds its calls.
     """
 
     def __init__(self, max_tokens, max_seqs, heads_k, heads_v, gate="gdn", dtype=torch.bfloat16, device="cuda",
