@@ -706,12 +706,7 @@ __global__ __launch_bounds__(256) void seq_scan_kernel(const SeqArgs A) {
         frag_share<3, FS>(sh_s, 4 * n + w, m, lane, s[m][n][0], s[m][n][1], s[m][n][2], s[m][n][3]);
       if (SAVE) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          float x[NT];
-#pragma unroll
-          for (int n = 0; n < NT; ++n) x[n] = s[m][n][r];
-          store_n<NT>(A.w.S + (at_ * D + 32 * w + 16 * m + 4 * g + r) * D + col, x);
-        }
+        for (int n = 0; n < NT; ++n) store_quad(A.w.S + at_ * D * D, 8 * w + 4 * m + g, col + n, s[m][n]);
       }
     }
     lds_barrier();
@@ -785,12 +780,7 @@ __global__ __launch_bounds__(256) void seq_scan_kernel(const SeqArgs A) {
     }
     if (SAVE) {
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        float x[NT];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) x[n] = u[n][r];
-        store_n<NT>(A.w.U + (at_ * C + tok + r) * D + col, x);
-      }
+      for (int n = 0; n < NT; ++n) store_quad(A.w.U + at_ * C * D, 4 * w + g, col + n, u[n]);
     }
     lds_barrier();
     Acc2 ds[2][NT];

@@ -104,14 +104,23 @@ __device__ __forceinline__ void load_n(const float *p, float (&x)[N]) {
     x[1] = a.y;
   }
 }
-// (streaming stores: what the scans keep for the backward pass outgrows the
-// caches; the reverse scan of 5,000 tokens x 16 heads 130 us, 144 without)
 template <int N>
 __device__ __forceinline__ void store_n(float *p, const float (&x)[N]) {
   if constexpr (N == 1)
     __builtin_nontemporal_store(x[0], p);
   else
     __builtin_nontemporal_store(vf2{x[0], x[1]}, reinterpret_cast<vf2 *>(p));
+}
+// [rows][128] fp32 arrays that the scans keep for the backward pass: four rows
+// together, [rows / 4][column][4], as a lane's accumulator holds them, so that
+// it is stored in one piece.  In a run of 32 columns the even ones come first:
+// a store covers whole lines whether a lane has one column or two.  Streaming
+// stores: these arrays outgrow the caches.
+__device__ __forceinline__ int quad_at(int quad, int col) {
+  return quad * D + (col & ~31) + (col & 1) * 16 + ((col & 31) >> 1);
+}
+__device__ __forceinline__ void store_quad(float *p, int quad, int col, floatx4 x) {
+  __builtin_nontemporal_store(x, reinterpret_cast<floatx4 *>(p) + quad_at(quad, col));
 }
 // four values at p (aligned to four elements)
 __device__ __forceinline__ void load4(const F32 *p, float (&x)[4]) {

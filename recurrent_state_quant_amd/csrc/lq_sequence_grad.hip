@@ -159,12 +159,7 @@ __global__ __launch_bounds__(512) void seq_rscan_kernel(const SeqArgs A) {
       frag_share<3, FS>(sh_g, 4 * n + (w >> 1), w & 1, lane, s[n][0], s[n][1], s[n][2], s[n][3]);
     }
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      float x[NT];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) x[n] = s[n][r];
-      store_n<NT>(A.w.G + (at_ * D + 16 * w + 4 * g + r) * D + col, x);
-    }
+    for (int n = 0; n < NT; ++n) store_quad(A.w.G + at_ * D * D, 4 * w + g, col + n, s[n]);
     lds_barrier();
     const float gm[4] = {gam.x, gam.y, gam.z, gam.w}, kp[4] = {kap.x, kap.y, kap.z, kap.w};
     const float la = last;
@@ -247,14 +242,10 @@ __global__ __launch_bounds__(512) void seq_rscan_kernel(const SeqArgs A) {
       E *out = at<E>(A.dv, t0 + tok, hv) + col;
       E o[4][NT];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        float x[NT];
+      for (int n = 0; n < NT; ++n) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          x[n] = u[n][r];
-          o[r][n] = from_f<E>(x[n]);
-        }
-        store_n<NT>(A.w.X + (at_ * C + tok + r) * D + col, x);
+        for (int r = 0; r < 4; ++r) o[r][n] = from_f<E>(u[n][r]);
+        store_quad(A.w.X + at_ * C * D, 4 * wt + g, col + n, u[n]);
       }
       if (len >= C) {  // a whole chunk: no branch for every row
 #pragma unroll
@@ -380,20 +371,27 @@ __global__ __launch_bounds__(512) void seq_grad_kernel(const SeqArgs A) {
       kp = A.w.dec[at_ * 2 * C + C + tid];
     }
     {
-      float4 u[4], x[4];
+      // thread: tokens 4 (tid >> 5) .. + 3 of two pairs of columns, 2 j and 2 j + 64 on
+      const int quad = tid >> 5, j = tid & 31;
+      floatx4 u[2][2], x[2][2];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        u[e] = reinterpret_cast<const float4 *>(U)[tid + 512 * e];
-        if (DELTA) x[e] = reinterpret_cast<const float4 *>(X)[tid + 512 * e];
-      }
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int o = quad_at(quad, 64 * e + 2 * j + c);
+          u[e][c] = reinterpret_cast<const floatx4 *>(U)[o];
+          if (DELTA) x[e][c] = reinterpret_cast<const floatx4 *>(X)[o];
+        }
       tile_load(fo, reinterpret_cast<float *>(sh_p) + w * 16 * LDC, at<const E>(A.go, ch.t0, hv), A.go.ts, 16 * wt,
                 ch.len, lane);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int o = (16 * e + (tid >> 5)) * LDD + 4 * (tid & 31);
-        *reinterpret_cast<float4 *>(sh_u + o) = u[e];
-        if (DELTA) *reinterpret_cast<float4 *>(sh_x + o) = x[e];
-      }
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int o = (4 * quad + r) * LDD + 64 * e + 2 * j;
+          *reinterpret_cast<float2 *>(sh_u + o) = make_float2(u[e][0][r], u[e][1][r]);
+          if (DELTA) *reinterpret_cast<float2 *>(sh_x + o) = make_float2(x[e][0][r], x[e][1][r]);
+        }
     }
     if (tid < C) {
       sh_a[tid] = tid < ch.len ? al : 1.f;
@@ -465,32 +463,33 @@ __global__ __launch_bounds__(512) void seq_grad_kernel(const SeqArgs A) {
       }
       if (NP > 1) __builtin_amdgcn_sched_barrier(0);
     }
-    // 32 value columns of S0 and G: eight threads a key row, four columns each
-    float4 xs[2], xg[2];
+    // 32 value columns of S0 and G: a thread has four key rows of two columns
+    floatx4 xs[2], xg[2];
     const auto load_states = [&](int x) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int o = (64 * e + (tid >> 3)) * D + 32 * x + 4 * (tid & 7);
-        xs[e] = *reinterpret_cast<const float4 *>(S0 + o);
-        xg[e] = *reinterpret_cast<const float4 *>(G + o);
+      for (int c = 0; c < 2; ++c) {
+        const int o = quad_at(tid >> 4, 32 * x + 2 * (tid & 15) + c);
+        xs[c] = reinterpret_cast<const floatx4 *>(S0)[o];
+        xg[c] = reinterpret_cast<const floatx4 *>(G)[o];
       }
     };
+    // their parts as fragments, each group g of 16 lanes with its rows in the
+    // order i ^ g: so the threads of a store ask 64 banks, not 16
     float gs = 0.f;
     const auto share_states = [&]() {
+      const int j = tid & 15, c = j >> 2, r0 = 4 * ((tid >> 4) & 3);
+      uint16_t *d = sh_p + (tid >> 6) * 3 * 512 + 16 * c * 8 + 2 * (j & 3);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int r = 64 * e + (tid >> 3), c = tid & 7;
-        uint16_t *d = sh_p + (r >> 4) * 3 * 512 + ((r & 15) + 16 * (c >> 1)) * 8 + 4 * (c & 1);
-        uint32_t p0[3], p1[3];
-        split_pair<3>(xs[e].x, xs[e].y, p0);
-        split_pair<3>(xs[e].z, xs[e].w, p1);
+      for (int r = 0; r < 4; ++r) {
+        uint16_t *const to = d + (r0 + (r ^ c)) * 8;
+        uint32_t p[3];
+        split_pair<3>(xs[0][r], xs[1][r], p);
 #pragma unroll
-        for (int n = 0; n < 3; ++n) *reinterpret_cast<uint2 *>(d + n * 512) = make_uint2(p0[n], p1[n]);
-        split_pair<3>(xg[e].x, xg[e].y, p0);
-        split_pair<3>(xg[e].z, xg[e].w, p1);
+        for (int n = 0; n < 3; ++n) *reinterpret_cast<uint32_t *>(to + n * 512) = p[n];
+        split_pair<3>(xg[0][r], xg[1][r], p);
 #pragma unroll
-        for (int n = 0; n < 3; ++n) *reinterpret_cast<uint2 *>(d + (24 + n) * 512) = make_uint2(p0[n], p1[n]);
-        gs += (xs[e].x * xg[e].x + xs[e].y * xg[e].y) + (xs[e].z * xg[e].z + xs[e].w * xg[e].w);
+        for (int n = 0; n < 3; ++n) *reinterpret_cast<uint32_t *>(to + (24 + n) * 512) = p[n];
+        gs += xs[0][r] * xg[0][r] + xs[1][r] * xg[1][r];
       }
     };
     load_states(0);
@@ -577,8 +576,8 @@ __global__ __launch_bounds__(512) void seq_grad_kernel(const SeqArgs A) {
 #pragma unroll
       for (int n = 0; n < 4; ++n) {
         bf8 bs[3], bg[3];
-        frag_load<3>(bs, sh_p + (4 * h + n) * 3 * 512, lane);
-        frag_load<3>(bg, sh_p + (8 + 4 * h + n) * 3 * 512, lane);
+        frag_load<3>(bs, sh_p + (4 * h + n) * 3 * 512, lane ^ g);
+        frag_load<3>(bg, sh_p + (8 + 4 * h + n) * 3 * 512, lane ^ g);
         mma_into<3, NP>(z1[n], bs, po);
         if (DELTA) mma_into<3, 3>(z2[n], bs, px);
         mma_into<3, 3>(z3[n], bg, pu);
