@@ -616,9 +616,11 @@ __global__ __launch_bounds__(256) void seq_scan_kernel(const SeqArgs A) {
   // workgroups b, b + 8, .. run on one XCD: the column blocks of one head
   // are placed there, so that its L2 serves their common operands
   const int64_t b = blockIdx.x;
-  const int64_t unit = (b / (8 * kBlocks)) * 8 + (b & 7);
-  if (unit >= (int64_t)A.seqs * A.hv) return;
-  const int seq = (int)(unit / A.hv), hv = (int)(unit % A.hv);
+  const int64_t place = (b / (8 * kBlocks)) * 8 + (b & 7);
+  if (place >= (int64_t)A.seqs * A.hv) return;
+  const int seq = seq_place(A, (int)(place / A.hv), gridDim.x, lane);
+  const int hv = (int)(place % A.hv);
+  const int64_t unit = (int64_t)seq * A.hv + hv;
   const int hk = KDA ? hv : hv / A.group, heads_k = KDA ? A.hv : A.hk;
   const int start = seq_start(A, seq), end = seq_end(A, seq, start);
   __shared__ __align__(16) uint16_t sh_s[3 * FS * 512];              // S, [column][key row]

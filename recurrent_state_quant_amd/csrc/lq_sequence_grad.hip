@@ -38,9 +38,11 @@ __global__ __launch_bounds__(512) void seq_rscan_kernel(const SeqArgs A) {
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wt = w & 3;
   const bool kwave = w < 4;
   const int64_t b = blockIdx.x;  // column blocks of a head on one XCD, as in the forward scan
-  const int64_t unit = (b / (8 * kBlocks)) * 8 + (b & 7);
-  if (unit >= (int64_t)A.seqs * A.hv) return;
-  const int seq = (int)(unit / A.hv), hv = (int)(unit % A.hv), hk = hv / A.group;
+  const int64_t place = (b / (8 * kBlocks)) * 8 + (b & 7);
+  if (place >= (int64_t)A.seqs * A.hv) return;
+  const int seq = seq_place(A, (int)(place / A.hv), gridDim.x, lane);
+  const int hv = (int)(place % A.hv), hk = hv / A.group;
+  const int64_t unit = (int64_t)seq * A.hv + hv;
   const int start = seq_start(A, seq), end = seq_end(A, seq, start);
   __shared__ __align__(16) uint16_t sh_g[3 * FS * 512];               // G, [column][key row]
   __shared__ __align__(16) uint16_t sh_o[NP * FX * 512];              // dO of the next chunk, [column][token]

@@ -552,6 +552,29 @@ def test_many_value_heads_for_a_key_head():
     check_backward(cu, backward(plan, cu, d, do.to(DEV)), ref[2:])
 
 
+MANY = [1, 0, 64, 64, 130, 37, 5, 0, 90, 17] * 4  # equal, empty and the longest in the middle
+
+
+@pytest.mark.parametrize("gate", ["gdn", "kda"])
+@pytest.mark.parametrize("lengths", [MANY, MANY + [70] * 25, [0] * 39 + [1100]])
+def test_more_workgroups_than_the_chip_holds(gate, lengths):
+    """Scans whose grid begins with the longest sequences, and (more than 64 sequences) in their order."""
+    cu, x = make(lengths, 2, 4, BF16, gate, seed=114, shift=2.0)
+    _, _, o, S = forward(cu, x, 2, 4, gate)
+    check_forward(cu, x, o, S, reference(cu, x))
+
+
+@pytest.mark.parametrize("lengths", [MANY, MANY + [33] * 25])
+def test_backward_of_more_workgroups_than_the_chip_holds(lengths):
+    cu, x = make(lengths, 2, 4, BF16, seed=115, shift=2.0)
+    g = torch.Generator().manual_seed(116)
+    do, dS = torch.randn(x["v"].shape, generator=g).to(BF16), torch.randn(x["S0"].shape, generator=g)
+    plan, d, o, S = forward(cu, x, 2, 4, save=True)
+    ref = reference(cu, x, grads=(do, dS))
+    check_forward(cu, x, o, S, ref[:2])
+    check_backward(cu, backward(plan, cu, d, do.to(DEV), dS.to(DEV)), ref[2:])
+
+
 def test_gradients_of_values_that_are_not_finite_stay_in_their_sequence():
     cu, x = make([70, 5, 90], 1, 2, F32, seed=112)
     do = torch.randn(x["v"].shape, generator=torch.Generator().manual_seed(113)).to(DEV)
