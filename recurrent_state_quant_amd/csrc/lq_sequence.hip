@@ -602,7 +602,7 @@ __global__ __launch_bounds__(512) void seq_prep_kda_kernel(const SeqArgs A) {
 // and P U there (never out of U and S).
 // Bound by the chain of a chunk (K S, T X, K^T U and the barriers between), 1.9
 // us with 16 columns: a prompt of 4,096 tokens x 32 heads 123 us; 16,384 tokens
-// in 24 sequences x 32 heads, where workgroups share the CUs, 327 to 388 us.
+// in 24 sequences x 32 heads, where two workgroups share a CU, 317 to 390 us.
 // Eight waves, four of them for the output, were no faster (142 us).
 // ---------------------------------------------------------------------------
 template <class E, bool KDA, bool DELTA, bool SAVE, int CB>

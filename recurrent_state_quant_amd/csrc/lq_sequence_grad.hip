@@ -28,7 +28,7 @@ namespace lq {
 // Waves 0 .. 3 take the chain (K G, dU, T^T dU, dX), a token tile each; waves
 // 4 .. 7 what does not depend on G: dO's parts and, one chunk ahead, P^T dO.
 // Bound by the chain of a chunk, as that one, and its stores of dX, dV and G: 8,192
-// tokens in 4 sequences x 16 heads 266 us.
+// tokens in 4 sequences x 16 heads 255 us.
 // ---------------------------------------------------------------------------
 template <class E, bool DELTA, int CB>
 __global__ __launch_bounds__(512) void seq_rscan_kernel(const SeqArgs A) {
@@ -283,9 +283,9 @@ __global__ __launch_bounds__(512) void seq_rscan_kernel(const SeqArgs A) {
 // bf16 parts; every other operand is a fragment of the wave's own.
 // One workgroup a CU: with four waves and two workgroups the accumulators of
 // 128 key columns did not fit (68 registers in scratch, no faster).
-// Bound by the latency of a workgroup's steps (36 us for a chunk and head, of
+// Bound by the latency of a workgroup's steps (32 us for a chunk and head, of
 // which the matrix products at their full rate are a third): 8,192 tokens x 16
-// heads 290 us, 5,000 tokens x 16 value heads on 4 key heads in fp16 265 us.
+// heads 265 us, 5,000 tokens x 16 value heads on 4 key heads in fp16 235 us.
 // ---------------------------------------------------------------------------
 // A tile of 16 rows of 128 values as the fragments of its four steps: lane (i,
 // g) holds values 32 x + 8 g .. + 7 of row i.  Rows are read whole, 256 bytes a
@@ -715,8 +715,8 @@ __global__ __launch_bounds__(512) void seq_grad_kernel(const SeqArgs A) {
 template <class E, bool DELTA>
 hipError_t backward(const SeqArgs &a, hipStream_t stream) {
   const int64_t units = ((int64_t)a.seqs * a.hv + 7) / 8 * 8;
-  // (both scans of 8,192 tokens x 16 heads, 256 wide or 512 narrow workgroups:
-  // forward 234 and 257 us, backward 290 and 275)
+  // (8,192 tokens x 16 heads, 256 wide or 512 narrow workgroups: this scan 280
+  // and 255 us, the forward one 238 and 246)
   if (scan_wide(a, 512))
     hipLaunchKernelGGL((seq_rscan_kernel<E, DELTA, 32>), dim3((unsigned)(units * 4)), dim3(512), 0, stream, a);
   else
