@@ -183,3 +183,20 @@ def test_captured():
         torch.cuda.synchronize()
         for a, b in zip((yq, yk, dq, dk, dw), want):
             assert torch.equal(a, b)
+
+
+def test_keys_alone_and_the_gradient_of_unit_weights():
+    T, hk = 37, 21
+    x = make(T, 0, hk, BF16, False, 64, seed=6)
+    args = how(x, "rms", 1.0, False)
+    q, k = x["q"].to(DEV), x["k"].to(DEV)
+    y, dk, dw = torch.empty((T, hk, 128), device=DEV), torch.empty_like(k), torch.empty(128, device=DEV)
+    lq.leapquant_head_norm(q, k, q.float(), y, **args)
+    lq.leapquant_head_norm_backward(q, k, q.float(), x["gk"].to(DEV), torch.empty_like(q), dk, dk_weight=dw,
+                                    workspace=lq.leapquant_head_norm_workspace(T, 0, hk), **args)
+    leaves = [x["k"].double().requires_grad_(True), torch.ones(128, dtype=torch.float64, requires_grad=True)]
+    ref = R.head_norm(leaves[0], "rms", 1e-5, leaves[1], 1.0, x["pos"], x["freq"], False)
+    R.check(y, ref, 160, "k")
+    for got, want, n, name in zip((dk, dw), torch.autograd.grad((ref * x["gk"].double()).sum(), leaves),
+                                  (320, 320 + T * hk), ("dk", "dw")):
+        R.check(got, want, n, name)

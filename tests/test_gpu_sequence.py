@@ -575,6 +575,24 @@ def test_backward_of_more_workgroups_than_the_chip_holds(lengths):
     check_backward(cu, backward(plan, cu, d, do.to(DEV), dS.to(DEV)), ref[2:])
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+def test_results_repeat_and_gradients_may_lie_over_states(dtype):
+    """The same call again gives the same bits; a second backward call on one workspace too, with dS0 in dS."""
+    cu, x = make([150, 0, 31, 64], 2, 4, dtype, seed=117, shift=2.0)
+    g = torch.Generator().manual_seed(118)
+    do, dS = torch.randn(x["v"].shape, generator=g).to(DEV, dtype), torch.randn(x["S0"].shape, generator=g).to(DEV)
+    plan, d, o, S = forward(cu, x, 2, 4, save=True)
+    first = backward(plan, cu, d, do, dS)
+    again = {m: torch.empty_like(y) for m, y in first.items()}
+    again["S0"] = dS.clone()
+    lq.leapquant_sequence_backward(plan, offsets(cu), d["q"], d["k"], d["beta"], d["alpha"], do, *[again[m] for m in GRADS[:5]],
+                                   dS=again["S0"], dS0=again["S0"])
+    for m in GRADS:
+        assert torch.equal(first[m], again[m]), m
+    _, _, o2, S2 = forward(cu, x, 2, 4, save=True, plan=plan)
+    assert torch.equal(o, o2) and torch.equal(S, S2)
+
+
 def test_gradients_of_values_that_are_not_finite_stay_in_their_sequence():
     cu, x = make([70, 5, 90], 1, 2, F32, seed=112)
     do = torch.randn(x["v"].shape, generator=torch.Generator().manual_seed(113)).to(DEV)
