@@ -41,7 +41,8 @@ def _launch(fn, device, stream, *args):
     if device.type != "cuda":
         raise ValueError("the call's tensors must be in device memory")
     if torch.cuda.current_device() == device.index:
-        handle = _stream(stream, device) if stream is not None else torch.cuda.current_stream().cuda_stream
+        # the current stream's handle without a Stream object: a call of 10 us, 12.5 with one
+        handle = _stream(stream, device) if stream is not None else torch._C._cuda_getCurrentRawStream(device.index)
         return L.check(fn(*args, handle))
     with torch.cuda.device(device):
         L.check(fn(*args, _stream(stream, device)))
