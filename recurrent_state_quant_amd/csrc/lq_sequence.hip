@@ -198,9 +198,8 @@ __device__ __forceinline__ void invert_unit_lower(float *sh_t, float *sh_m, int 
 }
 
 // T and P as the scan's fragments: rows 16 w + i, columns 32 x + 8 g .. + 7;
-// T's block above the diagonal in a step is not written in sh_t: zeros.  NO: the
-// parts of P that the output takes.
-template <bool DELTA, int NO>
+// T's block above the diagonal in a step is not written in sh_t: zeros.
+template <bool DELTA>
 __device__ __forceinline__ void store_triangles(const SeqArgs &A, size_t at_, const float *sh_t, const float *sh_p, int w,
                                                 int lane) {
   const int i = lane & 15, g = lane >> 4;
@@ -219,9 +218,8 @@ __device__ __forceinline__ void store_triangles(const SeqArgs &A, size_t at_, co
       frag_store<3>(A.w.T + ((at_ * 4 + w) * 2 + x) * 3 * 512, f, lane);
     }
     load8(reinterpret_cast<const F32 *>(sh_p + row * LDC + col), v);
-    bf8 fp[NO];
-    split8<NO>(v, fp);
-    frag_store<NO>(A.w.P + ((at_ * 4 + w) * 2 + x) * 3 * 512, fp, lane);
+    split8<3>(v, f);
+    frag_store<3>(A.w.P + ((at_ * 4 + w) * 2 + x) * 3 * 512, f, lane);
   }
 }
 
@@ -341,7 +339,7 @@ __global__ __launch_bounds__(256) void seq_prep_kernel(const SeqArgs A) {
   }
   __syncthreads();
   if (DELTA) invert_unit_lower(sh_t, sh_m, w, lane);
-  store_triangles<DELTA, kOutParts<E>>(A, at_, sh_t, sh_l, w, lane);
+  store_triangles<DELTA>(A, at_, sh_t, sh_l, w, lane);
   if (!SAVE) return;
   // transposes for the backward scan: columns 16 w + i, rows 32 x + 8 g .. + 7
 #pragma unroll
@@ -582,7 +580,7 @@ __global__ __launch_bounds__(512) void seq_prep_kda_kernel(const SeqArgs A) {
   if (tid < D) A.w.dec[at_ * 2 * C + tid] = (sh_bp[0][tid] * sh_bp[1][tid]) * (sh_bp[2][tid] * sh_bp[3][tid]);
   __syncthreads();
   if (DELTA) invert_unit_lower(sh_k, sh_m, w, lane);
-  if (kwave) store_triangles<DELTA, kOutParts<E>>(A, at_, sh_k, sh_p, w, lane);
+  if (kwave) store_triangles<DELTA>(A, at_, sh_k, sh_p, w, lane);
 }
 
 // ---------------------------------------------------------------------------
@@ -598,19 +596,22 @@ __global__ __launch_bounds__(512) void seq_prep_kda_kernel(const SeqArgs A) {
 // each reloaded for the next chunk right after its use, so the loads run
 // behind the rest of the chunk.  What the waves share (S, X, U) goes through
 // LDS as bf16 parts; three barriers a chunk.
-// The output's products take the parts that its type can hold: o in 16 bits
-// is rounded by up to 2^-8 or 2^-11, so parts below 2^-16 are left out of Q S
-// and P U there (never out of U and S).
 // Bound by the chain of a chunk (K S, T X, K^T U and the barriers between), 1.9
 // us with 16 columns: a prompt of 4,096 tokens x 32 heads 123 us; 16,384 tokens
 // in 24 sequences x 32 heads, where two workgroups share a CU, 317 to 390 us.
 // Eight waves, four of them for the output, were no faster (142 us).
 // ---------------------------------------------------------------------------
+// Workgroups that share a CU: the wide fp16 scan is held to the registers of two
+// (256; it would take 260): 5,000 tokens in 19 sequences x 16 heads 104 us, 129
+// with one
+template <class E, bool KDA, int CB>
+constexpr int scan_per_cu() { return !KDA && CB == 32 && Parts<E>::n == 2 ? 2 : 1; }
+
 template <class E, bool KDA, bool DELTA, bool SAVE, int CB>
-__global__ __launch_bounds__(256) void seq_scan_kernel(const SeqArgs A) {
-  constexpr int NT = CB / 16, kBlocks = D / CB, NO = kOutParts<E>;
-  // parts of K and K^T, and of Q; with a decay a channel they hold decays, per value head
-  constexpr int NP = KDA ? 3 : Parts<E>::n, NQ = KDA ? NO : NP;
+__global__ __launch_bounds__(256, (scan_per_cu<E, KDA, CB>())) void seq_scan_kernel(const SeqArgs A) {
+  constexpr int NT = CB / 16, kBlocks = D / CB;
+  // parts of K, Q and K^T; with a decay a channel they hold decays, per value head
+  constexpr int NP = KDA ? 3 : Parts<E>::n;
   constexpr int FS = 4 * NT, FX = 2 * NT;  // fragments of a part of [CB][128], [CB][64]
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -626,7 +627,7 @@ __global__ __launch_bounds__(256) void seq_scan_kernel(const SeqArgs A) {
   const int start = seq_start(A, seq), end = seq_end(A, seq, start);
   __shared__ __align__(16) uint16_t sh_s[3 * FS * 512];              // S, [column][key row]
   __shared__ __align__(16) uint16_t sh_x[DELTA ? 3 * FX * 512 : 8];  // X, [column][token]
-  __shared__ __align__(16) uint16_t sh_u[KDA ? 8 : NO * FX * 512];   // U
+  __shared__ __align__(16) uint16_t sh_u[KDA ? 8 : 3 * FX * 512];   // U
   __shared__ __align__(16) uint16_t sh_ku[3 * FX * 512];             // kappa * U; with a decay a channel U
   __shared__ __align__(16) float sh_dec[2][2 * C];                   // decays, of this chunk and the next
   const int i = lane & 15, g = lane >> 4, tok = 16 * w + 4 * g;
@@ -649,7 +650,7 @@ __global__ __launch_bounds__(256) void seq_scan_kernel(const SeqArgs A) {
   // end is the chunk's first row instead; its X is set to zero and its columns
   // of P and K^T are zero.  V's pointer moves on from chunk to chunk (`move`:
   // 1, or 0 where there is none: then the last chunk is read again).
-  bf8 fk[4][NP], fq[4][NQ], fT[2][3], fP[2][NO], fKT[2][2][NP];
+  bf8 fk[4][NP], fq[4][NP], fT[2][3], fP[2][3], fKT[2][2][NP];
   E v[4][NT];
   float dec;  // thread t < 128: value t of the next chunk's decays
   const int slot0 = start / C + seq;
@@ -661,7 +662,7 @@ __global__ __launch_bounds__(256) void seq_scan_kernel(const SeqArgs A) {
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
       if (DELTA) frag_load<NP>(fk[x], A.w.K + f + x * NP * 512, lane);
-      frag_load<NQ>(fq[x], A.w.Q + f + x * NP * 512, lane);
+      frag_load<NP>(fq[x], A.w.Q + f + x * NP * 512, lane);
     }
   };
   auto load_v = [&](int c, int move) {
@@ -680,8 +681,8 @@ __global__ __launch_bounds__(256) void seq_scan_kernel(const SeqArgs A) {
   };
   auto load_P = [&](int c) {
     const uint16_t *p = A.w.P + (((size_t)(slot0 + c) * A.hv + hv) * 4 + w) * 2 * 3 * 512;
-    frag_load<NO>(fP[0], p, lane);
-    if (w >= 2) frag_load<NO>(fP[1], p + 3 * 512, lane);
+    frag_load<3>(fP[0], p, lane);
+    if (w >= 2) frag_load<3>(fP[1], p + 3 * 512, lane);
   };
   auto load_KT = [&](int c) {
     const uint16_t *p = A.w.KT + (((size_t)(slot0 + c) * heads_k + hk) * 8 + 2 * w) * 2 * NP * 512;
@@ -723,7 +724,7 @@ __global__ __launch_bounds__(256) void seq_scan_kernel(const SeqArgs A) {
         bf8 fs[3];
         frag_get<3, FS>(fs, sh_s, 4 * n + x, lane);
         if (DELTA) mma_parts<NP, 3>(yk[n], fk[x], fs);
-        mma_parts<NQ, 3, NO>(yq[n], fq[x], fs);
+        mma_parts<NP, 3>(yq[n], fq[x], fs);
       }
     load_k(next);
     const float *sd = sh_dec[c & 1];
@@ -779,7 +780,7 @@ __global__ __launch_bounds__(256) void seq_scan_kernel(const SeqArgs A) {
     for (int n = 0; n < NT; ++n) {
       frag_share<3, FX>(sh_ku, 2 * n + (w >> 1), w & 1, lane, kp[0] * u[n][0], kp[1] * u[n][1], kp[2] * u[n][2],
                         kp[3] * u[n][3]);
-      if (!KDA) frag_share<NO, FX>(sh_u, 2 * n + (w >> 1), w & 1, lane, u[n][0], u[n][1], u[n][2], u[n][3]);
+      if (!KDA) frag_share<3, FX>(sh_u, 2 * n + (w >> 1), w & 1, lane, u[n][0], u[n][1], u[n][2], u[n][3]);
     }
     if (SAVE) {
 #pragma unroll
@@ -806,9 +807,9 @@ __global__ __launch_bounds__(256) void seq_scan_kernel(const SeqArgs A) {
       if (2 * x <= w) {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          bf8 fu[NO];
-          frag_get<NO, FX>(fu, KDA ? sh_ku : sh_u, 2 * n + x, lane);
-          mma_parts<NO, NO, NO>(yq[n], fP[x], fu);
+          bf8 fu[3];
+          frag_get<3, FX>(fu, KDA ? sh_ku : sh_u, 2 * n + x, lane);
+          mma_parts<3, 3>(yq[n], fP[x], fu);
         }
       }
     }

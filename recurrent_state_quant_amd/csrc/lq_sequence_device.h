@@ -259,7 +259,10 @@ __device__ __forceinline__ void decay_matrix(float *L, const float *al, int w, i
 // the previous ones leave), an fp16 value of two, a bf16 value is one.  A
 // product of two values takes the products of their parts that are not below
 // 2^-24 of it: parts (i, j) with i + j <= 2, where a dropped product has the
-// size of one fp32 rounding.  Sums are fp32 in the matrix unit.
+// size of one fp32 rounding.  Sums are fp32 in the matrix unit.  Results in 16
+// bits take no fewer parts: their terms may cancel (a token that overwrites a
+// large state: Q S0 and P U), and the parts count beside the terms, not beside
+// what is left of them.
 // ---------------------------------------------------------------------------
 typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
@@ -269,10 +272,6 @@ template <class E> struct Parts;
 template <> struct Parts<BF16> { static constexpr int n = 1; };
 template <> struct Parts<F16> { static constexpr int n = 2; };
 template <> struct Parts<F32> { static constexpr int n = 3; };
-
-// Parts that a result of type E can hold of its operands: what is rounded by
-// up to 2^-8 (bf16) or 2^-11 (fp16) takes no parts below 2^-16.
-template <class E> constexpr int kOutParts = Parts<E>::n == 3 ? 3 : 2;
 
 __device__ __forceinline__ uint32_t pair_bf16(float x, float y) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector((fl2){x, y}, bf2));
@@ -307,7 +306,7 @@ __device__ __forceinline__ void split8(const float (&x)[8], bf8 (&out)[N]) {
 __device__ __forceinline__ floatx4 mma16(bf8 a, bf8 b, floatx4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
-// All products of parts (i, j), i + j < TOP, small ones first, alternating
+// All products of parts (i, j), i + j <= 2, small ones first, alternating
 // between two sums: a product that adds to the previous one's result waits for
 // it, and a wave has few tiles to change between.
 struct Acc2 {
@@ -317,11 +316,11 @@ struct Acc2 {
 __device__ __forceinline__ Acc2 acc2_zero() {
   return Acc2{floatx4{0.f, 0.f, 0.f, 0.f}, floatx4{0.f, 0.f, 0.f, 0.f}};
 }
-template <int NA, int NB, int TOP = 3>
+template <int NA, int NB>
 __device__ __forceinline__ void mma_parts(Acc2 &c, const bf8 (&a)[NA], const bf8 (&b)[NB]) {
   int k = 0;
 #pragma unroll
-  for (int t = TOP - 1; t >= 0; --t)
+  for (int t = 2; t >= 0; --t)
 #pragma unroll
     for (int i = 0; i < NA; ++i) {
       const int j = t - i;
@@ -334,10 +333,10 @@ __device__ __forceinline__ void mma_parts(Acc2 &c, const bf8 (&a)[NA], const bf8
     }
 }
 // the same into one sum, for waves with many tiles to change between
-template <int NA, int NB, int TOP = 3>
+template <int NA, int NB>
 __device__ __forceinline__ void mma_into(floatx4 &c, const bf8 (&a)[NA], const bf8 (&b)[NB]) {
 #pragma unroll
-  for (int t = TOP - 1; t >= 0; --t)
+  for (int t = 2; t >= 0; --t)
 #pragma unroll
     for (int i = 0; i < NA; ++i) {
       const int j = t - i;

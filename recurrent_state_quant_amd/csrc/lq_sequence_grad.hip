@@ -322,8 +322,7 @@ __device__ __forceinline__ void tile_load(Row4<E> &f, float *lds, const E *p, in
 
 template <class E, bool DELTA>
 __global__ __launch_bounds__(512) void seq_grad_kernel(const SeqArgs A) {
-  // parts of E1 and E2: what dQ and dK can hold of them
-  constexpr int NP = Parts<E>::n, NE = kOutParts<E>;
+  constexpr int NP = Parts<E>::n;
   const int slot = blockIdx.x, hk = blockIdx.y;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const Chunk ch = find_chunk(A, slot, threadIdx.x & 63);
@@ -630,15 +629,15 @@ __global__ __launch_bounds__(512) void seq_grad_kernel(const SeqArgs A) {
         if (DELTA) v2[e] = j < row ? b : (j > row ? a : 0.f);
       }
       if (NP > 1) load_kq(x);
-      bf8 fr[NE], fc[NE], f2[NE];
-      split8<NE>(vr, fr);
-      split8<NE>(vc, fc);
-      if (DELTA) split8<NE>(v2, f2);
+      bf8 fr[3], fc[3], f2[3];
+      split8<3>(vr, fr);
+      split8<3>(vc, fc);
+      if (DELTA) split8<3>(v2, f2);
 #pragma unroll
       for (int n = 0; n < 4; ++n) {
-        mma_into<NP, NE, NE>(dq[n], bk[n], fr);
-        mma_into<NP, NE, NE>(dk[n], bq[n], fc);
-        if (DELTA) mma_into<NP, NE, NE>(dk[n], bk[n], f2);
+        mma_into<NP, 3>(dq[n], bk[n], fr);
+        mma_into<NP, 3>(dk[n], bq[n], fc);
+        if (DELTA) mma_into<NP, 3>(dk[n], bk[n], f2);
       }
       if (NP == 1 && x == 0) load_kq(1);
     }
