@@ -376,7 +376,11 @@ typedef enum lq_dtype {
  * multiples of 16 bytes; scalars need 4-byte alignment.  Inputs may repeat
  * memory (stride 0); of an output, no two elements may be the same memory.
  * Slices of one larger row (q, k and v out of one projection, or their
- * gradients into one) are fine. */
+ * gradients into one) are fine, also head by head.  Outputs share no memory
+ * with inputs or other outputs (LQ_ERR_ALIAS): exact for arrays of one token
+ * stride; arrays of other token strides whose ranges interleave, and more than
+ * 65,536 pairs of heads in interleaved head strides that differ, count as
+ * sharing. */
 typedef struct lq_rows {
   void *ptr;
   int64_t token_stride;
