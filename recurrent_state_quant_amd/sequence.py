@@ -66,7 +66,9 @@ class LeapQuantSequence:
     with heads_k query and key heads and heads_v value heads of `dtype`.
     save: for forward calls that a backward call follows; the workspace then
     holds what the backward call reads, so a plan serves one forward and its
-    backward calls at a time.  Calls that may run at the same time, and
+    backward calls at a time (a backward call whose tokens or sequences are not
+    those of the plan's last forward call, also into a capture, is refused).
+    Calls that may run at the same time, and
     captured graphs that may, need a plan each; a plan outlives the work that
     was launched with it, and every replay of a graph that holds its calls.
     """
@@ -80,6 +82,7 @@ class LeapQuantSequence:
         size = _bytes(L.load().leapquant_sequence_workspace(ctypes.byref(prm), int(self.save)))
         self.workspace = torch.empty(size, dtype=torch.uint8, device=device)
         self.device = self.workspace.device   # with its index resolved
+        self._saved = None   # tokens and sequences of the forward call that the workspace holds
 
     def params(self, tokens, seqs):
         return L.LqSequence(int(tokens), int(seqs), self.heads_k, self.heads_v, 128, 128, self.gate, self.flags,
@@ -118,6 +121,8 @@ def leapquant_sequence_forward(plan, cu_seqlens, q, k, v, beta, alpha, o, S0=Non
             _rows(alpha, _F32, ashape, "alpha", d), _rows(o, dt, (T, hv, 128), "o", d),
             _states(S0, seqs * hv, "S0", d), _states(S, seqs * hv, "S", d)]
     _launch(L.load().leapquant_sequence_forward, d, stream, prm, cu, *args, *plan._space(), int(plan.save))
+    if plan.save:
+        plan._saved = T, seqs
 
 
 def leapquant_sequence_backward(plan, cu_seqlens, q, k, beta, alpha, do, dq, dk, dv, dbeta, dalpha, dS=None,
@@ -128,7 +133,12 @@ def leapquant_sequence_backward(plan, cu_seqlens, q, k, beta, alpha, do, dq, dk,
     dalpha and dS0 (None: not wanted; may be dS), shaped as their inputs."""
     if not plan.save:
         raise ValueError("the plan was made without save")
+    if plan._saved is None:
+        raise ValueError("the plan holds no forward call")
     prm, cu, T, seqs = plan._call(cu_seqlens, q)
+    if plan._saved != (T, seqs):
+        raise ValueError("the plan holds a forward call of %d tokens in %d sequences, " % plan._saved +
+                         f"not of {T} in {seqs}")
     d, hk, hv, dt = plan.device, plan.heads_k, plan.heads_v, plan.dtype
     args = [_rows(q, dt, (T, hk, 128), "q", d), _rows(k, dt, (T, hk, 128), "k", d),
             _rows(beta, _F32, (T, hv), "beta", d), _rows(alpha, _F32, (T, hv), "alpha", d),
