@@ -11,6 +11,9 @@ from .api import _F32, _I32, _gate_id, _ptr, _stream
 
 _DTYPES = {torch.float32: L.LQ_F32, torch.bfloat16: L.LQ_BF16, torch.float16: L.LQ_F16}
 _NORMS = {"l2": L.LQ_NORM_L2, "rms": L.LQ_NORM_RMS, L.LQ_NORM_L2: L.LQ_NORM_L2, L.LQ_NORM_RMS: L.LQ_NORM_RMS}
+# The current stream's handle without a Stream object: a call of 10 us, 12.5 with
+# one.  No public name of torch's, so a version that lacks it takes the object.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _dtype_id(dtype):
@@ -41,8 +44,8 @@ def _launch(fn, device, stream, *args):
     if device.type != "cuda":
         raise ValueError("the call's tensors must be in device memory")
     if torch.cuda.current_device() == device.index:
-        # the current stream's handle without a Stream object: a call of 10 us, 12.5 with one
-        handle = _stream(stream, device) if stream is not None else torch._C._cuda_getCurrentRawStream(device.index)
+        raw = stream is None and _raw_stream is not None
+        handle = _raw_stream(device.index) if raw else _stream(stream, device)
         return L.check(fn(*args, handle))
     with torch.cuda.device(device):
         L.check(fn(*args, _stream(stream, device)))
