@@ -82,6 +82,9 @@
 extern "C" {
 #endif
 
+/* The version of the structures' layouts and of the entry points up to
+ * leapquant_stream_reference.  The sequence and head norm calls were added in
+ * version 6: whether a library of that version has them, its symbols tell. */
 #define LEAPQUANT_ABI_VERSION 6
 
 typedef enum lq_status {
@@ -405,6 +408,16 @@ typedef struct lq_sequence {
  * that backward call.  The workspace is 16-byte aligned device memory. */
 int64_t leapquant_sequence_workspace(const lq_sequence *sq, int32_t save);
 
+/* The forms of the forward call: token by token for few tokens a sequence,
+ * 64 tokens together otherwise.  Without save the call goes by the average,
+ * tokens / seqs (up to 24; up to 56 with fp32 operands or a decay a channel and
+ * 256 states or more), as the lengths are on the device.  A long sequence among
+ * many short ones therefore takes its tokens one by one (about 1 us each with
+ * thousands of states): such a batch is better two calls, the long sequences'
+ * and the short ones', on slices of the token arrays or, for a run of
+ * sequences, on the same arrays with cu_seqlens, S0 and S from the run's first
+ * sequence on (tokens, the arrays' rows, is what the average counts). */
+
 /* Forward: for every sequence and value head, from state S0 (NULL: zeros),
  *   u_t = v_t - S_{t-1}^T b_t,  S_t = D_t S_{t-1} + k~_t u_t^T,  o_t = S_t^T q_t.
  * Inputs: q, k [tokens][heads_k][128] and v [tokens][heads_v][128] of dtype;
@@ -439,7 +452,10 @@ int leapquant_sequence_backward(const lq_sequence *sq, const int32_t *cu_seqlens
  * Norm of query and key heads, with the position rotation.
  *
  * What makes the unit-norm queries and keys that the calls above and the
- * decode calls take.  For each head x of 128 values of token t:
+ * decode calls take: LQ_NORM_L2, or LQ_NORM_RMS with a weight that holds the
+ * factor 128^-1/2 (an RMS-normed head of 128 values has norm 128^1/2, and keys
+ * of a norm above 1 make the recurrence grow).  For each head x of 128 values
+ * of token t:
  *   r = (sum x^2 + eps)^-1/2 (LQ_NORM_L2) or (sum x^2 / 128 + eps)^-1/2 (LQ_NORM_RMS)
  *   y = s * R(positions[t]) (w * x * r)
  * with w the weight of 128 values (NULL: ones), s = q_scale for queries and 1

@@ -31,8 +31,8 @@ namespace lq {
 // from the same S_{t-1} (o_t = S_{t-1}^T (D q) + (k~.q) u_t), so both sums are
 // taken in one pass and reduced over the 8 row groups by DPP.
 // With few tokens bound by the states' bytes: 201 tokens in 64 sequences x 32
-// heads 52 us, 5.2 TB/s.  With many, by a token's chain (about 0.4 us), for
-// which the chunked form is there.
+// heads 52 us, 5.2 TB/s.  With many, by a token's chain (0.4 us, 1.1 us with four
+// columns a lane), for which the chunked form is there.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ float row8_sum(float x) {
   x += dpp<0xB1>(x);   // quad_perm [1,0,3,2]
@@ -229,10 +229,12 @@ __device__ __forceinline__ void store_triangles(const SeqArgs &A, size_t at_, co
 // value head of a key head, K, Q and K^T; with SAVE also the transposes of T,
 // P and Q for the backward scan.  M and T are fp32 (T's rounding enters every
 // later chunk).  Four waves, a tile of 16 rows of M and P each.
-// 4,096 tokens x 32 heads (2,048 workgroups) 52 us; with SAVE and 16 heads and
-// 8,192 tokens 64 us.  Bound by the latency of a workgroup's steps (load, decays,
-// products, the inverse's five barriers), which the workgroups that share a CU
-// hide from one another in part.
+// Bound by its bytes, nearly all of them written (T and P 18 KB each for a value
+// head, K, Q and K^T 16 KB each for a bf16 key head): 4,096 tokens x 32 heads 224
+// MB in 53 us, 4.2 TB/s; with SAVE and 8,192 tokens x 16 heads 325 MB in 64 us,
+// 5.1 TB/s; 16,384 tokens x 16 key and 32 value heads 644 MB in 180 to 203 us, 3.2
+// to 3.6 TB/s, the rest of it the latency of a workgroup's steps (load, decays,
+// products, the inverse's five barriers).
 // ---------------------------------------------------------------------------
 template <class E, bool DELTA, bool SAVE>
 __global__ __launch_bounds__(256) void seq_prep_kernel(const SeqArgs A) {
@@ -597,8 +599,8 @@ __global__ __launch_bounds__(512) void seq_prep_kda_kernel(const SeqArgs A) {
 // behind the rest of the chunk.  What the waves share (S, X, U) goes through
 // LDS as bf16 parts; three barriers a chunk.
 // Bound by the chain of a chunk (K S, T X, K^T U and the barriers between), 1.9
-// us with 16 columns: a prompt of 4,096 tokens x 32 heads 123 us; 16,384 tokens
-// in 24 sequences x 32 heads, where two workgroups share a CU, 317 to 390 us.
+// us with 16 columns: a prompt of 4,096 tokens x 32 heads 124 us; 16,384 tokens
+// in 24 sequences x 32 heads, where two workgroups share a CU, 338 to 405 us.
 // Eight waves, four of them for the output, were no faster (142 us).
 // ---------------------------------------------------------------------------
 // Workgroups that share a CU: the wide fp16 scan is held to the registers of two
@@ -887,9 +889,13 @@ hipError_t chunked(const SeqArgs &a, hipStream_t stream) {
     hipLaunchKernelGGL((seq_prep_kda_kernel<E, DELTA>), slots, dim3(512), 0, stream, a);
   else
     hipLaunchKernelGGL((seq_prep_kernel<E, DELTA, SAVE>), slots, dim3(256), 0, stream, a);
-  // (wide and narrow: a prompt of 4,096 tokens x 32 heads, 128 or 256
-  // workgroups, 197 and 148 us; 24 ragged sequences x 32 heads, many times
-  // what the chip holds, 385 and 574)
+  // (the scan wide and narrow: a prompt of 4,096 tokens x 32 heads, 128 or 256
+  // workgroups, 174 and 124 us; 24 ragged sequences x 32 heads, many times what
+  // the chip holds, 338 and 486.  Both launches of 1,536 tokens in bf16: 32
+  // heads 90 and 74 us, 48 heads 96 and 94, 64 heads 102 and 105, 128 heads 201
+  // and 257.  Operands of two or three parts leave the narrow scan one workgroup
+  // a CU, and 33 to 63 states two rounds of them: fp16 48 heads 133 and 151, fp32
+  // 203 and 244, and 32 heads 120 and 88, 153 and 124)
   if (scan_wide(a, 256))
     hipLaunchKernelGGL((seq_scan_kernel<E, KDA, DELTA, SAVE, 32>), dim3((unsigned)(units * 4)), dim3(256), 0, stream, a);
   else

@@ -20,7 +20,10 @@ constexpr int64_t kMaxPairs = 65536;            // heads of two arrays that are 
 // sequence: with operands of one or two parts at 22 (8 sequences x 32 heads),
 // 28 (64 x 32) and 30 (1 x 32); with three parts (fp32, or a decay a channel)
 // at 22 .. 34 for up to 32 states and at 52 .. 64 from 256 states on, where
-// the chunks' operands outweigh the states.
+// the chunks' operands outweigh the states.  The average decides, as the lengths
+// are on the device: a long sequence among many short ones goes token by token
+// too, 1.1 us a token with 8,192 states (4,096 tokens beside 255 of one, x 32
+// heads, 4,466 us; the two parts in a call each, 372).
 constexpr int64_t kShort = 24, kShortParts = 56, kManyStates = 256;
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }

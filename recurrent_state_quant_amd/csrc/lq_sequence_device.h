@@ -168,7 +168,7 @@ __device__ __forceinline__ int seq_end(const SeqArgs &A, int i, int start) {
 // The sequence of the n-th place in a scan's grid.  Where the grid is more than
 // the chip holds at once (one or two workgroups a CU), the longest come first,
 // so that the last workgroups to begin are short ones: 19 sequences x 16 heads
-// 103 us, 120 in their order; 5 x 32 with a decay a channel 163, 178.  A wave
+// 106 us, 130 in their order; 5 x 32 with a decay a channel 164, 179.  A wave
 // ranks up to 64 lengths; more sequences even out by themselves.
 __device__ __forceinline__ int seq_place(const SeqArgs &A, int n, int64_t workgroups, int lane) {
   if (workgroups <= 512 || A.seqs > 64 || A.seqs == 1) return n;

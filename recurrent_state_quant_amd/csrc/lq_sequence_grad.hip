@@ -285,7 +285,7 @@ __global__ __launch_bounds__(512) void seq_rscan_kernel(const SeqArgs A) {
 // 128 key columns did not fit (68 registers in scratch, no faster).
 // Bound by the latency of a workgroup's steps (32 us for a chunk and head, of
 // which the matrix products at their full rate are a third): 8,192 tokens x 16
-// heads 265 us, 5,000 tokens x 16 value heads on 4 key heads in fp16 235 us.
+// heads 270 us, 5,000 tokens x 16 value heads on 4 key heads in fp16 240 us.
 // ---------------------------------------------------------------------------
 // A tile of 16 rows of 128 values as the fragments of its four steps: lane (i,
 // g) holds values 32 x + 8 g .. + 7 of row i.  Rows are read whole, 256 bytes a
@@ -714,8 +714,8 @@ __global__ __launch_bounds__(512) void seq_grad_kernel(const SeqArgs A) {
 template <class E, bool DELTA>
 hipError_t backward(const SeqArgs &a, hipStream_t stream) {
   const int64_t units = ((int64_t)a.seqs * a.hv + 7) / 8 * 8;
-  // (8,192 tokens x 16 heads, 256 wide or 512 narrow workgroups: this scan 280
-  // and 255 us, the forward one 238 and 246)
+  // (8,192 tokens x 16 heads, 256 wide or 512 narrow workgroups: this scan 279
+  // and 254 us, the forward one 246 and 261)
   if (scan_wide(a, 512))
     hipLaunchKernelGGL((seq_rscan_kernel<E, DELTA, 32>), dim3((unsigned)(units * 4)), dim3(512), 0, stream, a);
   else

@@ -115,7 +115,8 @@ def leapquant_sequence_forward(plan, cu_seqlens, q, k, v, beta, alpha, o, S0=Non
     last axis contiguous); beta [tokens, heads_v]; alpha [tokens, heads_v]
     (gdn) or [tokens, heads_v, 128] (kda), float32.  States float32
     [sequences * heads_v, 128, 128]: S0 before (None: zeros), S after (None:
-    not wanted; may be S0)."""
+    not wanted; may be S0).  One long sequence among many short ones is better
+    a call of its own (include/leapquant.h says which form a call takes)."""
     prm, cu, T, seqs = plan._call(cu_seqlens, q)
     d, hk, hv, dt = plan.device, plan.heads_k, plan.heads_v, plan.dtype
     ashape = (T, hv) if plan.gate == L.LQ_GATE_GDN else (T, hv, 128)
