@@ -57,8 +57,8 @@ bool meet(int64_t off, int64_t step, int64_t least, int64_t most, int64_t wa, in
   return d <= most && off + d * step < wa;
 }
 
-// Exact for arrays with one token stride (or of one token), as views of one
-// buffer have; others whose ranges interleave count as overlapping.
+// Exact for arrays with one token stride (or of one token, or one for all), as
+// views of one buffer have; others whose ranges interleave count as overlapping.
 bool overlap(const Block &a, const Block &b) {
   if (a.lo == a.hi || b.lo == b.hi) return false;
   if (a.lo >= b.hi || b.lo >= a.hi) return false;
@@ -114,8 +114,8 @@ int check_rows(const lq_rows *r, int64_t tokens, int64_t heads, int64_t width, i
   if (last > (int64_t(1) << 58) || across > (int64_t(1) << 58)) return LQ_ERR_SHAPE;
   if (out && coincide(tokens, heads, ts, hs, width)) return LQ_ERR_SHAPE;
   *blk = dense(r->ptr, (last + across + width) * size);
-  blk->tokens = tokens;
-  blk->heads = heads;
+  blk->tokens = ts ? tokens : 1;  // (stride 0: one and the same)
+  blk->heads = hs ? heads : 1;
   blk->ts = ts * size;
   blk->hs = hs * size;
   blk->width = width * size;

@@ -44,10 +44,10 @@ struct Map {
   }
 };
 
-static int backward(int T, int hk, int hv, int dtype, const lq_rows (&out)[5]) {
+static int backward(int T, int hk, int hv, int dtype, const lq_rows (&out)[5], const lq_rows *go = nullptr) {
   lq_sequence sq = {T, 1, hk, hv, 128, 128, LQ_GATE_GDN, 0, dtype};
   lq_rows in = {(void *)0x600000000000, 0, 0}, sc = {(void *)0x610000000000, 0, 0};
-  return leapquant_sequence_backward(&sq, (const int32_t *)0x620000000000, &in, &in, &sc, &sc, &in, nullptr, &out[0],
+  return leapquant_sequence_backward(&sq, (const int32_t *)0x620000000000, &in, &in, &sc, &sc, go ? go : &in, nullptr, &out[0],
                                      &out[1], &out[2], &out[3], &out[4], nullptr, (void *)0x630000000000,
                                      int64_t(1) << 40, nullptr);
 }
@@ -87,6 +87,13 @@ static int named() {
   // one token: its heads interleaved
   const lq_rows one[5] = {{kBase, 0, 384}, {kBase + 256, 0, 384}, {kBase + 512, 0, 384}, b, a};
   EXPECT(backward(1, H, H, LQ_BF16, one), LQ_OK);
+  // one gradient of o for all tokens and heads, in a head of the first token's row that no output has
+  const int64_t ts = 512 * H;
+  const lq_rows q[5] = {{kBase, ts, 512}, {kBase + 256, ts, 512}, {kBase + 512, ts, 512}, b, a};
+  const lq_rows none = {kBase + 768, 0, 0}, taken = {kBase + 512, 0, 0}, part = {kBase + 768 + 16, 0, 0};
+  EXPECT(backward(T, H, H, LQ_BF16, q, &none), LQ_OK);
+  EXPECT(backward(T, H, H, LQ_BF16, q, &taken), LQ_ERR_ALIAS);
+  EXPECT(backward(T, H, H, LQ_BF16, q, &part), LQ_ERR_ALIAS);
   return wrong;
 }
 
