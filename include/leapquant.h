@@ -83,8 +83,9 @@ extern "C" {
 #endif
 
 /* The version of the structures' layouts and of the entry points up to
- * leapquant_stream_reference.  The sequence and head norm calls were added in
- * version 6: whether a library of that version has them, its symbols tell. */
+ * leapquant_stream_reference.  The sequence, head norm, convolution, scan and
+ * block norm calls were added in version 6: whether a library of that version
+ * has them, its symbols tell. */
 #define LEAPQUANT_ABI_VERSION 6
 
 typedef enum lq_status {
@@ -506,6 +507,170 @@ int leapquant_head_norm_backward(const lq_head_norm *nm, const lq_rows *q, const
                                  const lq_rows *gq, const lq_rows *gk, const lq_rows *dq,
                                  const lq_rows *dk, float *dq_weight, float *dk_weight,
                                  void *workspace, int64_t workspace_bytes, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Around the recurrence: the short causal convolution that queries, keys and
+ * values (or the inputs of a state space layer) pass before it, the selective
+ * state space scan, and the norms before and after a block with its gate and
+ * residual scale.
+ *
+ * Arrays of channels, [tokens][channels], are lq_rows whose head stride is not
+ * used: element (t, c) is ptr[t * token_stride + c], aligned to its type, with
+ * any stride and any number of channels.  Sequences are packed as above, with
+ * the same rules for cu_seqlens and for tokens of no sequence.  Sums, states
+ * and statistics are fp32 whatever the type of the arrays, results are rounded
+ * once, and every sum is added in a fixed order.
+ *
+ * The calls for single tokens take one token of each of `tokens` rows; row i is
+ * the next token of slot slots[i] (int32 on the device; NULL: of slot i, and
+ * tokens <= n_slots).  Rows whose slot is outside [0, n_slots) are idle: their
+ * outputs and every unlisted slot are left as they are.  A slot listed twice
+ * races: the caller lists each at most once (device values cannot be checked
+ * on the host).
+ * ------------------------------------------------------------------------- */
+
+typedef enum lq_activation {
+  LQ_ACT_NONE = 0,
+  LQ_ACT_SILU = 1,    /* x / (1 + e^-x) */
+  LQ_ACT_SIGMOID = 2  /* 1 / (1 + e^-x) */
+} lq_activation;
+
+/* Convolution of every channel with `width` weights over its own past:
+ *   v_t = bias + sum_{j < width} weight[c][j] x_{t - width + 1 + j},   y_t = act(v_t)
+ * The width - 1 inputs before a sequence's first token are X0[seq][0 ..][c],
+ * the last one next to it (NULL: zeros); X receives the last width - 1 inputs
+ * of each sequence (NULL: not wanted), for its next tokens.  X0 and X
+ * ([seqs][width - 1][channels] of dtype) may not overlap in the calls over
+ * sequences. */
+typedef struct lq_conv {
+  int64_t tokens;      /* rows of the token arrays, >= 0                       */
+  int32_t seqs;        /* sequences, >= 1 (not read for single tokens)         */
+  int32_t channels;    /* 1 .. 2^20                                            */
+  int32_t width;       /* 2, 3 or 4 (LQ_ERR_UNSUPPORTED otherwise)             */
+  int32_t activation;  /* LQ_ACT_NONE or LQ_ACT_SILU                           */
+  int32_t dtype;       /* lq_dtype of x, y, X0, X and their gradients          */
+  const float *weight; /* [channels][width]                                    */
+  const float *bias;   /* [channels] or NULL                                   */
+} lq_conv;
+
+int leapquant_conv_forward(const lq_conv *cv, const int32_t *cu_seqlens, const lq_rows *x, const lq_rows *y,
+                           const void *X0, void *X, hipStream_t stream);
+
+/* One token of each row: the slots' earlier inputs X0 [n_slots][width - 1]
+ * [channels] in, the ones after the token out to X (may be X0). */
+int leapquant_conv_step(const lq_conv *cv, const int32_t *slots, int32_t n_slots, const lq_rows *x, const lq_rows *y,
+                        const void *X0, void *X, hipStream_t stream);
+
+/* Bytes of workspace of leapquant_conv_backward with a weight or bias gradient,
+ * enough for at most these tokens, or a negative lq_status (weight is not
+ * read). */
+int64_t leapquant_conv_workspace(const lq_conv *cv);
+
+/* From dy, the gradient of y, and dX, that of X (NULL: zeros): dx, dX0,
+ * dweight and dbias (fp32; the last three each NULL if not wanted).  X0 as
+ * forward. */
+int leapquant_conv_backward(const lq_conv *cv, const int32_t *cu_seqlens, const lq_rows *x, const lq_rows *dy,
+                            const lq_rows *dx, const void *X0, const void *dX, void *dX0, float *dweight, float *dbias,
+                            void *workspace, int64_t workspace_bytes, hipStream_t stream);
+
+/* Selective state space scan.  Channel c of group g = c / (channels / groups)
+ * has `states` states h_n with a decay each:
+ *   d = dt + dt_bias, or log(1 + e^(dt + dt_bias)) with LQ_SCAN_SOFTPLUS
+ *   h_n <- e^(d A_n) h_n + d B_n x,   y = (sum_n C_n h_n + D x) z / (1 + e^-z)
+ * (without z: no last factor).  Where every channel of a head has one decay for
+ * all states and steps and inputs are its keys and values, the recurrence is
+ * that of leapquant_sequence_forward with LQ_NO_DELTA; here each channel and
+ * state has its own.  e^(d A) is a decay: d A <= 0, values finite. */
+enum { LQ_SCAN_SOFTPLUS = 1u };
+
+typedef struct lq_scan {
+  int64_t tokens;       /* rows of the token arrays, >= 0                      */
+  int32_t seqs;         /* sequences, >= 1 (not read for single tokens)        */
+  int32_t channels;     /* 1 .. 2^20, a multiple of groups                     */
+  int32_t states;       /* 8, 16 or 32 (LQ_ERR_UNSUPPORTED otherwise)          */
+  int32_t groups;       /* groups of channels that share B and C, >= 1         */
+  int32_t dtype;        /* lq_dtype of the token arrays                        */
+  uint32_t flags;       /* LQ_SCAN_SOFTPLUS or 0                               */
+  const float *A;       /* [channels][states], 16-byte aligned                 */
+  const float *D;       /* [channels] or NULL (zeros)                          */
+  const float *dt_bias; /* [channels] or NULL (zeros)                          */
+} lq_scan;
+
+/* Bytes of workspace that are enough for every call with these parameters and
+ * at most these tokens and seqs (0 is possible), or a negative lq_status.
+ * save: for a forward call that a backward call follows, and for that call. */
+int64_t leapquant_scan_workspace(const lq_scan *sc, int32_t save);
+
+/* x, dt, z (NULL: none), y [tokens][channels]; B, C [tokens][groups][states]
+ * (arrays of heads of `states` values: 16-byte aligned, also their strides);
+ * S0, S [seqs][channels][states] fp32, the states before (NULL: zeros) and
+ * after (NULL: not wanted; may be S0).  With save != 0 the workspace
+ * afterwards holds what leapquant_scan_backward reads. */
+int leapquant_scan_forward(const lq_scan *sc, const int32_t *cu_seqlens, const lq_rows *x, const lq_rows *dt,
+                           const lq_rows *B, const lq_rows *C, const lq_rows *z, const lq_rows *y, const float *S0,
+                           float *S, void *workspace, int64_t workspace_bytes, int32_t save, hipStream_t stream);
+
+/* One token of each row: the slots' states S0 [n_slots][channels][states] in,
+ * the ones after the token out to S (may be S0). */
+int leapquant_scan_step(const lq_scan *sc, const int32_t *slots, int32_t n_slots, const lq_rows *x, const lq_rows *dt,
+                        const lq_rows *B, const lq_rows *C, const lq_rows *z, const lq_rows *y, const float *S0, float *S,
+                        hipStream_t stream);
+
+/* From dy, the gradient of y, and dS, that of S (NULL: zeros), the gradients of
+ * every input: dx, ddt, dB, dC, dz (NULL without z, and only then), dA, dD and
+ * ddt_bias (these two NULL if not wanted, and without D and dt_bias) and dS0
+ * (NULL: not wanted; may be dS).  Call with the parameters and inputs of a forward call
+ * with save, and its workspace, unchanged since but by backward calls (there
+ * may be more than one). */
+int leapquant_scan_backward(const lq_scan *sc, const int32_t *cu_seqlens, const lq_rows *x, const lq_rows *dt,
+                            const lq_rows *B, const lq_rows *C, const lq_rows *z, const lq_rows *dy, const lq_rows *dx,
+                            const lq_rows *ddt, const lq_rows *dB, const lq_rows *dC, const lq_rows *dz, float *dA,
+                            float *dD, float *ddt_bias, const float *dS, float *dS0, void *workspace,
+                            int64_t workspace_bytes, hipStream_t stream);
+
+/* Norms before and after a block.  For a row of `dim` values of a token and
+ * head, with m(x) = (sum x^2 / dim + eps)^-1/2, from a block's output a,
+ *   n = out_weight * a * m(a)   (out_norm; otherwise n = a)
+ *   u = n * act(z)              (without a gate u = n)
+ *   h = res + scale * u         (without res h = scale * u)
+ *   y = in_weight * h * m(h)    (the input of the next block)
+ * With heads of 128 values, out_norm and a SiLU gate it is the gated norm of a
+ * recurrence's outputs; with one head of the model's width, res and y it joins
+ * a block to the residual stream and norms it for the next one.  y is made of h
+ * before h is rounded.  Values below 2^60. */
+typedef struct lq_block_norm {
+  int64_t tokens;          /* >= 0                                             */
+  int32_t heads;           /* rows of a token, >= 1                            */
+  int32_t dim;             /* values of a row, 8 .. 8192, a multiple of 8      */
+  int32_t dtype;           /* lq_dtype of a, z, y and their gradients          */
+  int32_t dtype_stream;    /* of res, h and their gradients: dtype or LQ_F32   */
+  int32_t gate;            /* lq_activation of z, or LQ_ACT_NONE without z     */
+  int32_t out_norm;        /* 1: norm of a                                     */
+  float eps;               /* > 0                                              */
+  float scale;
+  const float *out_weight; /* [dim], 16-byte aligned, or NULL (ones)           */
+  const float *in_weight;  /* [dim], 16-byte aligned, or NULL (ones)           */
+} lq_block_norm;
+
+/* Arrays of heads of dim values (lq_rows above; 16-byte aligned pointers and
+ * strides).  z and res NULL without them; h and y each NULL if not wanted.  An
+ * output may be a or res itself (the same pointer, strides and type). */
+int leapquant_block_norm(const lq_block_norm *bn, const lq_rows *a, const lq_rows *z, const lq_rows *res, const lq_rows *h,
+                         const lq_rows *y, hipStream_t stream);
+
+/* Bytes of workspace of leapquant_block_norm_backward with a weight gradient,
+ * enough for at most these tokens, or a negative lq_status. */
+int64_t leapquant_block_norm_workspace(int64_t tokens, int32_t heads, int32_t dim);
+
+/* From dh and dy, the gradients of h and y (one of them may be NULL: zeros),
+ * and the inputs of the forward call (res is not read without dy): da, dz
+ * (NULL without z, and only then), dres (NULL if not wanted; may be dh itself),
+ * dout_weight and din_weight (fp32 [dim], each NULL if not wanted, and without
+ * out_norm or dy). */
+int leapquant_block_norm_backward(const lq_block_norm *bn, const lq_rows *a, const lq_rows *z, const lq_rows *res,
+                                  const lq_rows *dh, const lq_rows *dy, const lq_rows *da, const lq_rows *dz,
+                                  const lq_rows *dres, float *dout_weight, float *din_weight, void *workspace,
+                                  int64_t workspace_bytes, hipStream_t stream);
 
 /* ---- Measurement reference, no part of the method: a plain stream in
  * the decode step's launch shape.  One 64-lane wave per block of

@@ -30,6 +30,10 @@ LQ_BF16 = 1
 LQ_F16 = 2
 LQ_NORM_L2 = 0
 LQ_NORM_RMS = 1
+LQ_ACT_NONE = 0
+LQ_ACT_SILU = 1
+LQ_ACT_SIGMOID = 2
+LQ_SCAN_SOFTPLUS = 1
 
 EXPORTED = (
     "leapquant_quantize_state",
@@ -53,6 +57,17 @@ EXPORTED = (
     "leapquant_head_norm",
     "leapquant_head_norm_workspace",
     "leapquant_head_norm_backward",
+    "leapquant_conv_forward",
+    "leapquant_conv_step",
+    "leapquant_conv_workspace",
+    "leapquant_conv_backward",
+    "leapquant_scan_workspace",
+    "leapquant_scan_forward",
+    "leapquant_scan_step",
+    "leapquant_scan_backward",
+    "leapquant_block_norm",
+    "leapquant_block_norm_workspace",
+    "leapquant_block_norm_backward",
     "leapquant_status_string",
     "leapquant_abi_version",
 )
@@ -88,6 +103,25 @@ class LqHeadNorm(ctypes.Structure):
                 ("dtype_out", ctypes.c_int32), ("rot", ctypes.c_int32), ("interleaved", ctypes.c_int32),
                 ("eps", ctypes.c_float), ("q_scale", ctypes.c_float), ("q_weight", ctypes.c_void_p),
                 ("k_weight", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("inv_freq", ctypes.c_void_p)]
+
+
+class LqConv(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("seqs", ctypes.c_int32), ("channels", ctypes.c_int32),
+                ("width", ctypes.c_int32), ("activation", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p)]
+
+
+class LqScan(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("seqs", ctypes.c_int32), ("channels", ctypes.c_int32),
+                ("states", ctypes.c_int32), ("groups", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("flags", ctypes.c_uint32), ("A", ctypes.c_void_p), ("D", ctypes.c_void_p), ("dt_bias", ctypes.c_void_p)]
+
+
+class LqBlockNorm(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("heads", ctypes.c_int32), ("dim", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("dtype_stream", ctypes.c_int32), ("gate", ctypes.c_int32),
+                ("out_norm", ctypes.c_int32), ("eps", ctypes.c_float), ("scale", ctypes.c_float),
+                ("out_weight", ctypes.c_void_p), ("in_weight", ctypes.c_void_p)]
 
 
 class LeapQuantError(RuntimeError):
@@ -131,9 +165,25 @@ def load():
     lib.leapquant_head_norm.argtypes = [N, R, R, R, R, vp]
     lib.leapquant_head_norm_workspace.argtypes = [i64, i32, i32]
     lib.leapquant_head_norm_backward.argtypes = [N, R, R, R, R, R, R, vp, vp, vp, i64, vp]
-    lib.leapquant_sequence_workspace.restype = lib.leapquant_head_norm_workspace.restype = i64
+    V, M, K = ctypes.POINTER(LqConv), ctypes.POINTER(LqScan), ctypes.POINTER(LqBlockNorm)
+    lib.leapquant_conv_forward.argtypes = [V, vp, R, R, vp, vp, vp]
+    lib.leapquant_conv_step.argtypes = [V, vp, i32, R, R, vp, vp, vp]
+    lib.leapquant_conv_workspace.argtypes = [V]
+    lib.leapquant_conv_backward.argtypes = [V, vp, R, R, R, vp, vp, vp, vp, vp, vp, i64, vp]
+    lib.leapquant_scan_workspace.argtypes = [M, i32]
+    lib.leapquant_scan_forward.argtypes = [M, vp, R, R, R, R, R, R, vp, vp, vp, i64, i32, vp]
+    lib.leapquant_scan_step.argtypes = [M, vp, i32, R, R, R, R, R, R, vp, vp, vp]
+    lib.leapquant_scan_backward.argtypes = [M, vp, R, R, R, R, R, R, R, R, R, R, R, vp, vp, vp, vp, vp, vp, i64, vp]
+    lib.leapquant_block_norm.argtypes = [K, R, R, R, R, R, vp]
+    lib.leapquant_block_norm_workspace.argtypes = [i64, i32, i32]
+    lib.leapquant_block_norm_backward.argtypes = [K, R, R, R, R, R, R, R, R, vp, vp, vp, i64, vp]
+    for f in ("leapquant_sequence_workspace", "leapquant_head_norm_workspace", "leapquant_conv_workspace",
+              "leapquant_scan_workspace", "leapquant_block_norm_workspace"):
+        getattr(lib, f).restype = i64
     for f in ("leapquant_sequence_forward", "leapquant_sequence_backward", "leapquant_head_norm",
-              "leapquant_head_norm_backward"):
+              "leapquant_head_norm_backward", "leapquant_conv_forward", "leapquant_conv_step", "leapquant_conv_backward",
+              "leapquant_scan_forward", "leapquant_scan_step", "leapquant_scan_backward", "leapquant_block_norm",
+              "leapquant_block_norm_backward"):
         getattr(lib, f).restype = ctypes.c_int
     for f in ("leapquant_quantize_state", "leapquant_decode_step", "leapquant_window_close",
               "leapquant_decode_close", "leapquant_dense_step", "leapquant_decode_step_slots",

@@ -1,23 +1,28 @@
 """Build libleapquant.so in-tree with hipcc for gfx950."""
+import concurrent.futures
 import os
 import subprocess
 import sys
+import tempfile
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
 LIB_PATH = os.path.join(PKG_DIR, "libleapquant.so")
 KERNEL_SOURCES = ("lq_device.h", "lq_decode_one.h", "lq_decode_body.inc", "lq_close16_body.inc", "lq_decode.hip",
                   "lq_close.hip", "lq_baselines.hip", "lq_sequence.h", "lq_sequence_device.h", "lq_sequence.hip",
-                  "lq_sequence_grad.hip", "lq_norm.hip")
+                  "lq_sequence_grad.hip", "lq_norm.hip", "lq_layer.h", "lq_layer_device.h", "lq_conv.hip",
+                  "lq_scan_device.h", "lq_scan.hip", "lq_scan_grad.hip", "lq_block_norm.hip")
 SOURCES = [os.path.join(PKG_DIR, "csrc", f) for f in ("lq_decode.hip", "lq_close.hip", "lq_baselines.hip",
                                                      "lq_sequence.hip", "lq_sequence_grad.hip", "lq_norm.hip",
-                                                     "lq_abi.cpp", "lq_sequence_abi.cpp")]
+                                                     "lq_conv.hip", "lq_scan.hip", "lq_scan_grad.hip",
+                                                     "lq_block_norm.hip", "lq_abi.cpp", "lq_sequence_abi.cpp",
+                                                     "lq_layer_abi.cpp")]
 ARCH = "gfx950"
 
 
-def hipcc_command(out=LIB_PATH, extra=()):
+def hipcc_command(out=LIB_PATH, extra=(), sources=SOURCES):
     hipcc = os.path.join(os.environ.get("ROCM_PATH", "/opt/rocm"), "bin", "hipcc")
-    return [hipcc, f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-shared",
+    return [hipcc, f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",
             # packed fp32 VALU ops stay off: only scalar fp32 ops are emitted
             "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
             # MFMA accumulators in VGPRs: the close kernel post-processes them
@@ -29,7 +34,7 @@ def hipcc_command(out=LIB_PATH, extra=()):
             # it, so one body included in two kernels could round differently
             "-ffp-contract=on",
             "-I", os.path.join(ROOT, "include"), "-I", os.path.join(PKG_DIR, "csrc"),
-            *extra, "-o", out, *SOURCES]
+            *extra, "-o", out, *sources]
 
 
 C_DRIVER_SRC = os.path.join(ROOT, "tests", "c_abi", "lq_c_driver.c")
@@ -49,26 +54,29 @@ def c_driver_command(out=C_DRIVER):
 
 def build_c_driver(verbose=False):
     """Compile tests/c_abi/lq_c_driver against the built library."""
-    cmd = c_driver_command()
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        sys.stderr.write(res.stdout + res.stderr)
-        raise subprocess.CalledProcessError(res.returncode, cmd, res.stdout, res.stderr)
+    _run(c_driver_command(), verbose)
     return C_DRIVER
 
 
-def build(verbose=False):
-    """Compile the HIP library; raises CalledProcessError on failure."""
-    tmp = LIB_PATH + ".tmp"
-    cmd = hipcc_command(tmp)
+def _run(cmd, verbose):
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         sys.stderr.write(res.stdout + res.stderr)
         raise subprocess.CalledProcessError(res.returncode, cmd, res.stdout, res.stderr)
+
+
+def build(verbose=False):
+    """Compile the HIP library, its sources side by side; raises CalledProcessError on failure."""
+    tmp = LIB_PATH + ".tmp"
+    with tempfile.TemporaryDirectory() as d:
+        objects = [os.path.join(d, os.path.basename(f) + ".o") for f in SOURCES]
+        with concurrent.futures.ThreadPoolExecutor(min(8, os.cpu_count() or 1)) as pool:
+            jobs = [pool.submit(_run, hipcc_command(o, ("-c",), [f]), verbose) for f, o in zip(SOURCES, objects)]
+            for j in jobs:
+                j.result()
+        _run(hipcc_command(tmp, ("-shared",), objects), verbose)
     os.replace(tmp, LIB_PATH)
     return LIB_PATH
 

@@ -1,0 +1,396 @@
+// Norms before and after a block with its gate and residual scale (gfx950),
+// forward and backward.  For a row of `dim` values of a token and head, with
+// m(x) = (sum x^2 / dim + eps)^-1/2,
+//   n = wo a m(a)  (or a),   u = n act(z)  (or n),   h = res + scale u,   y = wi h m(h)
+// Backward, from dh and dy,
+//   H = dh + m(h) wi dy - h m(h)^3 sum(h wi dy) / dim,   dres = H,   du = scale H
+//   dz = du n act'(z),   dn = du act(z)
+//   da = m(a) wo dn - a m(a)^3 sum(a wo dn) / dim  (or dn)
+//   dwi = sum of dy h m(h), dwo = sum of dn a m(a) over all rows
+//
+// LANES lanes hold a row, R pieces of eight values each (16-byte accesses in
+// 16-bit types), so that every value is read and written once; statistics are
+// in fp32.  Bound by memory traffic.
+#include "lq_layer_device.h"
+
+namespace lq {
+
+__device__ __forceinline__ float block_act(int gate, float z) {
+  const float s = sigmoid(z);
+  return gate == 1 ? z * s : s;
+}
+
+// The sum of a row's values: LANES lanes side by side, or a workgroup of LANES
+// threads, through `sh` ([2][LANES / 64], the halves in turn: a half is written
+// again only behind the next sum's barrier).
+template <int LANES>
+__device__ __forceinline__ float row_sum(float x, float *sh, int &turn) {
+  if constexpr (LANES == 16) return row16_sum(x);
+  x = wave_sum(x);
+  if constexpr (LANES == 64) return x;
+  constexpr int waves = LANES / 64;
+  float *s = sh + (turn ^= waves);
+  if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = x;
+  __syncthreads();
+  float y = 0.f;
+#pragma unroll
+  for (int w = 0; w < waves; ++w) y += s[w];
+  return y;
+}
+
+template <int LANES>
+constexpr int norm_threads() { return LANES > 256 ? LANES : 256; }
+
+// A row's arguments as a lane uses them
+struct BlockRow {
+  int64_t t;
+  int h, col;  // col: the lane's first value of piece 0; piece r is LANES * 8 further
+  bool on;
+};
+template <int LANES>
+__device__ __forceinline__ BlockRow block_row(const BlockNormArgs &A, int64_t row, int64_t rows) {
+  BlockRow b;
+  b.on = row < rows;
+  const int64_t r = b.on ? row : rows - 1;
+  b.t = r / A.heads;
+  b.h = (int)(r % A.heads);
+  b.col = (threadIdx.x & (LANES - 1)) * 8;
+  return b;
+}
+
+template <class E>
+__device__ __forceinline__ Raw8<E> block_load(const Rows &r, const BlockRow &b, int col, int dim) {
+  // (past the row's end: its beginning again, not used)
+  return raw_load(at<const E>(r, b.t, b.h) + (col < dim ? col : 0));
+}
+__device__ __forceinline__ void block_weights(const float *w, int col, int dim, float (&x)[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] = 1.f;
+  if (w && col < dim) load8(reinterpret_cast<const F32 *>(w + col), x);
+}
+
+template <class E, class S, int LANES, int R>
+__global__ __launch_bounds__(norm_threads<LANES>()) void block_norm_kernel(const BlockNormArgs A, int64_t rows) {
+  __shared__ float sh[LANES > 64 ? 2 * (LANES / 64) : 1];
+  int turn = 0;
+  constexpr int per = norm_threads<LANES>() / LANES;
+  const BlockRow b = block_row<LANES>(A, (int64_t)blockIdx.x * per + threadIdx.x / LANES, rows);
+  const bool gate = A.gate, res = A.res.ptr;
+  Raw8<E> ra[R], rz[R];
+  Raw8<S> rr[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int col = b.col + r * LANES * 8;
+    ra[r] = block_load<E>(A.a, b, col, A.dim);
+    if (gate) rz[r] = block_load<E>(A.z, b, col, A.dim);
+    if (res) rr[r] = block_load<S>(A.res, b, col, A.dim);
+  }
+  float x[R][8];
+  float ss = 0.f;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    raw_floats(x[r], ra[r]);
+    if (b.col + r * LANES * 8 < A.dim) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ss = fmaf(x[r][e], x[r][e], ss);
+    }
+  }
+  const float inv = 1.f / (float)A.dim;
+  if (A.out_norm) {
+    const float m = 1.f / sqrtf(fmaf(row_sum<LANES>(ss, sh, turn), inv, A.eps));
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      float w[8];
+      block_weights(A.wo, b.col + r * LANES * 8, A.dim, w);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[r][e] *= m * w[e];
+    }
+  }
+  ss = 0.f;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int col = b.col + r * LANES * 8;
+    if (gate) {
+      float z[8];
+      raw_floats(z, rz[r]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[r][e] *= block_act(A.gate, z[e]);
+    }
+    float s[8];
+    if (res) raw_floats(s, rr[r]);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[r][e] = res ? fmaf(A.scale, x[r][e], s[e]) : A.scale * x[r][e];
+    if (col < A.dim) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ss = fmaf(x[r][e], x[r][e], ss);
+      if (A.h.ptr && b.on) store8(at<S>(A.h, b.t, b.h) + col, x[r]);
+    }
+  }
+  if (!A.y.ptr) return;
+  const float m = 1.f / sqrtf(fmaf(row_sum<LANES>(ss, sh, turn), inv, A.eps));
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int col = b.col + r * LANES * 8;
+    float w[8];
+    block_weights(A.wi, col, A.dim, w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[r][e] *= m * w[e];
+    if (col < A.dim && b.on) store8(at<E>(A.y, b.t, b.h) + col, x[r]);
+  }
+}
+
+// Workgroups of the backward pass hold their weight gradients in registers and
+// take rows in turn.
+constexpr int kBlockNormBlocks = 1024;
+
+template <class E, class S, int LANES, int R>
+__global__ __launch_bounds__(norm_threads<LANES>()) void block_norm_backward_kernel(const BlockNormArgs A, int64_t rows) {
+  constexpr int threads = norm_threads<LANES>(), per = threads / LANES;
+  __shared__ float sh[LANES > 64 ? 2 * (LANES / 64) : 1];
+  __shared__ float sh_w[per > 1 ? 4 : 1][per > 1 ? LANES * R * 8 : 1];
+  int turn = 0;
+  const bool gate = A.gate, res = A.res.ptr, dy = A.dy.ptr, dh = A.dh.ptr;
+  const float inv = 1.f / (float)A.dim;
+  float dwo[R][8], dwi[R][8];
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) dwo[r][e] = dwi[r][e] = 0.f;
+  // whole rounds: every thread meets every barrier, past the end with the last row again
+  for (int64_t row0 = (int64_t)blockIdx.x * per; row0 < rows; row0 += (int64_t)gridDim.x * per) {
+    const BlockRow b = block_row<LANES>(A, row0 + threadIdx.x / LANES, rows);
+    Raw8<E> ra[R], rz[R], ry[R];
+    Raw8<S> rr[R], rh[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int col = b.col + r * LANES * 8;
+      ra[r] = block_load<E>(A.a, b, col, A.dim);
+      if (gate) rz[r] = block_load<E>(A.z, b, col, A.dim);
+      if (res && dy) rr[r] = block_load<S>(A.res, b, col, A.dim);
+      if (dy) ry[r] = block_load<E>(A.dy, b, col, A.dim);
+      if (dh) rh[r] = block_load<S>(A.dh, b, col, A.dim);
+    }
+    float ma = 1.f;
+    if (A.out_norm) {
+      float ss = 0.f;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        if (b.col + r * LANES * 8 >= A.dim) continue;
+        float a[8];
+        raw_floats(a, ra[r]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ss = fmaf(a[e], a[e], ss);
+      }
+      ma = 1.f / sqrtf(fmaf(row_sum<LANES>(ss, sh, turn), inv, A.eps));
+    }
+    // n, act(z) and its derivative of a piece
+    const auto forward = [&](int r, float (&n)[8], float (&act)[8], float (&slope)[8]) {
+      raw_floats(n, ra[r]);
+      if (A.out_norm) {
+        float w[8];
+        block_weights(A.wo, b.col + r * LANES * 8, A.dim, w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) n[e] *= ma * w[e];
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) act[e] = 1.f, slope[e] = 0.f;
+      if (gate) {
+        float z[8];
+        raw_floats(z, rz[r]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float s = sigmoid(z[e]);
+          act[e] = A.gate == 1 ? z[e] * s : s;
+          slope[e] = A.gate == 1 ? s * fmaf(z[e], 1.f - s, 1.f) : s * (1.f - s);
+        }
+      }
+    };
+    float mh = 0.f, c = 0.f;
+    if (dy) {
+      float ss = 0.f, hg = 0.f;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const int col = b.col + r * LANES * 8;
+        if (col >= A.dim) continue;
+        float h[8], act[8], slope[8], s[8], w[8], g[8];
+        forward(r, h, act, slope);
+        if (res) raw_floats(s, rr[r]);
+        block_weights(A.wi, col, A.dim, w);
+        raw_floats(g, ry[r]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float u = h[e] * act[e], x = res ? fmaf(A.scale, u, s[e]) : A.scale * u;
+          ss = fmaf(x, x, ss);
+          hg = fmaf(x, w[e] * g[e], hg);
+        }
+      }
+      ss = row_sum<LANES>(ss, sh, turn);
+      hg = row_sum<LANES>(hg, sh, turn);
+      mh = 1.f / sqrtf(fmaf(ss, inv, A.eps));
+      c = hg * inv * mh * mh;
+    }
+    float dn[R][8], ag = 0.f;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int col = b.col + r * LANES * 8;
+      if (col >= A.dim) continue;
+      float n[8], act[8], slope[8], H[8];
+      forward(r, n, act, slope);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) H[e] = 0.f;
+      if (dh) raw_floats(H, rh[r]);
+      if (dy) {
+        float s[8], w[8], g[8];
+        if (res) raw_floats(s, rr[r]);
+        block_weights(A.wi, col, A.dim, w);
+        raw_floats(g, ry[r]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float u = n[e] * act[e], x = res ? fmaf(A.scale, u, s[e]) : A.scale * u;
+          H[e] += mh * fmaf(-x, c, w[e] * g[e]);
+          dwi[r][e] += b.on ? g[e] * (x * mh) : 0.f;
+        }
+      }
+      if (A.dres.ptr && b.on) store8(at<S>(A.dres, b.t, b.h) + col, H);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) H[e] *= A.scale;
+      if (gate) {
+        float dz[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dz[e] = H[e] * n[e] * slope[e];
+        if (b.on) store8(at<E>(A.dz, b.t, b.h) + col, dz);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) dn[r][e] = H[e] * act[e];
+      if (A.out_norm) {
+        float a[8], w[8];
+        raw_floats(a, ra[r]);
+        block_weights(A.wo, col, A.dim, w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          dwo[r][e] += b.on ? dn[r][e] * (a[e] * ma) : 0.f;
+          dn[r][e] *= w[e];
+          ag = fmaf(a[e], dn[r][e], ag);
+        }
+      }
+    }
+    if (A.out_norm) {
+      const float ca = row_sum<LANES>(ag, sh, turn) * inv * ma * ma;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        float a[8];
+        raw_floats(a, ra[r]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dn[r][e] = ma * fmaf(-a[e], ca, dn[r][e]);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int col = b.col + r * LANES * 8;
+      if (col < A.dim && b.on) store8(at<E>(A.da, b.t, b.h) + col, dn[r]);
+    }
+  }
+  if (!A.dwo && !A.dwi) return;  // the whole block
+  // a workgroup's rows meet, then its sums go to `part`
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    if constexpr (per == 1) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const int col = (int)threadIdx.x * 8 + r * LANES * 8;
+        if (col < A.dim)
+          store8(reinterpret_cast<F32 *>(A.part + ((int64_t)blockIdx.x * 2 + p) * A.dim + col), p ? dwi[r] : dwo[r]);
+      }
+    } else {
+      const int lane = threadIdx.x & 63, w4 = threadIdx.x >> 6;
+      if (p) __syncthreads();
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          float x = p ? dwi[r][e] : dwo[r][e];
+          if (LANES == 16) {
+            x += __shfl_xor(x, 16);
+            x += __shfl_xor(x, 32);
+          }
+          if (lane < LANES) sh_w[w4][r * LANES * 8 + lane * 8 + e] = x;
+        }
+      __syncthreads();
+      for (int d = threadIdx.x; d < A.dim; d += threads)
+        A.part[((int64_t)blockIdx.x * 2 + p) * A.dim + d] =
+            ((sh_w[0][d] + sh_w[1][d]) + sh_w[2][d]) + sh_w[3][d];
+    }
+  }
+}
+
+// The workgroups' weight gradients, added in order: workgroup (which, 64
+// values), wave (a share of the workgroups)
+__global__ __launch_bounds__(1024) void block_norm_weight_kernel(const BlockNormArgs A, int64_t blocks) {
+  __shared__ float sh[16][64];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, p = blockIdx.x & 1;
+  const int d = (int)(blockIdx.x >> 1) * 64 + lane;
+  float x = 0.f;
+  if (d < A.dim) {
+#pragma unroll 8
+    for (int64_t n = w; n < blocks; n += 16) x += A.part[(n * 2 + p) * A.dim + d];
+  }
+  sh[w][lane] = x;
+  __syncthreads();
+  float *out = p ? A.dwi : A.dwo;
+  if (w || d >= A.dim || !out) return;
+  float y = 0.f;
+#pragma unroll
+  for (int v = 0; v < 16; ++v) y += sh[v][lane];
+  out[d] = y;
+}
+
+// Lanes of a row by its width: sixteen up to 128 values (the usual head), a
+// wave up to 1,024, workgroups beyond.
+static int norm_lanes(int dim) { return dim <= 128 ? 16 : dim <= 1024 ? 64 : dim <= 4096 ? 256 : 512; }
+
+int64_t block_norm_blocks(int64_t rows, int dim) {
+  const int lanes = norm_lanes(dim), per = lanes < 256 ? 256 / lanes : 1;
+  const int64_t b = (rows + per - 1) / per;
+  return b < kBlockNormBlocks ? b : kBlockNormBlocks;
+}
+
+template <class E, class S, int LANES, int R>
+static hipError_t norm_rows(const BlockNormArgs &a, bool back, hipStream_t stream) {
+  constexpr int threads = norm_threads<LANES>(), per = threads / LANES;
+  const int64_t rows = a.tokens * a.heads;
+  if (!back) {
+    hipLaunchKernelGGL((block_norm_kernel<E, S, LANES, R>), dim3((unsigned)((rows + per - 1) / per)), dim3(threads), 0,
+                       stream, a, rows);
+    return hipGetLastError();
+  }
+  const int64_t blocks = block_norm_blocks(rows, a.dim);
+  if (blocks)
+    hipLaunchKernelGGL((block_norm_backward_kernel<E, S, LANES, R>), dim3((unsigned)blocks), dim3(threads), 0, stream, a,
+                       rows);
+  if (a.dwo || a.dwi)
+    hipLaunchKernelGGL(block_norm_weight_kernel, dim3((unsigned)((a.dim + 63) / 64 * 2)), dim3(1024), 0, stream, a, blocks);
+  return hipGetLastError();
+}
+template <class E, class S>
+static hipError_t norm_dim(const BlockNormArgs &a, bool back, hipStream_t stream) {
+  if (a.dim <= 128) return norm_rows<E, S, 16, 1>(a, back, stream);
+  if (a.dim <= 512) return norm_rows<E, S, 64, 1>(a, back, stream);
+  if (a.dim <= 1024) return norm_rows<E, S, 64, 2>(a, back, stream);
+  if (a.dim <= 2048) return norm_rows<E, S, 256, 1>(a, back, stream);
+  if (a.dim <= 4096) return norm_rows<E, S, 256, 2>(a, back, stream);
+  return norm_rows<E, S, 512, 2>(a, back, stream);
+}
+static hipError_t norm_types(const BlockNormArgs &a, int dtype, int stream_dtype, bool back, hipStream_t stream) {
+  if (dtype == 0) return norm_dim<F32, F32>(a, back, stream);
+  if (dtype == 1)
+    return stream_dtype == 0 ? norm_dim<BF16, F32>(a, back, stream) : norm_dim<BF16, BF16>(a, back, stream);
+  return stream_dtype == 0 ? norm_dim<F16, F32>(a, back, stream) : norm_dim<F16, F16>(a, back, stream);
+}
+hipError_t launch_block_norm(const BlockNormArgs &a, int dtype, int stream_dtype, hipStream_t stream) {
+  return norm_types(a, dtype, stream_dtype, false, stream);
+}
+hipError_t launch_block_norm_backward(const BlockNormArgs &a, int dtype, int stream_dtype, hipStream_t stream) {
+  return norm_types(a, dtype, stream_dtype, true, stream);
+}
+
+}  // namespace lq

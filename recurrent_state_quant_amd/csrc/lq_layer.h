@@ -1,0 +1,122 @@
+// Internal launch interface between the entry points of the operators around
+// the recurrence (lq_layer_abi.cpp) and their gfx950 kernels (lq_conv.hip,
+// lq_scan.hip, lq_scan_grad.hip, lq_block_norm.hip).  Arguments are validated
+// by the caller.
+#pragma once
+#include <stdint.h>
+#include <hip/hip_runtime_api.h>
+
+#include "lq_sequence.h"
+
+namespace lq {
+
+// [tokens][channels] arrays are Rows whose head stride is not used.
+
+struct ConvArgs {
+  int64_t tokens;  // rows of the step
+  int seqs, channels, width, silu;
+  const int32_t *cu;
+  Rows x, y;
+  const float *w;     // [channels][width]
+  const float *bias;  // [channels] or nullptr
+  const void *X0;     // [seqs or slots][width - 1][channels] or nullptr (zeros)
+  void *X;
+  const int32_t *slots;  // step: [rows] or nullptr (row i has slot i)
+  int n_slots;
+  // backward
+  Rows dy, dx;
+  const void *dX;
+  void *dX0;
+  float *dw, *dbias;
+  float *part;  // [blocks of runs][width + 1][channels]
+};
+
+// Tokens of a run of the backward pass: a block takes four runs of the same
+// channels and joins their weight gradients.  Runs grow once there are 256
+// blocks of them, so the joined sums stay few.
+constexpr int kConvRunLeast = 32, kConvRunMost = 4096;
+constexpr int64_t kConvBlocks = 256;
+inline int conv_grad_run(int64_t tokens) {
+  int run = kConvRunLeast;
+  while (run < kConvRunMost && tokens > int64_t(run) * 4 * kConvBlocks) run *= 2;
+  return run;
+}
+inline int64_t conv_grad_blocks(int64_t tokens, int64_t run) { return (tokens + 4 * run - 1) / (4 * run); }
+inline int64_t conv_grad_blocks(int64_t tokens) { return conv_grad_blocks(tokens, conv_grad_run(tokens)); }
+// The most blocks of any call with at most these tokens
+inline int64_t conv_grad_most(int64_t tokens) {
+  const int64_t few = conv_grad_blocks(tokens, kConvRunLeast), many = conv_grad_blocks(tokens, kConvRunMost);
+  return few < kConvBlocks ? few : many > kConvBlocks ? many : kConvBlocks;
+}
+
+struct ScanArgs {
+  int64_t tokens, slots;
+  int seqs, channels, groups, per;  // per: channels of a group
+  int shift;                        // chunks of 2^shift tokens
+  int softplus;
+  const int32_t *cu;
+  Rows x, dt, z, y, B, C;  // z.ptr may be nullptr
+  const float *A, *skip, *bias;
+  const float *S0;  // [seqs][channels][states] or nullptr (zeros)
+  float *S;         // or nullptr
+  float *check;     // [sub slots][states][channels] or nullptr: the state before every kSub(states)-th token of a sequence
+  float *carry;     // [slots][states][channels]  chunks of sequences with several: the state before (backward: gradient behind)
+  float *sum;       // [slots][channels]          the sum of a chunk's steps
+  // step
+  const int32_t *which;  // [rows] or nullptr
+  int n_slots;
+  // backward
+  Rows dy, dx, ddt, dB, dC, dz;
+  float *dA, *dskip, *dbias;
+  const float *dS;
+  float *dS0;
+  float *part_bc;  // [groups * blocks][tokens][2 * states]
+  float *part_a;   // [slots][states + 2][channels]
+};
+
+// Tokens whose states the gradient holds in registers at once: 8 x 16 or 4 x 32
+// values a channel.
+constexpr int scan_sub_shift(int states) { return states > 16 ? 2 : 3; }
+
+// Waves take 64 channels of one group and one chunk of tokens.
+inline int64_t scan_tiles(int channels, int groups) {
+  return int64_t(groups) * ((channels / groups + 63) / 64);
+}
+// Chunks of 32 to 512 tokens, so many that about 4,096 waves have one.
+constexpr int kScanLeast = 5, kScanMost = 9;
+constexpr int64_t kScanWaves = 4096;
+inline int scan_shift(int64_t tokens, int64_t tiles) {
+  int s = kScanLeast;
+  while (s < kScanMost && tokens * tiles > (kScanWaves << s)) ++s;
+  return s;
+}
+// Slots of chunks: sequence i, chunk c has slot (cu[i] >> shift) + i + c.
+inline int64_t scan_slots(int64_t tokens, int64_t seqs, int shift) { return (tokens >> shift) + seqs; }
+// Blocks of four waves that share a group (backward)
+inline int64_t scan_group_blocks(int per) { return (per + 255) / 256; }
+
+struct BlockNormArgs {
+  int64_t tokens;
+  int heads, dim;
+  int gate, out_norm;  // gate: 0 none, 1 silu, 2 sigmoid
+  float eps, scale;
+  Rows a, z, res, h, y;  // res.ptr, h.ptr, y.ptr may be nullptr
+  const float *wo, *wi;  // [dim] or nullptr (ones)
+  // backward
+  Rows dh, dy, da, dz, dres;  // dh.ptr, dy.ptr, dres.ptr may be nullptr
+  float *dwo, *dwi;           // [dim] or nullptr
+  float *part;                // [blocks][2][dim]
+};
+
+// dtype: 0 fp32, 1 bf16, 2 fp16
+hipError_t launch_conv(const ConvArgs &a, int dtype, bool wide, hipStream_t stream);
+hipError_t launch_conv_step(const ConvArgs &a, int dtype, bool wide, hipStream_t stream);
+hipError_t launch_conv_backward(const ConvArgs &a, int dtype, bool wide, hipStream_t stream);
+hipError_t launch_scan(const ScanArgs &a, int dtype, int states, hipStream_t stream);
+hipError_t launch_scan_step(const ScanArgs &a, int dtype, int states, hipStream_t stream);
+hipError_t launch_scan_backward(const ScanArgs &a, int dtype, int states, hipStream_t stream);
+int64_t block_norm_blocks(int64_t rows, int dim);  // workgroups of the backward pass
+hipError_t launch_block_norm(const BlockNormArgs &a, int dtype, int stream_dtype, hipStream_t stream);
+hipError_t launch_block_norm_backward(const BlockNormArgs &a, int dtype, int stream_dtype, hipStream_t stream);
+
+}  // namespace lq

@@ -1,0 +1,223 @@
+// The selective state space scan over packed sequences, and for single tokens
+// (gfx950).  For every channel c of group g, with N states,
+//   d = softplus(dt + bias),  h_n <- e^(d A_n) h_n + d B_n x,
+//   y = (sum_n C_n h_n + D x) silu(z)
+//
+// A lane holds a channel with all of its states, so that B and C are the same
+// for a wave and come through the scalar cache, and y needs no sum across
+// lanes.  A wave takes 64 channels and one chunk of tokens; sequences of several
+// chunks take three launches: every chunk's states from zero and the sum of its
+// steps (the whole chunk decays by e^(A sum)), the states before every chunk
+// from these, and the tokens again from there.  Chunks of 32 to 512 tokens give
+// about 4,096 waves, four a SIMD.
+#include "lq_scan_device.h"
+
+namespace lq {
+
+constexpr int kScanAhead = 8;  // tokens whose inputs are loaded together
+
+// OUT: the chunks' outputs from the states before them; otherwise the chunks'
+// states from zero.
+template <class E, int N, bool OUT>
+__global__ __launch_bounds__(256) void scan_kernel(const ScanArgs A, int tiles, int64_t waves) {
+  const int lane = threadIdx.x & 63;
+  const int64_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) + (int64_t)blockIdx.x * 4;
+  if (wave >= waves) return;  // whole waves; the waves share nothing
+  const int slot = (int)(wave / tiles), tile = (int)(wave % tiles), tg = (A.per + 63) >> 6;
+  const ScanChunk k = scan_chunk(A, slot, lane);
+  if (!k.any || (!OUT && k.c + 1 >= k.chunks)) return;  // nothing comes behind the last chunk
+  const ScanTile ch = scan_tile(A, tile / tg, tile % tg, lane);
+  const int64_t width = A.channels;
+  float a2[N], h[N], sum = 0.f;
+  scan_decays<N>(A, ch.c, a2);
+#pragma unroll
+  for (int n = 0; n < N; ++n) h[n] = 0.f;
+  if (OUT) {
+    if (k.chunks > 1)
+      scan_load_cols<N>(A.carry + (int64_t)slot * N * width, width, ch.c, h);
+    else if (A.S0)
+      scan_load_rows<N>(A.S0, k.i * width + ch.c, h);
+  }
+  const float bias = A.bias ? A.bias[ch.c] : 0.f, skip = OUT && A.skip ? A.skip[ch.c] : 0.f;
+  const bool gate = OUT && A.z.ptr;
+  const E *x = at<const E>(A.x, 0, 0) + ch.c, *dt = at<const E>(A.dt, 0, 0) + ch.c;
+  const E *z = gate ? at<const E>(A.z, 0, 0) + ch.c : x;
+  E *y = OUT ? at<E>(A.y, 0, 0) + ch.c : nullptr;
+  constexpr int sub = 1 << scan_sub_shift(N);
+  E rx[kScanAhead], rd[kScanAhead], rz[kScanAhead];
+  const auto load = [&](int t) {
+#pragma unroll
+    for (int u = 0; u < kScanAhead; ++u) {
+      const int64_t tt = min(t + u, k.t1 - 1);
+      rx[u] = x[tt * A.x.ts];
+      rd[u] = dt[tt * A.dt.ts];
+      if (gate) rz[u] = z[tt * A.z.ts];
+    }
+  };
+  if (k.t0 < k.t1) load(k.t0);
+  for (int t = k.t0; t < k.t1; t += kScanAhead) {
+    float fx[kScanAhead], fd[kScanAhead], fz[kScanAhead];
+#pragma unroll
+    for (int u = 0; u < kScanAhead; ++u) {
+      fx[u] = to_f(rx[u]);
+      fd[u] = to_f(rd[u]) + bias;
+      fz[u] = gate ? to_f(rz[u]) : 0.f;
+    }
+    if (t + kScanAhead < k.t1) load(t + kScanAhead);
+#pragma unroll
+    for (int u = 0; u < kScanAhead; ++u) {
+      const int tt = t + u;
+      if (tt >= k.t1) break;
+      if (OUT && A.check && u % sub == 0) {
+        const int64_t s = (k.start >> scan_sub_shift(N)) + k.i + ((tt - k.start) >> scan_sub_shift(N));
+        if (ch.on) scan_store_cols<N>(A.check + s * N * width, width, ch.c, h);
+      }
+      float b[N];
+      scan_row<E, N>(A.B, tt, ch.g, b);
+      const float d = scan_step(A, fd[u]), dx = d * fx[u];
+      sum += d;
+#pragma unroll
+      for (int n = 0; n < N; ++n) h[n] = fmaf(__builtin_amdgcn_exp2f(d * a2[n]), h[n], dx * b[n]);
+      if (OUT) {
+        float cc[N];
+        scan_row<E, N>(A.C, tt, ch.g, cc);
+        float p0 = skip * fx[u], p1 = 0.f;
+#pragma unroll
+        for (int n = 0; n < N; n += 2) {
+          p0 = fmaf(cc[n], h[n], p0);
+          p1 = fmaf(cc[n + 1], h[n + 1], p1);
+        }
+        float p = p0 + p1;
+        if (gate) p *= fz[u] * sigmoid(fz[u]);
+        if (ch.on) y[tt * A.y.ts] = from_f<E>(p);
+      }
+    }
+  }
+  if (!ch.on) return;
+  if (!OUT) {
+    scan_store_cols<N>(A.carry + (int64_t)slot * N * width, width, ch.c, h);
+    A.sum[slot * width + ch.c] = sum;
+  } else if (A.S && k.c + 1 >= k.chunks) {
+    scan_store_rows<N>(A.S, k.i * width + ch.c, h);
+  }
+}
+
+// The states before every chunk of the sequences with several, over the chunks'
+// states from zero: thread (sequence, state, channel).  S0 is copied before the
+// first chunk, as S may lie over it.
+constexpr int kCarryAhead = 8;
+__global__ __launch_bounds__(256) void scan_carry_kernel(const ScanArgs A, int states, int64_t threads) {
+  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (id >= threads) return;
+  const int64_t width = A.channels, c = id % width, n = id / width % states, i = id / width / states;
+  const auto offset = [&](int64_t s) {
+    const int o = A.cu[s];
+    return o < 0 ? 0 : (o > A.tokens ? (int)A.tokens : o);
+  };
+  const int start = offset(i), end = max(start, offset(i + 1));
+  const int chunks = (end - start + (1 << A.shift) - 1) >> A.shift;
+  if (chunks < 2) return;
+  const int64_t slot = (start >> A.shift) + i;
+  const float a2 = A.A[c * states + n] * kLog2e;
+  float h = A.S0 ? A.S0[(i * width + c) * states + n] : 0.f;
+  float *carry = A.carry + (slot * states + n) * width + c;
+  const float *sum = A.sum + slot * width + c;
+  const int64_t step = states * width;
+  for (int k = 0; k < chunks; k += kCarryAhead) {
+    float v[kCarryAhead], s[kCarryAhead];
+#pragma unroll
+    for (int u = 0; u < kCarryAhead; ++u) {
+      const bool in = k + u + 1 < chunks;
+      v[u] = in ? carry[(k + u) * step] : 0.f;
+      s[u] = in ? sum[(k + u) * width] : 0.f;
+    }
+#pragma unroll
+    for (int u = 0; u < kCarryAhead; ++u) {
+      if (k + u >= chunks) break;
+      carry[(k + u) * step] = h;
+      h = fmaf(__builtin_amdgcn_exp2f(s[u] * a2), h, v[u]);
+    }
+  }
+}
+
+// One token of each row.  Four states a lane, the lanes of a channel side by
+// side, so that the states move in whole lines; bound by reading and writing
+// them.
+template <class E, int N>
+__global__ __launch_bounds__(256) void scan_step_kernel(const ScanArgs A, int64_t blocks_row) {
+  constexpr int lanes = N / 4;
+  const int64_t row = blockIdx.x / blocks_row;
+  const int64_t id = (blockIdx.x % blocks_row) * 256 + threadIdx.x;
+  const int64_t slot = A.which ? A.which[row] : row;
+  if (slot < 0 || slot >= A.n_slots) return;  // the whole block
+  const bool on = id < (int64_t)A.channels * lanes;
+  const int64_t c = on ? id / lanes : A.channels - 1;
+  const int n = (int)(id % lanes) * 4, g = (int)(c / A.per);
+  const int64_t at_s = (slot * A.channels + c) * N + n;
+  const vf4 h0 = __builtin_nontemporal_load(reinterpret_cast<const vf4 *>(A.S0 + at_s));
+  const float4 a = *reinterpret_cast<const float4 *>(A.A + c * N + n);
+  const float x = to_f(at<const E>(A.x, row, 0)[c]);
+  const float v = to_f(at<const E>(A.dt, row, 0)[c]) + (A.bias ? A.bias[c] : 0.f);
+  float b[4], cc[4];
+  load4(at<const E>(A.B, row, g) + n, b);
+  load4(at<const E>(A.C, row, g) + n, cc);
+  const float d = scan_step(A, v), dx = d * x, d2 = d * kLog2e;
+  vf4 h;
+  h.x = fmaf(__builtin_amdgcn_exp2f(d2 * a.x), h0.x, dx * b[0]);
+  h.y = fmaf(__builtin_amdgcn_exp2f(d2 * a.y), h0.y, dx * b[1]);
+  h.z = fmaf(__builtin_amdgcn_exp2f(d2 * a.z), h0.z, dx * b[2]);
+  h.w = fmaf(__builtin_amdgcn_exp2f(d2 * a.w), h0.w, dx * b[3]);
+  float p = fmaf(cc[0], h.x, cc[1] * h.y) + fmaf(cc[2], h.z, cc[3] * h.w);
+  if (lanes >= 2) p += dpp<0xB1>(p);
+  if (lanes >= 4) p += dpp<0x4E>(p);
+  if (lanes >= 8) p += dpp<0x141>(p);
+  if (!on) return;
+  __builtin_nontemporal_store(h, reinterpret_cast<vf4 *>(A.S + at_s));
+  if (n == 0) {
+    p = fmaf(A.skip ? A.skip[c] : 0.f, x, p);
+    if (A.z.ptr) {
+      const float z = to_f(at<const E>(A.z, row, 0)[c]);
+      p *= z * sigmoid(z);
+    }
+    at<E>(A.y, row, 0)[c] = from_f<E>(p);
+  }
+}
+
+template <class E, int N>
+static hipError_t scan_run(const ScanArgs &a, bool step, hipStream_t stream) {
+  if (step) {
+    const int64_t blocks_row = ((int64_t)a.channels * (N / 4) + 255) / 256;
+    if (a.tokens)
+      hipLaunchKernelGGL((scan_step_kernel<E, N>), dim3((unsigned)(a.tokens * blocks_row)), dim3(256), 0, stream, a,
+                         blocks_row);
+    return hipGetLastError();
+  }
+  const int64_t tiles = scan_tiles(a.channels, a.groups), waves = tiles * a.slots;
+  const dim3 grid((unsigned)((waves + 3) / 4));
+  if (a.tokens > (int64_t(1) << a.shift)) {  // a sequence may have several chunks
+    hipLaunchKernelGGL((scan_kernel<E, N, false>), grid, dim3(256), 0, stream, a, (int)tiles, waves);
+    const int64_t threads = (int64_t)a.seqs * a.channels * N;
+    hipLaunchKernelGGL(scan_carry_kernel, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, stream, a, N, threads);
+  }
+  hipLaunchKernelGGL((scan_kernel<E, N, true>), grid, dim3(256), 0, stream, a, (int)tiles, waves);
+  return hipGetLastError();
+}
+template <class E>
+static hipError_t scan_run(const ScanArgs &a, int states, bool step, hipStream_t stream) {
+  return states == 8    ? scan_run<E, 8>(a, step, stream)
+         : states == 16 ? scan_run<E, 16>(a, step, stream)
+                        : scan_run<E, 32>(a, step, stream);
+}
+static hipError_t scan_run(const ScanArgs &a, int dtype, int states, bool step, hipStream_t stream) {
+  return dtype == 0 ? scan_run<F32>(a, states, step, stream)
+         : dtype == 1 ? scan_run<BF16>(a, states, step, stream)
+                      : scan_run<F16>(a, states, step, stream);
+}
+hipError_t launch_scan(const ScanArgs &a, int dtype, int states, hipStream_t stream) {
+  return scan_run(a, dtype, states, false, stream);
+}
+hipError_t launch_scan_step(const ScanArgs &a, int dtype, int states, hipStream_t stream) {
+  return scan_run(a, dtype, states, true, stream);
+}
+
+}  // namespace lq

@@ -1,0 +1,124 @@
+// Device-side helpers of the selective scan (lq_scan.hip, lq_scan_grad.hip).
+#pragma once
+#include "lq_layer_device.h"
+
+namespace lq {
+
+// max(v, 0) + log(1 + e), e = e^-|v| in (0, 1].  log(1 + e) = 2 artanh(r) with
+// r = e / (2 + e) <= 1/3, by its series up to r^15 / 15 (the next term is below
+// 2^-28 of the sum): exact to rounding also where e is tiny, as it is for the
+// small steps that such layers take.
+__device__ __forceinline__ float softplus_of(float v, float e) {
+  const float r = e * __builtin_amdgcn_rcpf(2.f + e), q = r * r;
+  float p = fmaf(q, 1.f / 15.f, 1.f / 13.f);
+  p = fmaf(p, q, 1.f / 11.f);
+  p = fmaf(p, q, 1.f / 9.f);
+  p = fmaf(p, q, 1.f / 7.f);
+  p = fmaf(p, q, 1.f / 5.f);
+  p = fmaf(p, q, 1.f / 3.f);
+  p = fmaf(p * q, r, r);
+  return fmaf(2.f, p, fmaxf(v, 0.f));
+}
+// the step of a token and channel from its input v
+__device__ __forceinline__ float scan_step(const ScanArgs &A, float v) {
+  return A.softplus ? softplus_of(v, exp_full(-fabsf(v))) : v;
+}
+// The same with the step's derivative by v.
+__device__ __forceinline__ float scan_step(const ScanArgs &A, float v, float &slope) {
+  slope = 1.f;
+  if (!A.softplus) return v;
+  const float e = exp_full(-fabsf(v)), s = __builtin_amdgcn_rcpf(1.f + e);
+  slope = v >= 0.f ? s : e * s;
+  return softplus_of(v, e);
+}
+
+// A row of B or C: N values that are the same for the whole wave, through the
+// scalar cache (the address is made of wave-uniform values), so that they cost
+// the vector units nothing but their use as an operand.
+template <class E, int N>
+__device__ __forceinline__ void scan_row(const Rows &r, int t, int g, float (&f)[N]) {
+  typedef const uint32_t __attribute__((address_space(4))) *scalars;
+  const scalars p = (scalars)(uintptr_t)at<const E>(r, t, g);
+  constexpr int words = N * (int)sizeof(E) / 4;
+  uint32_t w[words];
+#pragma unroll
+  for (int i = 0; i < words; ++i) w[i] = p[i];
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    if constexpr (sizeof(E) == 4)
+      f[n] = __uint_as_float(w[n]);
+    else
+      f[n] = to_f(__builtin_bit_cast(E, (uint16_t)(w[n >> 1] >> (16 * (n & 1)))));
+  }
+}
+
+// A wave's channels: 64 of one group, one a lane.
+struct ScanTile {
+  int g;        // group
+  int c;        // this lane's channel (of lanes without one: the group's last)
+  bool on;      // this lane has a channel
+};
+__device__ __forceinline__ ScanTile scan_tile(const ScanArgs &A, int g, int tile, int lane) {
+  const int first = tile * 64 + lane;
+  ScanTile r;
+  r.g = g;
+  r.on = first < A.per;
+  r.c = g * A.per + (r.on ? first : A.per - 1);
+  return r;
+}
+
+// The chunk of a slot
+struct ScanChunk {
+  int i, c, chunks;  // sequence, chunk, chunks of the sequence
+  int start, t0, t1; // the sequence's first token, the chunk's tokens [t0, t1)
+  bool any;          // the slot has a chunk (an empty sequence has one of no tokens)
+};
+__device__ __forceinline__ ScanChunk scan_chunk(const ScanArgs &A, int slot, int lane) {
+  ScanChunk k{0, 0, 0, 0, 0, 0, false};
+  k.i = seq_search(A.cu, A.tokens, A.seqs, A.shift, 1, slot, lane);
+  if (k.i < 0) return k;
+  k.start = seq_offset(A.cu, A.tokens, k.i);
+  const int end = max(k.start, seq_offset(A.cu, A.tokens, k.i + 1));
+  k.chunks = (end - k.start + (1 << A.shift) - 1) >> A.shift;
+  k.c = slot - ((k.start >> A.shift) + k.i);
+  if (k.c < 0 || (k.c >= k.chunks && k.c > 0)) return k;
+  k.any = true;
+  k.t0 = k.start + (k.c << A.shift);
+  k.t1 = min(end, k.t0 + (1 << A.shift));
+  return k;
+}
+
+// A channel's states from or to [states][channels] or [channels][states]
+template <int N>
+__device__ __forceinline__ void scan_load_cols(const float *p, int64_t channels, int c, float (&h)[N]) {
+#pragma unroll
+  for (int n = 0; n < N; ++n) h[n] = p[n * channels + c];
+}
+template <int N>
+__device__ __forceinline__ void scan_store_cols(float *p, int64_t channels, int c, const float (&h)[N]) {
+#pragma unroll
+  for (int n = 0; n < N; ++n) p[n * channels + c] = h[n];
+}
+template <int N>
+__device__ __forceinline__ void scan_load_rows(const float *p, int64_t row, float (&h)[N]) {
+#pragma unroll
+  for (int n = 0; n < N; n += 4) {
+    const float4 v = *reinterpret_cast<const float4 *>(p + row * N + n);
+    h[n] = v.x; h[n + 1] = v.y; h[n + 2] = v.z; h[n + 3] = v.w;
+  }
+}
+template <int N>
+__device__ __forceinline__ void scan_store_rows(float *p, int64_t row, const float (&h)[N]) {
+#pragma unroll
+  for (int n = 0; n < N; n += 4)
+    *reinterpret_cast<float4 *>(p + row * N + n) = make_float4(h[n], h[n + 1], h[n + 2], h[n + 3]);
+}
+// decays as exponents of two: e^(d A) = 2^(d A log2 e)
+template <int N>
+__device__ __forceinline__ void scan_decays(const ScanArgs &A, int c, float (&a2)[N]) {
+  scan_load_rows<N>(A.A, c, a2);
+#pragma unroll
+  for (int n = 0; n < N; ++n) a2[n] *= kLog2e;
+}
+
+}  // namespace lq
