@@ -103,7 +103,7 @@ __global__ __launch_bounds__(256) void conv_kernel(const ConvArgs A, int tiles, 
     return;
   }
   const int t0 = (int)(run * kConvRun), t1 = (int)min((int64_t)t0 + kConvRun, A.tokens);
-  ConvSeq q = conv_seq(A, seq_search(A.cu, A.tokens, A.seqs, 0, 0, t0, lane));
+  ConvSeq q = conv_seq(A, seq_search(A.cu, A.tokens, A.seqs, 1, 0, t0, lane));
   if (!on) return;
   float w[K][V], b[V], win[K - 1][V];
   conv_weights<V, K>(A, c, w, b);
@@ -199,7 +199,7 @@ __global__ __launch_bounds__(256) void conv_backward_kernel(const ConvArgs A, in
   const int64_t first = (block * 4 + w4) * run_tokens;
   if (first < A.tokens) {
     const int t0 = (int)first, t1 = (int)min(first + run_tokens, A.tokens);
-    ConvSeq q = conv_seq(A, seq_search(A.cu, A.tokens, A.seqs, 0, 0, t0, lane));
+    ConvSeq q = conv_seq(A, seq_search(A.cu, A.tokens, A.seqs, 1, 0, t0, lane));
     if (on) {
       conv_weights<V, K>(A, c, w, b);
       float win[K - 1][V], acc[K - 1][V];

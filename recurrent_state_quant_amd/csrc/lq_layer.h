@@ -52,7 +52,7 @@ inline int64_t conv_grad_most(int64_t tokens) {
 struct ScanArgs {
   int64_t tokens, slots;
   int seqs, channels, groups, per;  // per: channels of a group
-  int shift;                        // chunks of 2^shift tokens
+  int chunk;                        // tokens of a chunk, a multiple of 8
   int softplus;
   const int32_t *cu;
   Rows x, dt, z, y, B, C;  // z.ptr may be nullptr
@@ -76,24 +76,44 @@ struct ScanArgs {
 
 // Tokens whose states the gradient holds in registers at once: 8 x 16 or 4 x 32
 // values a channel.
-constexpr int scan_sub_shift(int states) { return states > 16 ? 2 : 3; }
+constexpr int scan_sub_shift(int states) { return states > 8 ? 2 : 3; }
+inline int64_t scan_checks(int64_t tokens, int64_t seqs, int states) {
+  return (tokens >> scan_sub_shift(states)) + seqs;
+}
 
 // Waves take 64 channels of one group and one chunk of tokens.
 inline int64_t scan_tiles(int channels, int groups) {
   return int64_t(groups) * ((channels / groups + 63) / 64);
 }
-// Chunks of 32 to 512 tokens, so many that about 4,096 waves have one.
-constexpr int kScanLeast = 5, kScanMost = 9;
-constexpr int64_t kScanWaves = 4096;
-inline int scan_shift(int64_t tokens, int64_t tiles) {
-  int s = kScanLeast;
-  while (s < kScanMost && tokens * tiles > (kScanWaves << s)) ++s;
-  return s;
+// Slots of chunks: sequence i, chunk c has slot cu[i] / chunk + i + c.
+inline int64_t scan_slots(int64_t tokens, int64_t seqs, int chunk) { return tokens / chunk + seqs; }
+// Tokens of a chunk: the workgroups (or waves) of a chunk's channels run in
+// rounds of `at_once`, and the rounds times a chunk's length, with some tokens'
+// time for its beginning, are the time.  Either one round that is nearly full,
+// or many.
+constexpr int kScanLeast = 32, kScanMost = 512, kScanBegin = 12;
+inline int scan_chunk_tokens(int64_t tokens, int64_t seqs, int64_t units, int64_t at_once) {
+  int best = kScanLeast;
+  int64_t least = INT64_MAX;
+  for (int chunk = kScanLeast; chunk <= kScanMost; chunk += 8) {
+    // (half a chunk more for each sequence, as its last one is partly full)
+    const int64_t rounds = ((tokens / chunk + (seqs + 1) / 2) * units + at_once - 1) / at_once;
+    const int64_t time = rounds * (chunk + kScanBegin);
+    if (time < least) least = time, best = chunk;
+    if (rounds <= 1) break;
+  }
+  return best;
 }
-// Slots of chunks: sequence i, chunk c has slot (cu[i] >> shift) + i + c.
-inline int64_t scan_slots(int64_t tokens, int64_t seqs, int shift) { return (tokens >> shift) + seqs; }
 // Blocks of four waves that share a group (backward)
 inline int64_t scan_group_blocks(int per) { return (per + 255) / 256; }
+// What the chip holds at once: waves of the forward kernel, four a SIMD (three
+// with 32 states), workgroups of the gradient, two a CU (one with 32).
+inline int scan_forward_chunk(int64_t tokens, int64_t seqs, int channels, int groups, int states) {
+  return scan_chunk_tokens(tokens, seqs, scan_tiles(channels, groups), states > 16 ? 3072 : 4096);
+}
+inline int scan_grad_chunk(int64_t tokens, int64_t seqs, int channels, int groups, int states) {
+  return scan_chunk_tokens(tokens, seqs, groups * scan_group_blocks(channels / groups), states > 16 ? 256 : 512);
+}
 
 struct BlockNormArgs {
   int64_t tokens;

@@ -78,7 +78,7 @@ int check_scan(const lq_scan *sc, bool step) {
   // gradient a workgroup for each 256 channels of a group), the states of all
   // sequences, and the gradient's sums of B and C
   const int64_t tiles = lq::scan_tiles(sc->channels, sc->groups);
-  const int64_t slots = lq::scan_slots(sc->tokens, sc->seqs, lq::scan_shift(sc->tokens, tiles));
+  const int64_t slots = lq::scan_slots(sc->tokens, sc->seqs, lq::kScanLeast);
   if (slots > kMaxGrid / (sc->groups * lq::scan_group_blocks(sc->channels / sc->groups))) return LQ_ERR_SHAPE;
   if (slots > kMaxGrid / ((tiles + 3) / 4)) return LQ_ERR_SHAPE;
   if (int64_t(sc->channels) * sc->states > (kMaxGrid * 256) / sc->seqs) return LQ_ERR_SHAPE;
@@ -87,15 +87,18 @@ int check_scan(const lq_scan *sc, bool step) {
 }
 
 // The arrays of the workspace, one behind another from `base`; returns the
-// bytes they take.
-int64_t scan_space(const lq_scan *sc, int64_t slots, bool save, char *base, lq::ScanArgs *a) {
+// bytes they take: room for the shortest chunks, so that more tokens or
+// sequences never need less.
+int64_t scan_space(const lq_scan *sc, bool save, char *base, lq::ScanArgs *a) {
   const int64_t channels = sc->channels, state = channels * sc->states * 4;
+  const int64_t slots = lq::scan_slots(sc->tokens, sc->seqs, lq::kScanLeast);
   int64_t used = 0;
   const auto take = [&](auto **p, int64_t bytes) {
     if (base) *p = reinterpret_cast<std::remove_reference_t<decltype(*p)>>(base + used);
     used += (bytes + 15) / 16 * 16;
   };
-  if (save) take(&a->check, lq::scan_slots(sc->tokens, sc->seqs, lq::scan_sub_shift(sc->states)) * state);
+  if (!save && sc->tokens <= lq::kScanLeast) return 0;  // no sequence has two chunks
+  if (save) take(&a->check, lq::scan_checks(sc->tokens, sc->seqs, sc->states) * state);
   take(&a->carry, slots * state);
   take(&a->sum, slots * channels * 4);
   if (save) {
@@ -104,9 +107,9 @@ int64_t scan_space(const lq_scan *sc, int64_t slots, bool save, char *base, lq::
   }
   return used;
 }
-int64_t scan_need(const lq_scan *sc, int64_t slots, bool save) {
+int64_t scan_need(const lq_scan *sc, bool save) {
   lq::ScanArgs none{};
-  return scan_space(sc, slots, save, nullptr, &none);
+  return scan_space(sc, save, nullptr, &none);
 }
 
 int scan_weights(const lq_scan *sc, Blocks *bl, lq::ScanArgs *a) {
@@ -150,21 +153,22 @@ int scan_inputs(const lq_scan *sc, const lq_rows *x, const lq_rows *dt, const lq
 }
 
 // Offsets, chunks and workspace of the calls over sequences
-int scan_chunks(const lq_scan *sc, const int32_t *cu, void *ws, int64_t ws_bytes, bool save, Blocks *bl,
+int scan_chunks(const lq_scan *sc, const int32_t *cu, void *ws, int64_t ws_bytes, bool save, bool back, Blocks *bl,
                 lq::ScanArgs *a) {
   if (!cu) return LQ_ERR_NULL;
   if (!aligned(cu, 4)) return LQ_ERR_ALIGN;
   bl->add_in(dense(cu, (int64_t(sc->seqs) + 1) * 4));
   a->cu = cu;
-  a->shift = lq::scan_shift(sc->tokens, lq::scan_tiles(sc->channels, sc->groups));
-  a->slots = lq::scan_slots(sc->tokens, sc->seqs, a->shift);
-  const int64_t need = save || sc->tokens > (int64_t(1) << a->shift) ? scan_need(sc, a->slots, save) : 0;
+  a->chunk = (back ? lq::scan_grad_chunk : lq::scan_forward_chunk)(sc->tokens, sc->seqs, sc->channels, sc->groups,
+                                                                  sc->states);
+  a->slots = lq::scan_slots(sc->tokens, sc->seqs, a->chunk);
+  const int64_t need = scan_need(sc, save);
   if (need) {
     if (!ws) return LQ_ERR_NULL;
     if (!aligned(ws, 16)) return LQ_ERR_ALIGN;
     if (ws_bytes < need) return LQ_ERR_SHAPE;
     bl->add_out(dense(ws, need));
-    scan_space(sc, a->slots, save, static_cast<char *>(ws), a);
+    scan_space(sc, save, static_cast<char *>(ws), a);
   }
   return LQ_OK;
 }
@@ -335,13 +339,7 @@ int leapquant_conv_backward(const lq_conv *cv, const int32_t *cu_seqlens, const 
 int64_t leapquant_scan_workspace(const lq_scan *sc, int32_t save) {
   const int rc = check_scan(sc, false);
   if (rc) return rc;
-  // the most chunks that any call with at most these tokens has (scan_shift)
-  const int64_t T = sc->tokens, tiles = lq::scan_tiles(sc->channels, sc->groups);
-  int64_t most = lq::kScanWaves / tiles;
-  if (most < (T >> lq::kScanMost)) most = T >> lq::kScanMost;
-  if (most > (T >> lq::kScanLeast)) most = T >> lq::kScanLeast;
-  if (!save && T <= (int64_t(1) << lq::kScanLeast)) return 0;
-  return scan_need(sc, most + sc->seqs, save != 0);
+  return scan_need(sc, save != 0);
 }
 
 int leapquant_scan_forward(const lq_scan *sc, const int32_t *cu_seqlens, const lq_rows *x, const lq_rows *dt,
@@ -353,7 +351,7 @@ int leapquant_scan_forward(const lq_scan *sc, const int32_t *cu_seqlens, const l
   lq::ScanArgs a{};
   if ((rc = scan_weights(sc, &bl, &a))) return rc;
   if ((rc = scan_inputs(sc, x, dt, B, C, z, &bl, &a))) return rc;
-  if ((rc = scan_chunks(sc, cu_seqlens, workspace, workspace_bytes, save != 0, &bl, &a))) return rc;
+  if ((rc = scan_chunks(sc, cu_seqlens, workspace, workspace_bytes, save != 0, false, &bl, &a))) return rc;
   Block b;
   if ((rc = check_channels(y, sc->tokens, sc->channels, dtype_size(sc->dtype), true, &b, &a.y))) return rc;
   bl.add_out(b);
@@ -406,7 +404,7 @@ int leapquant_scan_backward(const lq_scan *sc, const int32_t *cu_seqlens, const 
   lq::ScanArgs a{};
   if ((rc = scan_weights(sc, &bl, &a))) return rc;
   if ((rc = scan_inputs(sc, x, dt, B, C, z, &bl, &a))) return rc;
-  if ((rc = scan_chunks(sc, cu_seqlens, workspace, workspace_bytes, true, &bl, &a))) return rc;
+  if ((rc = scan_chunks(sc, cu_seqlens, workspace, workspace_bytes, true, true, &bl, &a))) return rc;
   if (!dA || (dD && !sc->D) || (ddt_bias && !sc->dt_bias) || (dz && !z)) return LQ_ERR_NULL;
   const int64_t T = sc->tokens, size = dtype_size(sc->dtype), channels = sc->channels;
   Block b;

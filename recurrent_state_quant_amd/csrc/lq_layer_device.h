@@ -14,9 +14,9 @@ __device__ __forceinline__ int seq_offset(const int32_t *cu, int64_t tokens, int
   return __builtin_amdgcn_readfirstlane(c < 0 ? 0 : (c > tokens ? (int)tokens : c));
 }
 
-// The last i of [0, seqs) with (offset(i) >> shift) + i * step <= at, or -1.
+// The last i of [0, seqs) with offset(i) / chunk + i * step <= at, or -1.
 // All 64 lanes search together, 64 boundaries a step.
-__device__ __forceinline__ int seq_search(const int32_t *cu, int64_t tokens, int seqs, int shift, int step, int at,
+__device__ __forceinline__ int seq_search(const int32_t *cu, int64_t tokens, int seqs, int chunk, int step, int at,
                                           int lane) {
   int lo = 0, n = seqs;
   while (n > 0) {
@@ -26,7 +26,7 @@ __device__ __forceinline__ int seq_search(const int32_t *cu, int64_t tokens, int
     if (lane * stride < n) {
       const int c = cu[i];
       const int o = c < 0 ? 0 : (c > tokens ? (int)tokens : c);
-      below = (o >> shift) + i * step <= at;
+      below = o / chunk + i * step <= at;
     }
     const int m = __popcll(__ballot(below));
     if (m == 0) return lo - 1;  // (only in the first round: later ones begin below `at`)

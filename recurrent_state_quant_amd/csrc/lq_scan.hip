@@ -8,18 +8,20 @@
 // lanes.  A wave takes 64 channels and one chunk of tokens; sequences of several
 // chunks take three launches: every chunk's states from zero and the sum of its
 // steps (the whole chunk decays by e^(A sum)), the states before every chunk
-// from these, and the tokens again from there.  Chunks of 32 to 512 tokens give
-// about 4,096 waves, four a SIMD.
+// from these, and the tokens again from there.
 #include "lq_scan_device.h"
 
 namespace lq {
 
 constexpr int kScanAhead = 8;  // tokens whose inputs are loaded together
 
-// OUT: the chunks' outputs from the states before them; otherwise the chunks'
-// states from zero.
-template <class E, int N, bool OUT>
-__global__ __launch_bounds__(256) void scan_kernel(const ScanArgs A, int tiles, int64_t waves) {
+// kScanOut, kScanGated: the chunks' outputs from the states before them (gated
+// by z); kScanLocal: the chunks' states from zero.
+enum { kScanLocal, kScanOut, kScanGated };
+template <class E, int N, int MODE>
+__global__ __launch_bounds__(256, MODE == kScanLocal ? 4 : N > 16 ? 3 : 4) void scan_kernel(const ScanArgs A, int tiles,
+                                                                                            int64_t waves) {
+  constexpr bool OUT = MODE != kScanLocal, GATE = MODE == kScanGated;
   const int lane = threadIdx.x & 63;
   const int64_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) + (int64_t)blockIdx.x * 4;
   if (wave >= waves) return;  // whole waves; the waves share nothing
@@ -39,57 +41,67 @@ __global__ __launch_bounds__(256) void scan_kernel(const ScanArgs A, int tiles, 
       scan_load_rows<N>(A.S0, k.i * width + ch.c, h);
   }
   const float bias = A.bias ? A.bias[ch.c] : 0.f, skip = OUT && A.skip ? A.skip[ch.c] : 0.f;
-  const bool gate = OUT && A.z.ptr;
-  const E *x = at<const E>(A.x, 0, 0) + ch.c, *dt = at<const E>(A.dt, 0, 0) + ch.c;
-  const E *z = gate ? at<const E>(A.z, 0, 0) + ch.c : x;
-  E *y = OUT ? at<E>(A.y, 0, 0) + ch.c : nullptr;
-  constexpr int sub = 1 << scan_sub_shift(N);
+  const bool save = OUT && A.check;
+  constexpr int shift = scan_sub_shift(N), sub = 1 << shift;
   E rx[kScanAhead], rd[kScanAhead], rz[kScanAhead];
   const auto load = [&](int t) {
+    const ScanArgs &P = scan_args();
+    const E *x = at<const E>(P.x, t, 0), *dt = at<const E>(P.dt, t, 0), *z = GATE ? at<const E>(P.z, t, 0) : x;
 #pragma unroll
     for (int u = 0; u < kScanAhead; ++u) {
-      const int64_t tt = min(t + u, k.t1 - 1);
-      rx[u] = x[tt * A.x.ts];
-      rd[u] = dt[tt * A.dt.ts];
-      if (gate) rz[u] = z[tt * A.z.ts];
+      rx[u] = lane_load(x, ch.c);
+      rd[u] = lane_load(dt, ch.c);
+      if (GATE) rz[u] = lane_load(z, ch.c);
+      if (t + u + 1 < k.t1) {
+        x += P.x.ts;
+        dt += P.dt.ts;
+        if (GATE) z += P.z.ts;
+      }
     }
   };
-  if (k.t0 < k.t1) load(k.t0);
+  ScanRow<E, N> B, C;
+  if (k.t0 < k.t1) {
+    load(k.t0);
+    B.load(A.B, k.t0, ch.g);
+    if (OUT) C.load(A.C, k.t0, ch.g);
+  }
   for (int t = k.t0; t < k.t1; t += kScanAhead) {
     float fx[kScanAhead], fd[kScanAhead], fz[kScanAhead];
 #pragma unroll
     for (int u = 0; u < kScanAhead; ++u) {
       fx[u] = to_f(rx[u]);
       fd[u] = to_f(rd[u]) + bias;
-      fz[u] = gate ? to_f(rz[u]) : 0.f;
+      fz[u] = GATE ? to_f(rz[u]) : 0.f;
     }
     if (t + kScanAhead < k.t1) load(t + kScanAhead);
 #pragma unroll
     for (int u = 0; u < kScanAhead; ++u) {
+      __builtin_amdgcn_sched_barrier(0);
       const int tt = t + u;
-      if (tt >= k.t1) break;
-      if (OUT && A.check && u % sub == 0) {
-        const int64_t s = (k.start >> scan_sub_shift(N)) + k.i + ((tt - k.start) >> scan_sub_shift(N));
+      const ScanRow<E, N> b = B, cc = C;
+      const int next = min(tt + 1, k.t1 - 1);
+      B.load(A.B, next, ch.g);
+      if (OUT) C.load(A.C, next, ch.g);
+      if (OUT && u % sub == 0 && save && tt < k.t1) {
+        const int64_t s = (k.start >> shift) + k.i + ((tt - k.start) >> shift);
         if (ch.on) scan_store_cols<N>(A.check + s * N * width, width, ch.c, h);
       }
-      float b[N];
-      scan_row<E, N>(A.B, tt, ch.g, b);
-      const float d = scan_step(A, fd[u]), dx = d * fx[u];
+      // past the chunk's end: a step of zero
+      const bool in = tt < k.t1;
+      const float d = in ? scan_step(A, fd[u]) : 0.f, x = in ? fx[u] : 0.f, dx = d * x;
       sum += d;
 #pragma unroll
       for (int n = 0; n < N; ++n) h[n] = fmaf(__builtin_amdgcn_exp2f(d * a2[n]), h[n], dx * b[n]);
       if (OUT) {
-        float cc[N];
-        scan_row<E, N>(A.C, tt, ch.g, cc);
-        float p0 = skip * fx[u], p1 = 0.f;
+        float p0 = skip * x, p1 = 0.f;
 #pragma unroll
         for (int n = 0; n < N; n += 2) {
           p0 = fmaf(cc[n], h[n], p0);
           p1 = fmaf(cc[n + 1], h[n + 1], p1);
         }
         float p = p0 + p1;
-        if (gate) p *= fz[u] * sigmoid(fz[u]);
-        if (ch.on) y[tt * A.y.ts] = from_f<E>(p);
+        if (GATE) p *= fz[u] * sigmoid(fz[u]);
+        if (ch.on && in) lane_store(at<E>(scan_args().y, tt, 0), ch.c, from_f<E>(p));
       }
     }
   }
@@ -115,9 +127,9 @@ __global__ __launch_bounds__(256) void scan_carry_kernel(const ScanArgs A, int s
     return o < 0 ? 0 : (o > A.tokens ? (int)A.tokens : o);
   };
   const int start = offset(i), end = max(start, offset(i + 1));
-  const int chunks = (end - start + (1 << A.shift) - 1) >> A.shift;
+  const int chunks = (end - start + A.chunk - 1) / A.chunk;
   if (chunks < 2) return;
-  const int64_t slot = (start >> A.shift) + i;
+  const int64_t slot = start / A.chunk + i;
   const float a2 = A.A[c * states + n] * kLog2e;
   float h = A.S0 ? A.S0[(i * width + c) * states + n] : 0.f;
   float *carry = A.carry + (slot * states + n) * width + c;
@@ -194,12 +206,15 @@ static hipError_t scan_run(const ScanArgs &a, bool step, hipStream_t stream) {
   }
   const int64_t tiles = scan_tiles(a.channels, a.groups), waves = tiles * a.slots;
   const dim3 grid((unsigned)((waves + 3) / 4));
-  if (a.tokens > (int64_t(1) << a.shift)) {  // a sequence may have several chunks
-    hipLaunchKernelGGL((scan_kernel<E, N, false>), grid, dim3(256), 0, stream, a, (int)tiles, waves);
+  if (a.tokens > a.chunk) {  // a sequence may have several chunks
+    hipLaunchKernelGGL((scan_kernel<E, N, kScanLocal>), grid, dim3(256), 0, stream, a, (int)tiles, waves);
     const int64_t threads = (int64_t)a.seqs * a.channels * N;
     hipLaunchKernelGGL(scan_carry_kernel, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, stream, a, N, threads);
   }
-  hipLaunchKernelGGL((scan_kernel<E, N, true>), grid, dim3(256), 0, stream, a, (int)tiles, waves);
+  if (a.z.ptr)
+    hipLaunchKernelGGL((scan_kernel<E, N, kScanGated>), grid, dim3(256), 0, stream, a, (int)tiles, waves);
+  else
+    hipLaunchKernelGGL((scan_kernel<E, N, kScanOut>), grid, dim3(256), 0, stream, a, (int)tiles, waves);
   return hipGetLastError();
 }
 template <class E>

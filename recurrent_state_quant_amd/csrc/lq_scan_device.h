@@ -1,5 +1,7 @@
 // Device-side helpers of the selective scan (lq_scan.hip, lq_scan_grad.hip).
 #pragma once
+#include <type_traits>
+
 #include "lq_layer_device.h"
 
 namespace lq {
@@ -35,21 +37,28 @@ __device__ __forceinline__ float scan_step(const ScanArgs &A, float v, float &sl
 // A row of B or C: N values that are the same for the whole wave, through the
 // scalar cache (the address is made of wave-uniform values), so that they cost
 // the vector units nothing but their use as an operand.
+template <class E, int N> struct ScanRow {
+  static constexpr int words = N * (int)sizeof(E) / 4;
+  uint32_t w[words];
+  __device__ __forceinline__ void load(const Rows &r, int t, int g) {
+    typedef const uint32_t __attribute__((address_space(4))) *scalars;
+    const scalars p = (scalars)(uintptr_t)at<const E>(r, t, g);
+#pragma unroll
+    for (int i = 0; i < words; ++i) w[i] = p[i];
+  }
+  __device__ __forceinline__ float operator[](int n) const {
+    if constexpr (sizeof(E) == 4)
+      return __uint_as_float(w[n]);
+    else
+      return to_f(__builtin_bit_cast(E, (uint16_t)(w[n >> 1] >> (16 * (n & 1)))));
+  }
+};
 template <class E, int N>
 __device__ __forceinline__ void scan_row(const Rows &r, int t, int g, float (&f)[N]) {
-  typedef const uint32_t __attribute__((address_space(4))) *scalars;
-  const scalars p = (scalars)(uintptr_t)at<const E>(r, t, g);
-  constexpr int words = N * (int)sizeof(E) / 4;
-  uint32_t w[words];
+  ScanRow<E, N> row;
+  row.load(r, t, g);
 #pragma unroll
-  for (int i = 0; i < words; ++i) w[i] = p[i];
-#pragma unroll
-  for (int n = 0; n < N; ++n) {
-    if constexpr (sizeof(E) == 4)
-      f[n] = __uint_as_float(w[n]);
-    else
-      f[n] = to_f(__builtin_bit_cast(E, (uint16_t)(w[n >> 1] >> (16 * (n & 1)))));
-  }
+  for (int n = 0; n < N; ++n) f[n] = row[n];
 }
 
 // A wave's channels: 64 of one group, one a lane.
@@ -75,29 +84,61 @@ struct ScanChunk {
 };
 __device__ __forceinline__ ScanChunk scan_chunk(const ScanArgs &A, int slot, int lane) {
   ScanChunk k{0, 0, 0, 0, 0, 0, false};
-  k.i = seq_search(A.cu, A.tokens, A.seqs, A.shift, 1, slot, lane);
+  k.i = seq_search(A.cu, A.tokens, A.seqs, A.chunk, 1, slot, lane);
   if (k.i < 0) return k;
   k.start = seq_offset(A.cu, A.tokens, k.i);
   const int end = max(k.start, seq_offset(A.cu, A.tokens, k.i + 1));
-  k.chunks = (end - k.start + (1 << A.shift) - 1) >> A.shift;
-  k.c = slot - ((k.start >> A.shift) + k.i);
+  k.chunks = (end - k.start + A.chunk - 1) / A.chunk;
+  k.c = slot - (k.start / A.chunk + k.i);
   if (k.c < 0 || (k.c >= k.chunks && k.c > 0)) return k;
   k.any = true;
-  k.t0 = k.start + (k.c << A.shift);
-  k.t1 = min(end, k.t0 + (1 << A.shift));
+  k.t0 = k.start + k.c * A.chunk;
+  k.t1 = min(end, k.t0 + A.chunk);
   return k;
 }
 
+// Element c of a row whose address is the same for the wave: the address stays
+// in scalar registers (it is hidden from the compiler, which would otherwise add
+// it to the lane's offset first, in vector registers), the lane's offset is one
+// register for all rows (of at most 2^20 elements).
+template <class T> using lane_bits = std::conditional_t<sizeof(T) == 4, uint32_t, uint16_t>;
+template <class T>
+__device__ __forceinline__ uintptr_t row_address(T *row) {
+  uintptr_t p = reinterpret_cast<uintptr_t>(row);
+  asm("" : "+s"(p));
+  return p;
+}
+template <class T>
+__device__ __forceinline__ T lane_load(const T *row, int c) {
+  typedef const char __attribute__((address_space(1))) *bytes;
+  typedef const lane_bits<T> __attribute__((address_space(1))) *global;
+  const uint32_t off = (uint32_t)c * (uint32_t)sizeof(T);
+  return __builtin_bit_cast(T, *(global)((bytes)row_address(row) + off));
+}
+template <class T>
+__device__ __forceinline__ void lane_store(T *row, int c, T x) {
+  typedef char __attribute__((address_space(1))) *bytes;
+  typedef lane_bits<T> __attribute__((address_space(1))) *global;
+  const uint32_t off = (uint32_t)c * (uint32_t)sizeof(T);
+  *(global)((bytes)row_address(row) + off) = __builtin_bit_cast(lane_bits<T>, x);
+}
+// The kernel's arguments (its first) read again where they are used: pointers
+// and strides of a dozen arrays do not stay in scalar registers that way.
+__device__ __forceinline__ const ScanArgs &scan_args() {
+  uintptr_t p = (uintptr_t)__builtin_amdgcn_kernarg_segment_ptr();
+  asm("" : "+s"(p));
+  return *(const ScanArgs *)(const ScanArgs __attribute__((address_space(4))) *)p;
+}
 // A channel's states from or to [states][channels] or [channels][states]
 template <int N>
 __device__ __forceinline__ void scan_load_cols(const float *p, int64_t channels, int c, float (&h)[N]) {
 #pragma unroll
-  for (int n = 0; n < N; ++n) h[n] = p[n * channels + c];
+  for (int n = 0; n < N; ++n) h[n] = lane_load(p + n * channels, c);
 }
 template <int N>
 __device__ __forceinline__ void scan_store_cols(float *p, int64_t channels, int c, const float (&h)[N]) {
 #pragma unroll
-  for (int n = 0; n < N; ++n) p[n * channels + c] = h[n];
+  for (int n = 0; n < N; ++n) lane_store(p + n * channels, c, h[n]);
 }
 template <int N>
 __device__ __forceinline__ void scan_load_rows(const float *p, int64_t row, float (&h)[N]) {

@@ -87,9 +87,9 @@ __global__ __launch_bounds__(256) void scan_grad_carry_kernel(const ScanArgs A, 
     return o < 0 ? 0 : (o > A.tokens ? (int)A.tokens : o);
   };
   const int start = offset(i), end = max(start, offset(i + 1));
-  const int chunks = (end - start + (1 << A.shift) - 1) >> A.shift;
+  const int chunks = (end - start + A.chunk - 1) / A.chunk;
   if (chunks < 2) return;
-  const int64_t slot = (start >> A.shift) + i;
+  const int64_t slot = start / A.chunk + i;
   const float a2 = A.A[c * states + n] * kLog2e;
   float g = A.dS ? A.dS[(i * width + c) * states + n] : 0.f;
   float *carry = A.carry + (slot * states + n) * width + c;
@@ -112,59 +112,27 @@ __global__ __launch_bounds__(256) void scan_grad_carry_kernel(const ScanArgs A, 
   }
 }
 
-// Sums across the wave of many values at once: each step halves the lanes that
-// a value is spread over and packs two values into one register.
-// Four values: afterwards rows of 16 lanes 0, 1, 2, 3 hold a, c, b, d.
-__device__ __forceinline__ float fold4(float a, float b, float c, float d) {
-  const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false, false);
-  const auto q = __builtin_amdgcn_permlane32_swap(__float_as_uint(c), __float_as_uint(d), false, false);
-  const float x = __uint_as_float(p[0]) + __uint_as_float(p[1]), y = __uint_as_float(q[0]) + __uint_as_float(q[1]);
-  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(y), false, false);
-  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
-}
-// Two values into one register: lanes with `high` keep b.
-template <int CTRL>
-__device__ __forceinline__ float fold2(float a, float b, bool high) {
-  return (high ? b : a) + dpp<CTRL>(high ? a : b);
-}
-// Q registers of fold4 into one: lane (row r, i) holds a sum of register q(i),
-// the bits of q being bits 3, 2, 1, 0 of i in this order (as many as Q has).
-template <int Q>
-__device__ __forceinline__ float fold_row(float (&v)[Q], int lane) {
-  static_assert(Q == 4 || Q == 8 || Q == 16, "");
-  float a[Q / 2];
+// Sums across the wave of many registers, on the matrix pipe beside the vector
+// work.  Four products of 16 blocks, (4 x 1) times (1 x 4) with a row that is one
+// in its n-th place, put the four lanes of each block of the n-th register into
+// four registers of one lane, where they are added: 4 registers become one, lane 4
+// b + n holding the sum of block b.  Of those, products of 16 x 4 times 4 x 16 with
+// a matrix that is one in its q-th column add every fourth block: register r of
+// lane 16 g + q then holds a fourth (of blocks g, g + 4 ..) of the sum of register
+// 4 q + r.  The fourths are added where the waves' sums meet.
+__device__ __forceinline__ float sum_blocks(const float (&v)[4], const float (&one)[4]) {
+  floatx4 x = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int k = 0; k < Q / 2; ++k) a[k] = fold2<0x140>(v[2 * k], v[2 * k + 1], lane & 8);  // row_mirror
-  float b[Q / 4];
-#pragma unroll
-  for (int k = 0; k < Q / 4; ++k) b[k] = fold2<0x141>(a[2 * k], a[2 * k + 1], lane & 4);  // row_half_mirror
-  if constexpr (Q == 4) {
-    b[0] += dpp<0x1B>(b[0]);  // quad_perm [3,2,1,0]
-    return b[0] + dpp<0xB1>(b[0]);  // quad_perm [1,0,3,2]
-  } else {
-    float c[Q / 8];
-#pragma unroll
-    for (int k = 0; k < Q / 8; ++k) c[k] = fold2<0x1B>(b[2 * k], b[2 * k + 1], lane & 2);
-    if constexpr (Q == 8) return c[0] + dpp<0xB1>(c[0]);
-    if constexpr (Q == 16) return fold2<0xB1>(c[0], c[1], lane & 1);
-  }
-}
-// The number of the sum that a lane holds after fold_row.
-template <int Q>
-__device__ __forceinline__ int fold_place(int lane) {
-  const int row = lane >> 4;
-  int q = (lane >> 3 & 1) | (lane >> 2 & 1) << 1;
-  if (Q > 4) q |= (lane >> 1 & 1) << 2;
-  if (Q > 8) q |= (lane & 1) << 3;
-  return 4 * q + ((row & 1) << 1 | row >> 1);
+  for (int n = 0; n < 4; ++n) x = __builtin_amdgcn_mfma_f32_4x4x1f32(v[n], one[n], x, 0, 0, 0);
+  return (x[0] + x[1]) + (x[2] + x[3]);
 }
 
 // A block's four waves share a group and a chunk: their sums over the channels
 // meet in LDS after every run of tokens.
-template <class E, int N>
-__global__ __launch_bounds__(256) void scan_grad_kernel(const ScanArgs A, int blocks_group) {
-  constexpr int shift = scan_sub_shift(N), sub = 1 << shift, Q = N / 2;
-  __shared__ float sh[2][4][sub][2 * N];
+template <class E, int N, bool GATE>
+__global__ __launch_bounds__(256, N > 16 ? 1 : 2) void scan_grad_kernel(const ScanArgs A, int blocks_group) {
+  constexpr int shift = scan_sub_shift(N), sub = 1 << shift, Q = N / 2;  // Q: fours of sums
+  __shared__ float sh[2][sub][16][2 * N];
   const int lane = threadIdx.x & 63, w4 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int blocks = A.groups * blocks_group;
   const int slot = blockIdx.x / blocks, gb = blockIdx.x % blocks;
@@ -184,89 +152,127 @@ __global__ __launch_bounds__(256) void scan_grad_kernel(const ScanArgs A, int bl
         scan_load_rows<N>(A.dS, k.i * width + ch.c, g);
     }
     const float bias = A.bias ? A.bias[ch.c] : 0.f, skip = A.skip ? A.skip[ch.c] : 0.f;
-    const bool gate = A.z.ptr;
-    const E *x = at<const E>(A.x, 0, 0) + ch.c, *dt = at<const E>(A.dt, 0, 0) + ch.c;
-    const E *dy = at<const E>(A.dy, 0, 0) + ch.c, *z = gate ? at<const E>(A.z, 0, 0) + ch.c : x;
-    E *out_x = at<E>(A.dx, 0, 0) + ch.c, *out_t = at<E>(A.ddt, 0, 0) + ch.c;
-    E *out_z = gate ? at<E>(A.dz, 0, 0) + ch.c : out_x;
     const int len = k.t1 - k.t0, runs = (len + sub - 1) >> shift;
     const int64_t first = (k.start >> shift) + k.i + ((k.t0 - k.start) >> shift);
-    const int place = fold_place<Q>(lane);
-    const bool holder = Q == 16 || (Q == 8 ? !(lane & 1) : !(lane & 3));
+    float one4[4], one16[Q];
+#pragma unroll
+    for (int n = 0; n < 4; ++n) one4[n] = (lane & 3) == n ? 1.f : 0.f;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) one16[q] = (lane & 15) == q ? 1.f : 0.f;
+    E rx[sub], rd[sub], ry[sub], rz[sub];
+    float start[N];  // the states before the run's tokens
+    const auto load = [&](int r) {
+      const int t = k.t0 + (r << shift);
+      const ScanArgs &P = scan_args();
+      const E *x = at<const E>(P.x, t, 0), *dt = at<const E>(P.dt, t, 0), *dy = at<const E>(P.dy, t, 0);
+      const E *z = GATE ? at<const E>(P.z, t, 0) : x;
+#pragma unroll
+      for (int u = 0; u < sub; ++u) {
+        rx[u] = lane_load(x, ch.c);
+        rd[u] = lane_load(dt, ch.c);
+        ry[u] = lane_load(dy, ch.c);
+        if (GATE) rz[u] = lane_load(z, ch.c);
+        if (t + u + 1 < k.t1) {
+          x += P.x.ts;
+          dt += P.dt.ts;
+          dy += P.dy.ts;
+          if (GATE) z += P.z.ts;
+        }
+      }
+      scan_load_cols<N>(P.check + (first + r) * N * width, width, ch.c, start);
+    };
+    if (runs) load(runs - 1);
     for (int r = runs - 1; r >= 0; --r) {
       const int t = k.t0 + (r << shift), n_t = min(sub, k.t1 - t);
       float fx[sub], fd[sub], fy[sub], fz[sub], slope[sub], hist[sub][N];
 #pragma unroll
       for (int u = 0; u < sub; ++u) {
-        const int64_t tt = min(t + u, k.t1 - 1);
-        fx[u] = ch.on ? to_f(x[tt * A.x.ts]) : 0.f;
-        fd[u] = to_f(dt[tt * A.dt.ts]) + bias;
-        fy[u] = ch.on ? to_f(dy[tt * A.dy.ts]) : 0.f;
-        fz[u] = gate ? to_f(z[tt * A.z.ts]) : 0.f;
+        fx[u] = ch.on ? to_f(rx[u]) : 0.f;
+        fd[u] = to_f(rd[u]) + bias;
+        fy[u] = ch.on ? to_f(ry[u]) : 0.f;
+        fz[u] = GATE ? to_f(rz[u]) : 0.f;
       }
-      // the states before the run's tokens
-      scan_load_cols<N>(A.check + (first + r) * N * width, width, ch.c, hist[0]);
+#pragma unroll
+      for (int n = 0; n < N; ++n) hist[0][n] = start[n];
+      ScanRow<E, N> B, C;
+      B.load(A.B, t, ch.g);
 #pragma unroll
       for (int u = 0; u < sub; ++u) {
         fd[u] = scan_step(A, fd[u], slope[u]);
-        if (u + 1 < sub) {
-          float b[N];
-          scan_row<E, N>(A.B, min(t + u, k.t1 - 1), ch.g, b);
-          const float dx = fd[u] * fx[u];
+        if (u >= n_t) fd[u] = fy[u] = 0.f;  // past the chunk's end: a step of zero that nothing comes of
+      }
 #pragma unroll
-          for (int n = 0; n < N; ++n)
-            hist[u + 1][n] = fmaf(__builtin_amdgcn_exp2f(fd[u] * a2[n]), hist[u][n], dx * b[n]);
-        }
+      for (int u = 0; u + 1 < sub; ++u) {
+        __builtin_amdgcn_sched_barrier(0);
+        const ScanRow<E, N> b = B;
+        B.load(A.B, min(t + u + 1, k.t1 - 1), ch.g);
+        if (u + 2 == sub) C.load(A.C, min(t + u + 1, k.t1 - 1), ch.g);
+        const float dx = fd[u] * fx[u];
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+          hist[u + 1][n] = fmaf(__builtin_amdgcn_exp2f(fd[u] * a2[n]), hist[u][n], dx * b[n]);
       }
 #pragma unroll
       for (int u = sub - 1; u >= 0; --u) {
-        if (u >= n_t) continue;
-        float b[N], cc[N];
-        scan_row<E, N>(A.B, t + u, ch.g, b);
-        scan_row<E, N>(A.C, t + u, ch.g, cc);
-        const float d = fd[u], xd = d * fx[u];
+        __builtin_amdgcn_sched_barrier(0);
+        if (u == 0 && r > 0) load(r - 1);  // into the registers of the tokens that are done
+        const ScanRow<E, N> b = B, cc = C;
+        if (u > 0) {
+          B.load(A.B, min(t + u - 1, k.t1 - 1), ch.g);
+          C.load(A.C, min(t + u - 1, k.t1 - 1), ch.g);
+        }
+        float d = fd[u];
+        asm("" : "+v"(d));  // the decays again: keeping those of the run would cost 48 registers
+        const float xd = d * fx[u];
         float s = 0.f, dp = fy[u];
-        if (gate) {
+        if (GATE) {
           s = sigmoid(fz[u]);
           dp *= fz[u] * s;
         }
-        float p = skip * fx[u], gb = 0.f, ea = 0.f, fold[Q];
+        float p = skip * fx[u], gb = 0.f, ea = 0.f;
+        floatx4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int n = 0; n < N; n += 4) {
+        for (int q = 0; q < N / 4; ++q) {
           float vb[4], vc[4];
 #pragma unroll
           for (int m = 0; m < 4; ++m) {
-            const float a = __builtin_amdgcn_exp2f(d * a2[n + m]), ah = a * hist[u][n + m];
-            const float h = fmaf(xd, b[n + m], ah);
-            p = fmaf(cc[n + m], h, p);
-            const float gn = fmaf(cc[n + m], dp, g[n + m]);
-            gb = fmaf(gn, b[n + m], gb);
+            const int n = 4 * q + m;
+            const float a = __builtin_amdgcn_exp2f(d * a2[n]), ah = a * hist[u][n];
+            const float h = u + 1 < sub ? hist[u + 1 < sub ? u + 1 : u][n] : fmaf(xd, b[n], ah);
+            p = fmaf(cc[n], h, p);
+            const float gn = fmaf(cc[n], dp, g[n]);
+            gb = fmaf(gn, b[n], gb);
             const float e = gn * ah;
-            ea = fmaf(e, a2[n + m], ea);
-            dA[n + m] = fmaf(e, d, dA[n + m]);
+            ea = fmaf(e, a2[n], ea);
+            dA[n] = fmaf(e, d, dA[n]);
             vb[m] = gn * xd;
             vc[m] = dp * h;
-            g[n + m] = gn * a;
+            g[n] = gn * a;
           }
-          fold[n / 4] = fold4(vb[0], vb[1], vb[2], vb[3]);
-          fold[Q / 2 + n / 4] = fold4(vc[0], vc[1], vc[2], vc[3]);
+          // sums 0 .. N - 1 are dB's, N .. 2 N - 1 dC's
+          acc = __builtin_amdgcn_mfma_f32_16x16x4f32(sum_blocks(vb, one4), one16[q], acc, 0, 0, 0);
+          acc = __builtin_amdgcn_mfma_f32_16x16x4f32(sum_blocks(vc, one4), one16[N / 4 + q], acc, 0, 0, 0);
         }
-        const float total = fold_row<Q>(fold, lane);
-        if (holder) sh[r & 1][w4][u][place] = total;
+        if ((lane & 15) < Q)
+          *reinterpret_cast<floatx4 *>(&sh[r & 1][u][w4 * 4 + (lane >> 4)][(lane & 15) * 4]) = acc;
         const float ddt = fmaf(gb, fx[u], ea * kLn2) * slope[u];
+        const float dz = fy[u] * p * (s * fmaf(fz[u], 1.f - s, 1.f));
         dskip = fmaf(dp, fx[u], dskip);
-        dbias += ddt;
-        if (ch.on) {
-          out_x[(t + u) * A.dx.ts] = from_f<E>(fmaf(gb, d, skip * dp));
-          out_t[(t + u) * A.ddt.ts] = from_f<E>(ddt);
-          if (gate) out_z[(t + u) * A.dz.ts] = from_f<E>(fy[u] * p * (s * fmaf(fz[u], 1.f - s, 1.f)));
+        dbias += u < n_t ? ddt : 0.f;
+        if (ch.on && u < n_t) {
+          const ScanArgs &P = scan_args();
+          lane_store(at<E>(P.dx, t + u, 0), ch.c, from_f<E>(fmaf(gb, d, skip * dp)));
+          lane_store(at<E>(P.ddt, t + u, 0), ch.c, from_f<E>(ddt));
+          if (GATE) lane_store(at<E>(P.dz, t + u, 0), ch.c, from_f<E>(dz));
         }
       }
       __syncthreads();  // (the other half of `sh` is written next)
       for (int v = threadIdx.x; v < n_t * 2 * N; v += 256) {
         const int u = v / (2 * N), n = v % (2 * N);
-        A.part_bc[((int64_t)gb * A.tokens + t + u) * 2 * N + n] =
-            ((sh[r & 1][0][u][n] + sh[r & 1][1][u][n]) + sh[r & 1][2][u][n]) + sh[r & 1][3][u][n];
+        float y = 0.f;
+#pragma unroll
+        for (int m = 0; m < 16; ++m) y += sh[r & 1][u][m][n];
+        A.part_bc[((int64_t)gb * A.tokens + t + u) * 2 * N + n] = y;
       }
     }
     if (A.dS0 && k.c == 0 && ch.on) scan_store_rows<N>(A.dS0, k.i * width + ch.c, g);
@@ -328,15 +334,18 @@ __global__ __launch_bounds__(512) void scan_grad_sum_kernel(const ScanArgs A, in
 template <class E, int N>
 static hipError_t scan_back(const ScanArgs &a, hipStream_t stream) {
   const int64_t tiles = scan_tiles(a.channels, a.groups), waves = tiles * a.slots, blocks = scan_group_blocks(a.per);
-  if (a.tokens > (int64_t(1) << a.shift)) {
+  if (a.tokens > a.chunk) {
     hipLaunchKernelGGL((scan_grad_local_kernel<E, N>), dim3((unsigned)((waves + 3) / 4)), dim3(256), 0, stream, a,
                        (int)tiles, waves);
     const int64_t threads = (int64_t)a.seqs * a.channels * N;
     hipLaunchKernelGGL(scan_grad_carry_kernel, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, stream, a, N,
                        threads);
   }
-  hipLaunchKernelGGL((scan_grad_kernel<E, N>), dim3((unsigned)(a.slots * a.groups * blocks)), dim3(256), 0, stream, a,
-                     (int)blocks);
+  const dim3 grid((unsigned)(a.slots * a.groups * blocks));
+  if (a.z.ptr)
+    hipLaunchKernelGGL((scan_grad_kernel<E, N, true>), grid, dim3(256), 0, stream, a, (int)blocks);
+  else
+    hipLaunchKernelGGL((scan_grad_kernel<E, N, false>), grid, dim3(256), 0, stream, a, (int)blocks);
   const int64_t threads = a.tokens * a.groups * 2 * N;
   if (threads)
     hipLaunchKernelGGL((scan_grad_bc_kernel<E>), dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, stream, a, N,
