@@ -20,22 +20,36 @@ __device__ __forceinline__ float block_act(int gate, float z) {
   return gate == 1 ? z * s : s;
 }
 
-// The sum of a row's values: LANES lanes side by side, or a workgroup of LANES
+// Two sums of a row's values: LANES lanes side by side, or a workgroup of LANES
 // threads, through `sh` ([2][LANES / 64], the halves in turn: a half is written
 // again only behind the next sum's barrier).
 template <int LANES>
-__device__ __forceinline__ float row_sum(float x, float *sh, int &turn) {
-  if constexpr (LANES == 16) return row16_sum(x);
+__device__ __forceinline__ void row_sums(float &x, float &y, float2 *sh, int &turn) {
+  if constexpr (LANES == 16) {
+    x = row16_sum(x);
+    y = row16_sum(y);
+    return;
+  }
   x = wave_sum(x);
-  if constexpr (LANES == 64) return x;
+  y = wave_sum(y);
+  if constexpr (LANES == 64) return;
   constexpr int waves = LANES / 64;
-  float *s = sh + (turn ^= waves);
-  if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = x;
+  float2 *s = sh + (turn ^= waves);
+  if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = make_float2(x, y);
   __syncthreads();
-  float y = 0.f;
+  x = y = 0.f;
 #pragma unroll
-  for (int w = 0; w < waves; ++w) y += s[w];
-  return y;
+  for (int w = 0; w < waves; ++w) {
+    x += s[w].x;
+    y += s[w].y;
+  }
+}
+
+template <int LANES>
+__device__ __forceinline__ float row_sum(float x, float2 *sh, int &turn) {
+  float none = 0.f;
+  row_sums<LANES>(x, none, sh, turn);
+  return x;
 }
 
 template <int LANES>
@@ -71,7 +85,7 @@ __device__ __forceinline__ void block_weights(const float *w, int col, int dim, 
 
 template <class E, class S, int LANES, int R>
 __global__ __launch_bounds__(norm_threads<LANES>()) void block_norm_kernel(const BlockNormArgs A, int64_t rows) {
-  __shared__ float sh[LANES > 64 ? 2 * (LANES / 64) : 1];
+  __shared__ float2 sh[LANES > 64 ? 2 * (LANES / 64) : 1];
   int turn = 0;
   constexpr int per = norm_threads<LANES>() / LANES;
   const BlockRow b = block_row<LANES>(A, (int64_t)blockIdx.x * per + threadIdx.x / LANES, rows);
@@ -139,38 +153,67 @@ __global__ __launch_bounds__(norm_threads<LANES>()) void block_norm_kernel(const
   }
 }
 
-// Workgroups of the backward pass hold their weight gradients in registers and
-// take rows in turn.
-constexpr int kBlockNormBlocks = 1024;
+// Workgroups of the backward pass take rows in turn and hold their weight gradients
+// in LDS, each lane's own columns for each row of a workgroup: in registers they
+// would take the room of a third wave a SIMD.
+constexpr int kBlockNormBlocks = 512;
 
 template <class E, class S, int LANES, int R>
-__global__ __launch_bounds__(norm_threads<LANES>()) void block_norm_backward_kernel(const BlockNormArgs A, int64_t rows) {
+__global__ __launch_bounds__(norm_threads<LANES>(), 2) void block_norm_backward_kernel(const BlockNormArgs A, int64_t rows) {
   constexpr int threads = norm_threads<LANES>(), per = threads / LANES;
-  __shared__ float sh[LANES > 64 ? 2 * (LANES / 64) : 1];
-  __shared__ float sh_w[per > 1 ? 4 : 1][per > 1 ? LANES * R * 8 : 1];
+  __shared__ float2 sh[LANES > 64 ? 2 * (LANES / 64) : 1];
+  __shared__ float sum[per][2][LANES * R * 8];
   int turn = 0;
-  const bool gate = A.gate, res = A.res.ptr, dy = A.dy.ptr, dh = A.dh.ptr;
+  const bool gate = A.gate, silu = A.gate == 1, res = A.res.ptr, dy = A.dy.ptr, dh = A.dh.ptr;
   const float inv = 1.f / (float)A.dim;
-  float dwo[R][8], dwi[R][8];
+  const int group = threadIdx.x / LANES;
+  const auto add = [&](int p, int r, const float (&x)[8]) {
+    float y[8];
+    F32 *at_s = reinterpret_cast<F32 *>(&sum[group][p][(threadIdx.x & (LANES - 1)) * 8 + r * LANES * 8]);
+    load8(at_s, y);
 #pragma unroll
-  for (int r = 0; r < R; ++r)
+    for (int e = 0; e < 8; ++e) y[e] += x[e];
+    store8(at_s, y);
+  };
 #pragma unroll
-    for (int e = 0; e < 8; ++e) dwo[r][e] = dwi[r][e] = 0.f;
+  for (int r = 0; r < R; ++r) {
+    const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    F32 *at_s = reinterpret_cast<F32 *>(&sum[group][0][(threadIdx.x & (LANES - 1)) * 8 + r * LANES * 8]);
+    store8(at_s, zero);
+    store8(at_s + LANES * R * 8, zero);
+  }
   // whole rounds: every thread meets every barrier, past the end with the last row again
-  for (int64_t row0 = (int64_t)blockIdx.x * per; row0 < rows; row0 += (int64_t)gridDim.x * per) {
-    const BlockRow b = block_row<LANES>(A, row0 + threadIdx.x / LANES, rows);
+  // The next row's values are on their way while a row is computed.
+  Raw8<E> na[R], nz[R], ny[R];
+  Raw8<S> nr[R], nh[R];
+  const auto load = [&](int64_t row) {
+    const BlockRow b = block_row<LANES>(A, row, rows);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int col = b.col + r * LANES * 8;
+      na[r] = block_load<E>(A.a, b, col, A.dim);
+      if (gate) nz[r] = block_load<E>(A.z, b, col, A.dim);
+      if (res && dy) nr[r] = block_load<S>(A.res, b, col, A.dim);
+      if (dy) ny[r] = block_load<E>(A.dy, b, col, A.dim);
+      if (dh) nh[r] = block_load<S>(A.dh, b, col, A.dim);
+    }
+  };
+  const int64_t step = (int64_t)gridDim.x * per;
+  load((int64_t)blockIdx.x * per + group);
+  for (int64_t row0 = (int64_t)blockIdx.x * per; row0 < rows; row0 += step) {
+    const BlockRow b = block_row<LANES>(A, row0 + group, rows);
     Raw8<E> ra[R], rz[R], ry[R];
     Raw8<S> rr[R], rh[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const int col = b.col + r * LANES * 8;
-      ra[r] = block_load<E>(A.a, b, col, A.dim);
-      if (gate) rz[r] = block_load<E>(A.z, b, col, A.dim);
-      if (res && dy) rr[r] = block_load<S>(A.res, b, col, A.dim);
-      if (dy) ry[r] = block_load<E>(A.dy, b, col, A.dim);
-      if (dh) rh[r] = block_load<S>(A.dh, b, col, A.dim);
+      ra[r] = na[r];
+      rz[r] = nz[r];
+      ry[r] = ny[r];
+      rr[r] = nr[r];
+      rh[r] = nh[r];
     }
-    float ma = 1.f;
+    if (row0 + step < rows) load(row0 + step + group);
+    float ma = 1.f, x[R][8], n[R][8], sg[R][8];  // h; the normed a; 1 / (1 + e^-z)
     if (A.out_norm) {
       float ss = 0.f;
 #pragma unroll
@@ -183,49 +226,50 @@ __global__ __launch_bounds__(norm_threads<LANES>()) void block_norm_backward_ker
       }
       ma = 1.f / sqrtf(fmaf(row_sum<LANES>(ss, sh, turn), inv, A.eps));
     }
-    // n, act(z) and its derivative of a piece
-    const auto forward = [&](int r, float (&n)[8], float (&act)[8], float (&slope)[8]) {
-      raw_floats(n, ra[r]);
+    float ss = 0.f, hg = 0.f;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int col = b.col + r * LANES * 8;
+      raw_floats(n[r], ra[r]);
       if (A.out_norm) {
         float w[8];
-        block_weights(A.wo, b.col + r * LANES * 8, A.dim, w);
+        block_weights(A.wo, col, A.dim, w);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) n[e] *= ma * w[e];
+        for (int e = 0; e < 8; ++e) n[r][e] *= ma * w[e];
       }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) act[e] = 1.f, slope[e] = 0.f;
+      for (int e = 0; e < 8; ++e) x[r][e] = A.scale * n[r][e];
       if (gate) {
         float z[8];
         raw_floats(z, rz[r]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float s = sigmoid(z[e]);
-          act[e] = A.gate == 1 ? z[e] * s : s;
-          slope[e] = A.gate == 1 ? s * fmaf(z[e], 1.f - s, 1.f) : s * (1.f - s);
+        for (int e = 0; e < 8; ++e) sg[r][e] = sigmoid_for<E>(z[e]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[r][e] *= sg[r][e];
+        if (silu) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[r][e] *= z[e];
         }
       }
-    };
-    float mh = 0.f, c = 0.f;
-    if (dy) {
-      float ss = 0.f, hg = 0.f;
+      if (dy && col < A.dim) {
+        float w[8], g[8];
+        if (res) {
+          raw_floats(g, rr[r]);
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const int col = b.col + r * LANES * 8;
-        if (col >= A.dim) continue;
-        float h[8], act[8], slope[8], s[8], w[8], g[8];
-        forward(r, h, act, slope);
-        if (res) raw_floats(s, rr[r]);
+          for (int e = 0; e < 8; ++e) x[r][e] += g[e];
+        }
         block_weights(A.wi, col, A.dim, w);
         raw_floats(g, ry[r]);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const float u = h[e] * act[e], x = res ? fmaf(A.scale, u, s[e]) : A.scale * u;
-          ss = fmaf(x, x, ss);
-          hg = fmaf(x, w[e] * g[e], hg);
+          ss = fmaf(x[r][e], x[r][e], ss);
+          hg = fmaf(x[r][e], w[e] * g[e], hg);
         }
       }
-      ss = row_sum<LANES>(ss, sh, turn);
-      hg = row_sum<LANES>(hg, sh, turn);
+    }
+    float mh = 0.f, c = 0.f;
+    if (dy) {
+      row_sums<LANES>(ss, hg, sh, turn);
       mh = 1.f / sqrtf(fmaf(ss, inv, A.eps));
       c = hg * inv * mh * mh;
     }
@@ -234,41 +278,52 @@ __global__ __launch_bounds__(norm_threads<LANES>()) void block_norm_backward_ker
     for (int r = 0; r < R; ++r) {
       const int col = b.col + r * LANES * 8;
       if (col >= A.dim) continue;
-      float n[8], act[8], slope[8], H[8];
-      forward(r, n, act, slope);
+      float H[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) H[e] = 0.f;
       if (dh) raw_floats(H, rh[r]);
       if (dy) {
-        float s[8], w[8], g[8];
-        if (res) raw_floats(s, rr[r]);
+        float w[8], g[8];
         block_weights(A.wi, col, A.dim, w);
         raw_floats(g, ry[r]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float u = n[e] * act[e], x = res ? fmaf(A.scale, u, s[e]) : A.scale * u;
-          H[e] += mh * fmaf(-x, c, w[e] * g[e]);
-          dwi[r][e] += b.on ? g[e] * (x * mh) : 0.f;
+        for (int e = 0; e < 8; ++e) H[e] = fmaf(mh, fmaf(-x[r][e], c, w[e] * g[e]), H[e]);
+        if (A.dwi && b.on) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) g[e] *= x[r][e] * mh;
+          add(1, r, g);
         }
       }
       if (A.dres.ptr && b.on) store8(at<S>(A.dres, b.t, b.h) + col, H);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) H[e] *= A.scale;
-      if (gate) {
-        float dz[8];
+      for (int e = 0; e < 8; ++e) dn[r][e] = H[e] * A.scale;
+      if (gate) {  // dz = du n act'(z), dn = du act(z)
+        float z[8], dz[8];
+        raw_floats(z, rz[r]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) dz[e] = H[e] * n[e] * slope[e];
+        for (int e = 0; e < 8; ++e) {
+          const float s = sg[r][e], t = s * (1.f - s);
+          dz[e] = dn[r][e] * n[r][e] * (silu ? fmaf(z[e], t, s) : t);
+          dn[r][e] *= s;
+        }
+        if (silu) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) dn[r][e] *= z[e];
+        }
         if (b.on) store8(at<E>(A.dz, b.t, b.h) + col, dz);
       }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) dn[r][e] = H[e] * act[e];
       if (A.out_norm) {
         float a[8], w[8];
         raw_floats(a, ra[r]);
         block_weights(A.wo, col, A.dim, w);
+        if (A.dwo && b.on) {
+          float g[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) g[e] = dn[r][e] * (a[e] * ma);
+          add(0, r, g);
+        }
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          dwo[r][e] += b.on ? dn[r][e] * (a[e] * ma) : 0.f;
           dn[r][e] *= w[e];
           ag = fmaf(a[e], dn[r][e], ag);
         }
@@ -291,35 +346,14 @@ __global__ __launch_bounds__(norm_threads<LANES>()) void block_norm_backward_ker
     }
   }
   if (!A.dwo && !A.dwi) return;  // the whole block
-  // a workgroup's rows meet, then its sums go to `part`
+  // the rows of a workgroup, added in order
+  __syncthreads();
+  for (int d = threadIdx.x; d < 2 * A.dim; d += threads) {
+    const int p = d >= A.dim, col = d - p * A.dim;
+    float x = 0.f;
 #pragma unroll
-  for (int p = 0; p < 2; ++p) {
-    if constexpr (per == 1) {
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const int col = (int)threadIdx.x * 8 + r * LANES * 8;
-        if (col < A.dim)
-          store8(reinterpret_cast<F32 *>(A.part + ((int64_t)blockIdx.x * 2 + p) * A.dim + col), p ? dwi[r] : dwo[r]);
-      }
-    } else {
-      const int lane = threadIdx.x & 63, w4 = threadIdx.x >> 6;
-      if (p) __syncthreads();
-#pragma unroll
-      for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          float x = p ? dwi[r][e] : dwo[r][e];
-          if (LANES == 16) {
-            x += __shfl_xor(x, 16);
-            x += __shfl_xor(x, 32);
-          }
-          if (lane < LANES) sh_w[w4][r * LANES * 8 + lane * 8 + e] = x;
-        }
-      __syncthreads();
-      for (int d = threadIdx.x; d < A.dim; d += threads)
-        A.part[((int64_t)blockIdx.x * 2 + p) * A.dim + d] =
-            ((sh_w[0][d] + sh_w[1][d]) + sh_w[2][d]) + sh_w[3][d];
-    }
+    for (int k = 0; k < per; ++k) x += sum[k][p][col];
+    A.part[((int64_t)blockIdx.x * 2 + p) * A.dim + col] = x;
   }
 }
 

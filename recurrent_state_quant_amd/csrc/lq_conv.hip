@@ -125,7 +125,7 @@ __global__ __launch_bounds__(256) void conv_kernel(const ConvArgs A, int tiles, 
       conv_sum<V, K>(w, b, win, x, y);
       if (A.silu) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) y[v] *= sigmoid(y[v]);
+        for (int v = 0; v < V; ++v) y[v] *= sigmoid_for<E>(y[v]);
       }
       vec_store(at<E>(A.y, tt, 0) + c, vec_round<E, V>(y));
       conv_shift<V, K>(win, x);
@@ -159,7 +159,7 @@ __global__ __launch_bounds__(256) void conv_step_kernel(const ConvArgs A, int ti
   conv_sum<V, K>(w, b, win, x, y);
   if (A.silu) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) y[v] *= sigmoid(y[v]);
+    for (int v = 0; v < V; ++v) y[v] *= sigmoid_for<E>(y[v]);
   }
   vec_store(at<E>(A.y, row, 0) + c, vec_round<E, V>(y));
 #pragma unroll
@@ -167,12 +167,12 @@ __global__ __launch_bounds__(256) void conv_step_kernel(const ConvArgs A, int ti
 }
 
 // dv_t from v_t and dy_t
-template <int V>
+template <class E, int V>
 __device__ __forceinline__ void conv_back(bool silu, const float (&v)[V], float (&d)[V]) {
   if (!silu) return;
 #pragma unroll
   for (int e = 0; e < V; ++e) {
-    const float s = sigmoid(v[e]);
+    const float s = sigmoid_for<E>(v[e]);
     d[e] *= s * fmaf(v[e], 1.f - s, 1.f);
   }
 }
@@ -235,7 +235,7 @@ __global__ __launch_bounds__(256) void conv_backward_kernel(const ConvArgs A, in
           vec_floats(x, rx[u]);
           vec_floats(d, rg[u]);
           conv_sum<V, K>(w, b, win, x, y);
-          conv_back<V>(A.silu, y, d);
+          conv_back<E, V>(A.silu, y, d);
           if (tt < t1) {
 #pragma unroll
             for (int v = 0; v < V; ++v) {
@@ -317,7 +317,7 @@ __global__ __launch_bounds__(256) void conv_before_kernel(const ConvArgs A, int 
     vec_floats(x, vec_load<E, V>(at<const E>(A.x, q.s + t, 0) + c));
     vec_floats(d, vec_load<E, V>(at<const E>(A.dy, q.s + t, 0) + c));
     conv_sum<V, K>(w, b, win, x, y);
-    conv_back<V>(A.silu, y, d);
+    conv_back<E, V>(A.silu, y, d);
     // token t's window begins with the inputs t .. K - 2 before the sequence
 #pragma unroll
     for (int j = 0; j + t < K - 1; ++j)

@@ -52,7 +52,8 @@ inline int64_t conv_grad_most(int64_t tokens) {
 struct ScanArgs {
   int64_t tokens, slots;
   int seqs, channels, groups, per;  // per: channels of a group
-  int chunk;                        // tokens of a chunk, a multiple of 8
+  int chunk;                        // tokens of a chunk, a multiple of 16
+  int part;                         // tokens of a chunk from zero: chunk, or half of it
   int softplus;
   const int32_t *cu;
   Rows x, dt, z, y, B, C;  // z.ptr may be nullptr
@@ -60,8 +61,8 @@ struct ScanArgs {
   const float *S0;  // [seqs][channels][states] or nullptr (zeros)
   float *S;         // or nullptr
   float *check;     // [sub slots][states][channels] or nullptr: the state before every kSub(states)-th token of a sequence
-  float *carry;     // [slots][states][channels]  chunks of sequences with several: the state before (backward: gradient behind)
-  float *sum;       // [slots][channels]          the sum of a chunk's steps
+  float *carry;     // [part slots][states][channels]  of sequences with several: the state before (backward: gradient behind)
+  float *sum;       // [part slots][channels]          the sum of a part's steps
   // step
   const int32_t *which;  // [rows] or nullptr
   int n_slots;
@@ -87,32 +88,41 @@ inline int64_t scan_tiles(int channels, int groups) {
 }
 // Slots of chunks: sequence i, chunk c has slot cu[i] / chunk + i + c.
 inline int64_t scan_slots(int64_t tokens, int64_t seqs, int chunk) { return tokens / chunk + seqs; }
-// Tokens of a chunk: the workgroups (or waves) of a chunk's channels run in
-// rounds of `at_once`, and the rounds times a chunk's length, with some tokens'
-// time for its beginning, are the time.  Either one round that is nearly full,
-// or many.
-constexpr int kScanLeast = 32, kScanMost = 512, kScanBegin = 12;
-inline int scan_chunk_tokens(int64_t tokens, int64_t seqs, int64_t units, int64_t at_once) {
+// Tokens of a chunk.  A workgroup has a wave on each SIMD of a CU, and with w
+// waves a token takes w + stall times a wave's own vector instructions (stall:
+// what w waves leave unhidden; 1.4 measured forward, 0.7 in the gradient, whose
+// instructions are three times as many).  `most` workgroups fit a CU; more run in
+// rounds.  So the time is (chunk + what a wave's beginning takes, in tokens) times
+// the rounds' w + stall, and the best length one that fills the CUs evenly: 4,096
+// tokens x 64 waves take 98 us forward in chunks of 72 (3.6 waves a SIMD), 105 of
+// 80 (3.3).
+constexpr int kScanPart = 16, kScanLeast = 32, kScanMost = 512, kScanBegin = 12, kScanCus = 256;
+inline int scan_chunk_tokens(int64_t tokens, int64_t seqs, int64_t workgroups, int step, int most, double stall) {
   int best = kScanLeast;
-  int64_t least = INT64_MAX;
-  for (int chunk = kScanLeast; chunk <= kScanMost; chunk += 8) {
+  double least = 0;
+  for (int chunk = kScanLeast; chunk <= kScanMost; chunk += step) {
     // (half a chunk more for each sequence, as its last one is partly full)
-    const int64_t rounds = ((tokens / chunk + (seqs + 1) / 2) * units + at_once - 1) / at_once;
-    const int64_t time = rounds * (chunk + kScanBegin);
-    if (time < least) least = time, best = chunk;
-    if (rounds <= 1) break;
+    const int64_t each = ((tokens / chunk + (seqs + 1) / 2) * workgroups + kScanCus - 1) / kScanCus;
+    const int64_t rounds = each / most, rest = each % most;
+    const double time = (chunk + kScanBegin) * (rounds * (most + stall) + (rest ? rest + stall : 0));
+    if (chunk == kScanLeast || time < least) least = time, best = chunk;
+    if (each <= 1) break;
   }
   return best;
 }
 // Blocks of four waves that share a group (backward)
 inline int64_t scan_group_blocks(int per) { return (per + 255) / 256; }
-// What the chip holds at once: waves of the forward kernel, four a SIMD (three
-// with 32 states), workgroups of the gradient, two a CU (one with 32).
+// Waves of the forward kernel that a SIMD holds
+constexpr int scan_forward_waves(int states) { return states > 16 ? 3 : states > 8 ? 5 : 6; }
 inline int scan_forward_chunk(int64_t tokens, int64_t seqs, int channels, int groups, int states) {
-  return scan_chunk_tokens(tokens, seqs, scan_tiles(channels, groups), states > 16 ? 3072 : 4096);
+  return scan_chunk_tokens(tokens, seqs, (scan_tiles(channels, groups) + 3) / 4, 8, scan_forward_waves(states), 1.4);
 }
+// Of the gradient; its chunks from zero are half as long, as their kernel has
+// room for more waves.
+constexpr int scan_grad_waves(int states) { return states > 16 ? 1 : 2; }
 inline int scan_grad_chunk(int64_t tokens, int64_t seqs, int channels, int groups, int states) {
-  return scan_chunk_tokens(tokens, seqs, groups * scan_group_blocks(channels / groups), states > 16 ? 256 : 512);
+  return scan_chunk_tokens(tokens, seqs, groups * scan_group_blocks(channels / groups), kScanPart,
+                           scan_grad_waves(states), 0.7);
 }
 
 struct BlockNormArgs {

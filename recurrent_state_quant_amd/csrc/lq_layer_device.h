@@ -97,5 +97,12 @@ __device__ __forceinline__ float exp_full(float x) {
 }
 // 1 / (1 + e^-x)
 __device__ __forceinline__ float sigmoid(float x) { return __builtin_amdgcn_rcpf(1.f + exp_full(-x)); }
+// The same for results of type E: where they have 16 bits, without the rest of the
+// exponent's product (|x| 2^-24 of e^-x), at half of the instructions
+template <class E>
+__device__ __forceinline__ float sigmoid_for(float x) {
+  if constexpr (sizeof(E) == 4) return sigmoid(x);
+  return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-kLog2e * x));
+}
 
 }  // namespace lq

@@ -19,14 +19,13 @@ constexpr int kScanAhead = 8;  // tokens whose inputs are loaded together
 // by z); kScanLocal: the chunks' states from zero.
 enum { kScanLocal, kScanOut, kScanGated };
 template <class E, int N, int MODE>
-__global__ __launch_bounds__(256, MODE == kScanLocal ? 4 : N > 16 ? 3 : 4) void scan_kernel(const ScanArgs A, int tiles,
-                                                                                            int64_t waves) {
+__global__ __launch_bounds__(256, scan_forward_waves(N)) void scan_kernel(const ScanArgs A, int tiles, int64_t waves) {
   constexpr bool OUT = MODE != kScanLocal, GATE = MODE == kScanGated;
   const int lane = threadIdx.x & 63;
   const int64_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) + (int64_t)blockIdx.x * 4;
   if (wave >= waves) return;  // whole waves; the waves share nothing
   const int slot = (int)(wave / tiles), tile = (int)(wave % tiles), tg = (A.per + 63) >> 6;
-  const ScanChunk k = scan_chunk(A, slot, lane);
+  const ScanChunk k = scan_chunk(A, OUT ? A.chunk : A.part, slot, lane);
   if (!k.any || (!OUT && k.c + 1 >= k.chunks)) return;  // nothing comes behind the last chunk
   const ScanTile ch = scan_tile(A, tile / tg, tile % tg, lane);
   const int64_t width = A.channels;
@@ -36,7 +35,7 @@ __global__ __launch_bounds__(256, MODE == kScanLocal ? 4 : N > 16 ? 3 : 4) void 
   for (int n = 0; n < N; ++n) h[n] = 0.f;
   if (OUT) {
     if (k.chunks > 1)
-      scan_load_cols<N>(A.carry + (int64_t)slot * N * width, width, ch.c, h);
+      scan_load_cols<N>(A.carry + scan_first_part(A, k) * N * width, width, ch.c, h);
     else if (A.S0)
       scan_load_rows<N>(A.S0, k.i * width + ch.c, h);
   }
@@ -59,6 +58,9 @@ __global__ __launch_bounds__(256, MODE == kScanLocal ? 4 : N > 16 ? 3 : 4) void 
       }
     }
   };
+  // the output's row: reading the arguments for each token would wait for the rows
+  // of B and C on their way
+  E *y = OUT ? at<E>(A.y, k.t0, 0) : nullptr;
   ScanRow<E, N> B, C;
   if (k.t0 < k.t1) {
     load(k.t0);
@@ -91,7 +93,7 @@ __global__ __launch_bounds__(256, MODE == kScanLocal ? 4 : N > 16 ? 3 : 4) void 
       const float d = in ? scan_step(A, fd[u]) : 0.f, x = in ? fx[u] : 0.f, dx = d * x;
       sum += d;
 #pragma unroll
-      for (int n = 0; n < N; ++n) h[n] = fmaf(__builtin_amdgcn_exp2f(d * a2[n]), h[n], dx * b[n]);
+      for (int n = 0; n < N; ++n) h[n] = fmaf(__builtin_amdgcn_exp2f(d * a2[n]), h[n], scan_times<E>(dx, b[n]));
       if (OUT) {
         float p0 = skip * x, p1 = 0.f;
 #pragma unroll
@@ -100,8 +102,9 @@ __global__ __launch_bounds__(256, MODE == kScanLocal ? 4 : N > 16 ? 3 : 4) void 
           p1 = fmaf(cc[n + 1], h[n + 1], p1);
         }
         float p = p0 + p1;
-        if (GATE) p *= fz[u] * sigmoid(fz[u]);
-        if (ch.on && in) lane_store(at<E>(scan_args().y, tt, 0), ch.c, from_f<E>(p));
+        if (GATE) p *= fz[u] * sigmoid_for<E>(fz[u]);
+        if (ch.on && in) lane_store(y, ch.c, from_f<E>(p));
+        y += A.y.ts;
       }
     }
   }
@@ -117,7 +120,7 @@ __global__ __launch_bounds__(256, MODE == kScanLocal ? 4 : N > 16 ? 3 : 4) void 
 // The states before every chunk of the sequences with several, over the chunks'
 // states from zero: thread (sequence, state, channel).  S0 is copied before the
 // first chunk, as S may lie over it.
-constexpr int kCarryAhead = 8;
+constexpr int kCarryAhead = 16;
 __global__ __launch_bounds__(256) void scan_carry_kernel(const ScanArgs A, int states, int64_t threads) {
   const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (id >= threads) return;
@@ -127,9 +130,9 @@ __global__ __launch_bounds__(256) void scan_carry_kernel(const ScanArgs A, int s
     return o < 0 ? 0 : (o > A.tokens ? (int)A.tokens : o);
   };
   const int start = offset(i), end = max(start, offset(i + 1));
-  const int chunks = (end - start + A.chunk - 1) / A.chunk;
+  const int chunks = (end - start + A.part - 1) / A.part;
   if (chunks < 2) return;
-  const int64_t slot = start / A.chunk + i;
+  const int64_t slot = start / A.part + i;
   const float a2 = A.A[c * states + n] * kLog2e;
   float h = A.S0 ? A.S0[(i * width + c) * states + n] : 0.f;
   float *carry = A.carry + (slot * states + n) * width + c;
@@ -139,9 +142,9 @@ __global__ __launch_bounds__(256) void scan_carry_kernel(const ScanArgs A, int s
     float v[kCarryAhead], s[kCarryAhead];
 #pragma unroll
     for (int u = 0; u < kCarryAhead; ++u) {
-      const bool in = k + u + 1 < chunks;
-      v[u] = in ? carry[(k + u) * step] : 0.f;
-      s[u] = in ? sum[(k + u) * width] : 0.f;
+      const int64_t at = min(k + u, chunks - 2);  // (the last one has none: nothing comes behind it)
+      v[u] = carry[at * step];
+      s[u] = sum[at * width];
     }
 #pragma unroll
     for (int u = 0; u < kCarryAhead; ++u) {
@@ -205,12 +208,14 @@ static hipError_t scan_run(const ScanArgs &a, bool step, hipStream_t stream) {
     return hipGetLastError();
   }
   const int64_t tiles = scan_tiles(a.channels, a.groups), waves = tiles * a.slots;
-  const dim3 grid((unsigned)((waves + 3) / 4));
   if (a.tokens > a.chunk) {  // a sequence may have several chunks
-    hipLaunchKernelGGL((scan_kernel<E, N, kScanLocal>), grid, dim3(256), 0, stream, a, (int)tiles, waves);
+    const int64_t parts = tiles * scan_slots(a.tokens, a.seqs, a.part);
+    hipLaunchKernelGGL((scan_kernel<E, N, kScanLocal>), dim3((unsigned)((parts + 3) / 4)), dim3(256), 0, stream, a,
+                       (int)tiles, parts);
     const int64_t threads = (int64_t)a.seqs * a.channels * N;
     hipLaunchKernelGGL(scan_carry_kernel, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, stream, a, N, threads);
   }
+  const dim3 grid((unsigned)((waves + 3) / 4));
   if (a.z.ptr)
     hipLaunchKernelGGL((scan_kernel<E, N, kScanGated>), grid, dim3(256), 0, stream, a, (int)tiles, waves);
   else

@@ -7,17 +7,15 @@
 namespace lq {
 
 // max(v, 0) + log(1 + e), e = e^-|v| in (0, 1].  log(1 + e) = 2 artanh(r) with
-// r = e / (2 + e) <= 1/3, by its series up to r^15 / 15 (the next term is below
-// 2^-28 of the sum): exact to rounding also where e is tiny, as it is for the
-// small steps that such layers take.
+// r = e / (2 + e) <= 1/3, and artanh(r) = r (1 + r^2 P(r^2)) with a polynomial P
+// fitted to the series 1/3 + r^2 / 5 + .. on [0, 1/9] (least largest error of the
+// whole: 5.4e-9 relative): exact to rounding also where e is tiny, as it is for
+// the small steps that such layers take.
 __device__ __forceinline__ float softplus_of(float v, float e) {
   const float r = e * __builtin_amdgcn_rcpf(2.f + e), q = r * r;
-  float p = fmaf(q, 1.f / 15.f, 1.f / 13.f);
-  p = fmaf(p, q, 1.f / 11.f);
-  p = fmaf(p, q, 1.f / 9.f);
-  p = fmaf(p, q, 1.f / 7.f);
-  p = fmaf(p, q, 1.f / 5.f);
-  p = fmaf(p, q, 1.f / 3.f);
+  float p = fmaf(q, 0.14005996f, 0.14000902f);
+  p = fmaf(p, q, 0.20010763f);
+  p = fmaf(p, q, 0.33333209f);
   p = fmaf(p * q, r, r);
   return fmaf(2.f, p, fmaxf(v, 0.f));
 }
@@ -53,14 +51,13 @@ template <class E, int N> struct ScanRow {
       return to_f(__builtin_bit_cast(E, (uint16_t)(w[n >> 1] >> (16 * (n & 1)))));
   }
 };
-template <class E, int N>
-__device__ __forceinline__ void scan_row(const Rows &r, int t, int g, float (&f)[N]) {
-  ScanRow<E, N> row;
-  row.load(r, t, g);
-#pragma unroll
-  for (int n = 0; n < N; ++n) f[n] = row[n];
+// x b, as a fused product and sum with zero for fp16: that instruction takes an
+// fp16 operand as it is
+template <class E>
+__device__ __forceinline__ float scan_times(float x, float b) {
+  if constexpr (std::is_same_v<E, F16>) return fmaf(x, b, 0.f);
+  return x * b;
 }
-
 // A wave's channels: 64 of one group, one a lane.
 struct ScanTile {
   int g;        // group
@@ -82,18 +79,18 @@ struct ScanChunk {
   int start, t0, t1; // the sequence's first token, the chunk's tokens [t0, t1)
   bool any;          // the slot has a chunk (an empty sequence has one of no tokens)
 };
-__device__ __forceinline__ ScanChunk scan_chunk(const ScanArgs &A, int slot, int lane) {
+__device__ __forceinline__ ScanChunk scan_chunk(const ScanArgs &A, int chunk, int slot, int lane) {
   ScanChunk k{0, 0, 0, 0, 0, 0, false};
-  k.i = seq_search(A.cu, A.tokens, A.seqs, A.chunk, 1, slot, lane);
+  k.i = seq_search(A.cu, A.tokens, A.seqs, chunk, 1, slot, lane);
   if (k.i < 0) return k;
   k.start = seq_offset(A.cu, A.tokens, k.i);
   const int end = max(k.start, seq_offset(A.cu, A.tokens, k.i + 1));
-  k.chunks = (end - k.start + A.chunk - 1) / A.chunk;
-  k.c = slot - (k.start / A.chunk + k.i);
+  k.chunks = (end - k.start + chunk - 1) / chunk;
+  k.c = slot - (k.start / chunk + k.i);
   if (k.c < 0 || (k.c >= k.chunks && k.c > 0)) return k;
   k.any = true;
-  k.t0 = k.start + k.c * A.chunk;
-  k.t1 = min(end, k.t0 + A.chunk);
+  k.t0 = k.start + k.c * chunk;
+  k.t1 = min(end, k.t0 + chunk);
   return k;
 }
 
@@ -128,6 +125,14 @@ __device__ __forceinline__ const ScanArgs &scan_args() {
   uintptr_t p = (uintptr_t)__builtin_amdgcn_kernarg_segment_ptr();
   asm("" : "+s"(p));
   return *(const ScanArgs *)(const ScanArgs __attribute__((address_space(4))) *)p;
+}
+// The slot of the chunks from zero (M of them in one of k's) that chunk k begins
+// with, and ends with.
+__device__ __forceinline__ int64_t scan_first_part(const ScanArgs &A, const ScanChunk &k) {
+  return k.start / A.part + k.i + (int64_t)k.c * (A.chunk / A.part);
+}
+__device__ __forceinline__ int64_t scan_last_part(const ScanArgs &A, const ScanChunk &k) {
+  return k.start / A.part + k.i + (k.t1 - k.start + A.part - 1) / A.part - 1;
 }
 // A channel's states from or to [states][channels] or [channels][states]
 template <int N>

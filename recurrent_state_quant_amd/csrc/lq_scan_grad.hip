@@ -18,13 +18,13 @@
 namespace lq {
 
 // The chunks' gradients behind from zero: what comes out of their first token.
-template <class E, int N>
-__global__ __launch_bounds__(256) void scan_grad_local_kernel(const ScanArgs A, int tiles, int64_t waves) {
+template <class E, int N, bool GATE>
+__global__ __launch_bounds__(256, 4) void scan_grad_local_kernel(const ScanArgs A, int tiles, int64_t waves) {
   const int lane = threadIdx.x & 63;
   const int64_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) + (int64_t)blockIdx.x * 4;
   if (wave >= waves) return;
   const int slot = (int)(wave / tiles), tile = (int)(wave % tiles), tg = (A.per + 63) >> 6;
-  const ScanChunk k = scan_chunk(A, slot, lane);
+  const ScanChunk k = scan_chunk(A, A.part, slot, lane);
   if (!k.any || k.c == 0) return;  // nothing comes before the first chunk
   const ScanTile ch = scan_tile(A, tile / tg, tile % tg, lane);
   const int64_t width = A.channels;
@@ -33,37 +33,43 @@ __global__ __launch_bounds__(256) void scan_grad_local_kernel(const ScanArgs A, 
 #pragma unroll
   for (int n = 0; n < N; ++n) g[n] = 0.f;
   const float bias = A.bias ? A.bias[ch.c] : 0.f;
-  const bool gate = A.z.ptr;
-  const E *dt = at<const E>(A.dt, 0, 0) + ch.c, *dy = at<const E>(A.dy, 0, 0) + ch.c;
-  const E *z = gate ? at<const E>(A.z, 0, 0) + ch.c : dy;
   constexpr int ahead = 8;
   E rd[ahead], ry[ahead], rz[ahead];
   const auto load = [&](int t) {  // tokens t, t - 1 ..
+    const ScanArgs &P = scan_args();
+    const E *dt = at<const E>(P.dt, t, 0), *dy = at<const E>(P.dy, t, 0), *z = GATE ? at<const E>(P.z, t, 0) : dy;
 #pragma unroll
     for (int u = 0; u < ahead; ++u) {
-      const int64_t tt = max(t - u, k.t0);
-      rd[u] = dt[tt * A.dt.ts];
-      ry[u] = dy[tt * A.dy.ts];
-      if (gate) rz[u] = z[tt * A.z.ts];
+      rd[u] = lane_load(dt, ch.c);
+      ry[u] = lane_load(dy, ch.c);
+      if (GATE) rz[u] = lane_load(z, ch.c);
+      if (t - u > k.t0) {
+        dt -= P.dt.ts;
+        dy -= P.dy.ts;
+        if (GATE) z -= P.z.ts;
+      }
     }
   };
+  ScanRow<E, N> C;
   load(k.t1 - 1);
+  C.load(A.C, k.t1 - 1, ch.g);
   for (int t = k.t1 - 1; t >= k.t0; t -= ahead) {
     float fd[ahead], fy[ahead], fz[ahead];
 #pragma unroll
     for (int u = 0; u < ahead; ++u) {
       fd[u] = to_f(rd[u]) + bias;
       fy[u] = to_f(ry[u]);
-      fz[u] = gate ? to_f(rz[u]) : 0.f;
+      fz[u] = GATE ? to_f(rz[u]) : 0.f;
     }
     if (t - ahead >= k.t0) load(t - ahead);
 #pragma unroll
     for (int u = 0; u < ahead; ++u) {
-      if (t - u < k.t0) break;
-      float cc[N];
-      scan_row<E, N>(A.C, t - u, ch.g, cc);
-      const float d = scan_step(A, fd[u]);
-      const float dp = gate ? fy[u] * (fz[u] * sigmoid(fz[u])) : fy[u];
+      __builtin_amdgcn_sched_barrier(0);
+      const ScanRow<E, N> cc = C;
+      C.load(A.C, max(t - u - 1, k.t0), ch.g);
+      const bool in = t - u >= k.t0;  // before the chunk's beginning: a step of zero
+      const float d = in ? scan_step(A, fd[u]) : 0.f;
+      const float dp = !in ? 0.f : GATE ? fy[u] * (fz[u] * sigmoid_for<E>(fz[u])) : fy[u];
       sum += d;
 #pragma unroll
       for (int n = 0; n < N; ++n) g[n] = __builtin_amdgcn_exp2f(d * a2[n]) * fmaf(cc[n], dp, g[n]);
@@ -77,7 +83,7 @@ __global__ __launch_bounds__(256) void scan_grad_local_kernel(const ScanArgs A, 
 // The gradients behind every chunk of the sequences with several, over the
 // chunks' own: thread (sequence, state, channel), the last chunk first.  dS is
 // copied behind the last chunk, as dS0 may lie over it.
-constexpr int kCarryAhead = 8;
+constexpr int kCarryAhead = 16;
 __global__ __launch_bounds__(256) void scan_grad_carry_kernel(const ScanArgs A, int states, int64_t threads) {
   const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (id >= threads) return;
@@ -87,9 +93,9 @@ __global__ __launch_bounds__(256) void scan_grad_carry_kernel(const ScanArgs A, 
     return o < 0 ? 0 : (o > A.tokens ? (int)A.tokens : o);
   };
   const int start = offset(i), end = max(start, offset(i + 1));
-  const int chunks = (end - start + A.chunk - 1) / A.chunk;
+  const int chunks = (end - start + A.part - 1) / A.part;
   if (chunks < 2) return;
-  const int64_t slot = start / A.chunk + i;
+  const int64_t slot = start / A.part + i;
   const float a2 = A.A[c * states + n] * kLog2e;
   float g = A.dS ? A.dS[(i * width + c) * states + n] : 0.f;
   float *carry = A.carry + (slot * states + n) * width + c;
@@ -99,9 +105,9 @@ __global__ __launch_bounds__(256) void scan_grad_carry_kernel(const ScanArgs A, 
     float v[kCarryAhead], s[kCarryAhead];
 #pragma unroll
     for (int u = 0; u < kCarryAhead; ++u) {
-      const bool in = k - u > 0;
-      v[u] = in ? carry[(k - u) * step] : 0.f;
-      s[u] = in ? sum[(k - u) * width] : 0.f;
+      const int64_t at = max(k - u, 1);  // (chunk 0 has none: nothing comes before it)
+      v[u] = carry[at * step];
+      s[u] = sum[at * width];
     }
 #pragma unroll
     for (int u = 0; u < kCarryAhead; ++u) {
@@ -112,32 +118,40 @@ __global__ __launch_bounds__(256) void scan_grad_carry_kernel(const ScanArgs A, 
   }
 }
 
-// Sums across the wave of many registers, on the matrix pipe beside the vector
-// work.  Four products of 16 blocks, (4 x 1) times (1 x 4) with a row that is one
-// in its n-th place, put the four lanes of each block of the n-th register into
-// four registers of one lane, where they are added: 4 registers become one, lane 4
-// b + n holding the sum of block b.  Of those, products of 16 x 4 times 4 x 16 with
-// a matrix that is one in its q-th column add every fourth block: register r of
-// lane 16 g + q then holds a fourth (of blocks g, g + 4 ..) of the sum of register
-// 4 q + r.  The fourths are added where the waves' sums meet.
-__device__ __forceinline__ float sum_blocks(const float (&v)[4], const float (&one)[4]) {
-  floatx4 x = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int n = 0; n < 4; ++n) x = __builtin_amdgcn_mfma_f32_4x4x1f32(v[n], one[n], x, 0, 0, 0);
-  return (x[0] + x[1]) + (x[2] + x[3]);
+// Sums of many registers over the 16 lanes of a row at once: two registers become
+// one, in which half of the lanes go on with the one and half with the other.
+// Three instructions a step, 90 for 32 sums (8,192 tokens x 2,048 channels 296 us;
+// with four-lane sums by products of ones on the matrix pipe 350, whose
+// instructions wait for it and for one another).
+template <int CTRL>
+__device__ __forceinline__ float fold2(float a, float b, bool high) {
+  return (high ? b : a) + dpp<CTRL>(high ? a : b);
+}
+// Afterwards lanes with bits 3 and 2 of (0, 0), (1, 0), (0, 1), (1, 1) hold a, b, c, d.
+__device__ __forceinline__ float fold4(const float (&v)[4], int lane) {
+  const float x = fold2<0x128>(v[0], v[1], lane & 8), y = fold2<0x128>(v[2], v[3], lane & 8);  // row_ror:8
+  return fold2<0x141>(x, y, lane & 4);  // row_half_mirror
+}
+// Four of those: the sum of a row in every lane, number fold_place.
+__device__ __forceinline__ float fold16(const float (&v)[4], int lane) {
+  const float x = fold2<0x4E>(v[0], v[1], lane & 2), y = fold2<0x4E>(v[2], v[3], lane & 2);  // quad_perm [2,3,0,1]
+  return fold2<0xB1>(x, y, lane & 1);  // quad_perm [1,0,3,2]
+}
+__device__ __forceinline__ int fold_place(int lane) {
+  return 8 * (lane & 1) + 4 * (lane >> 1 & 1) + 2 * (lane >> 2 & 1) + (lane >> 3 & 1);
 }
 
 // A block's four waves share a group and a chunk: their sums over the channels
 // meet in LDS after every run of tokens.
 template <class E, int N, bool GATE>
-__global__ __launch_bounds__(256, N > 16 ? 1 : 2) void scan_grad_kernel(const ScanArgs A, int blocks_group) {
-  constexpr int shift = scan_sub_shift(N), sub = 1 << shift, Q = N / 2;  // Q: fours of sums
-  __shared__ float sh[2][sub][16][2 * N];
+__global__ __launch_bounds__(256, scan_grad_waves(N)) void scan_grad_kernel(const ScanArgs A, int blocks_group) {
+  constexpr int shift = scan_sub_shift(N), sub = 1 << shift, Q = N / 2;  // Q: fours of sums, dB's and dC's
+  __shared__ float sh[2][sub][16][2 * N + 4];
   const int lane = threadIdx.x & 63, w4 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int blocks = A.groups * blocks_group;
   const int slot = blockIdx.x / blocks, gb = blockIdx.x % blocks;
   const int group = gb / blocks_group, tile = gb % blocks_group * 4 + w4;
-  const ScanChunk k = scan_chunk(A, slot, lane);
+  const ScanChunk k = scan_chunk(A, A.chunk, slot, lane);
   const ScanTile ch = scan_tile(A, group, tile, lane);
   const int64_t width = A.channels;
   float a2[N], g[N], dA[N], dskip = 0.f, dbias = 0.f;
@@ -147,18 +161,14 @@ __global__ __launch_bounds__(256, N > 16 ? 1 : 2) void scan_grad_kernel(const Sc
     scan_decays<N>(A, ch.c, a2);
     if (ch.on) {
       if (k.chunks > 1)
-        scan_load_cols<N>(A.carry + (int64_t)slot * N * width, width, ch.c, g);
+        scan_load_cols<N>(A.carry + scan_last_part(A, k) * N * width, width, ch.c, g);
       else if (A.dS)
         scan_load_rows<N>(A.dS, k.i * width + ch.c, g);
     }
     const float bias = A.bias ? A.bias[ch.c] : 0.f, skip = A.skip ? A.skip[ch.c] : 0.f;
     const int len = k.t1 - k.t0, runs = (len + sub - 1) >> shift;
     const int64_t first = (k.start >> shift) + k.i + ((k.t0 - k.start) >> shift);
-    float one4[4], one16[Q];
-#pragma unroll
-    for (int n = 0; n < 4; ++n) one4[n] = (lane & 3) == n ? 1.f : 0.f;
-#pragma unroll
-    for (int q = 0; q < Q; ++q) one16[q] = (lane & 15) == q ? 1.f : 0.f;
+    const int place = fold_place(lane);
     E rx[sub], rd[sub], ry[sub], rz[sub];
     float start[N];  // the states before the run's tokens
     const auto load = [&](int r) {
@@ -179,9 +189,14 @@ __global__ __launch_bounds__(256, N > 16 ? 1 : 2) void scan_grad_kernel(const Sc
           if (GATE) z += P.z.ts;
         }
       }
-      scan_load_cols<N>(P.check + (first + r) * N * width, width, ch.c, start);
     };
-    if (runs) load(runs - 1);
+    const auto load_start = [&](int r) {
+      scan_load_cols<N>(scan_args().check + (first + r) * N * width, width, ch.c, start);
+    };
+    if (runs) {
+      load(runs - 1);
+      load_start(runs - 1);
+    }
     for (int r = runs - 1; r >= 0; --r) {
       const int t = k.t0 + (r << shift), n_t = min(sub, k.t1 - t);
       float fx[sub], fd[sub], fy[sub], fz[sub], slope[sub], hist[sub][N];
@@ -194,6 +209,14 @@ __global__ __launch_bounds__(256, N > 16 ? 1 : 2) void scan_grad_kernel(const Sc
       }
 #pragma unroll
       for (int n = 0; n < N; ++n) hist[0][n] = start[n];
+      if (r > 0) load(r - 1);
+      // the output rows of the run's last token, and the way to the one before:
+      // reading them for each token would wait for the rows of B and C on their way
+      const ScanArgs &P = scan_args();
+      int64_t step_x = P.dx.ts, step_t = P.ddt.ts, step_z = GATE ? P.dz.ts : 0;
+      E *out_x = at<E>(P.dx, t + sub - 1, 0), *out_t = at<E>(P.ddt, t + sub - 1, 0);
+      E *out_z = GATE ? at<E>(P.dz, t + sub - 1, 0) : nullptr;
+      asm volatile("" : "+s"(step_x), "+s"(step_t), "+s"(step_z), "+s"(out_x), "+s"(out_t), "+s"(out_z));
       ScanRow<E, N> B, C;
       B.load(A.B, t, ch.g);
 #pragma unroll
@@ -210,27 +233,29 @@ __global__ __launch_bounds__(256, N > 16 ? 1 : 2) void scan_grad_kernel(const Sc
         const float dx = fd[u] * fx[u];
 #pragma unroll
         for (int n = 0; n < N; ++n)
-          hist[u + 1][n] = fmaf(__builtin_amdgcn_exp2f(fd[u] * a2[n]), hist[u][n], dx * b[n]);
+          hist[u + 1][n] = fmaf(__builtin_amdgcn_exp2f(fd[u] * a2[n]), hist[u][n], scan_times<E>(dx, b[n]));
       }
 #pragma unroll
       for (int u = sub - 1; u >= 0; --u) {
         __builtin_amdgcn_sched_barrier(0);
-        if (u == 0 && r > 0) load(r - 1);  // into the registers of the tokens that are done
+        if (u == 1 && r > 0) load_start(r - 1);  // into the registers of the tokens that are done
         const ScanRow<E, N> b = B, cc = C;
         if (u > 0) {
           B.load(A.B, min(t + u - 1, k.t1 - 1), ch.g);
           C.load(A.C, min(t + u - 1, k.t1 - 1), ch.g);
         }
         float d = fd[u];
-        asm("" : "+v"(d));  // the decays again: keeping those of the run would cost 48 registers
+        // the decays again, but for those used next: keeping the run's would cost 32
+        // registers more
+        if (u + 2 != sub || N != 16) asm("" : "+v"(d));
         const float xd = d * fx[u];
         float s = 0.f, dp = fy[u];
         if (GATE) {
-          s = sigmoid(fz[u]);
+          s = sigmoid_for<E>(fz[u]);
           dp *= fz[u] * s;
         }
         float p = skip * fx[u], gb = 0.f, ea = 0.f;
-        floatx4 acc = {0.f, 0.f, 0.f, 0.f};
+        float fold[Q];
 #pragma unroll
         for (int q = 0; q < N / 4; ++q) {
           float vb[4], vc[4];
@@ -249,30 +274,36 @@ __global__ __launch_bounds__(256, N > 16 ? 1 : 2) void scan_grad_kernel(const Sc
             vc[m] = dp * h;
             g[n] = gn * a;
           }
-          // sums 0 .. N - 1 are dB's, N .. 2 N - 1 dC's
-          acc = __builtin_amdgcn_mfma_f32_16x16x4f32(sum_blocks(vb, one4), one16[q], acc, 0, 0, 0);
-          acc = __builtin_amdgcn_mfma_f32_16x16x4f32(sum_blocks(vc, one4), one16[N / 4 + q], acc, 0, 0, 0);
+          fold[q] = fold4(vb, lane);
+          fold[N / 4 + q] = fold4(vc, lane);
         }
-        if ((lane & 15) < Q)
-          *reinterpret_cast<floatx4 *>(&sh[r & 1][u][w4 * 4 + (lane >> 4)][(lane & 15) * 4]) = acc;
+#pragma unroll
+        for (int q = 0; q < Q; q += 4) {
+          const float four[4] = {fold[q], fold[q + 1], fold[q + 2], fold[q + 3]};
+          sh[r & 1][u][w4 * 4 + (lane >> 4)][4 * q + place] = fold16(four, lane);
+        }
         const float ddt = fmaf(gb, fx[u], ea * kLn2) * slope[u];
         const float dz = fy[u] * p * (s * fmaf(fz[u], 1.f - s, 1.f));
         dskip = fmaf(dp, fx[u], dskip);
         dbias += u < n_t ? ddt : 0.f;
         if (ch.on && u < n_t) {
-          const ScanArgs &P = scan_args();
-          lane_store(at<E>(P.dx, t + u, 0), ch.c, from_f<E>(fmaf(gb, d, skip * dp)));
-          lane_store(at<E>(P.ddt, t + u, 0), ch.c, from_f<E>(ddt));
-          if (GATE) lane_store(at<E>(P.dz, t + u, 0), ch.c, from_f<E>(dz));
+          lane_store(out_x, ch.c, from_f<E>(fmaf(gb, d, skip * dp)));
+          lane_store(out_t, ch.c, from_f<E>(ddt));
+          if (GATE) lane_store(out_z, ch.c, from_f<E>(dz));
         }
+        out_x -= step_x;
+        out_t -= step_t;
+        if (GATE) out_z -= step_z;
       }
       __syncthreads();  // (the other half of `sh` is written next)
-      for (int v = threadIdx.x; v < n_t * 2 * N; v += 256) {
-        const int u = v / (2 * N), n = v % (2 * N);
+      // two lanes a sum, eight of its sixteen shares each
+      for (int v = threadIdx.x; v < n_t * 4 * N; v += 256) {
+        const int u = v / (4 * N), n = v % (4 * N) / 2, m0 = (v & 1) * 8;
         float y = 0.f;
 #pragma unroll
-        for (int m = 0; m < 16; ++m) y += sh[r & 1][u][m][n];
-        A.part_bc[((int64_t)gb * A.tokens + t + u) * 2 * N + n] = y;
+        for (int m = 0; m < 8; ++m) y += sh[r & 1][u][m0 + m][n];
+        y += dpp<0xB1>(y);
+        if (!(v & 1)) A.part_bc[((int64_t)gb * A.tokens + t + u) * 2 * N + n] = y;
       }
     }
     if (A.dS0 && k.c == 0 && ch.on) scan_store_rows<N>(A.dS0, k.i * width + ch.c, g);
@@ -333,10 +364,14 @@ __global__ __launch_bounds__(512) void scan_grad_sum_kernel(const ScanArgs A, in
 
 template <class E, int N>
 static hipError_t scan_back(const ScanArgs &a, hipStream_t stream) {
-  const int64_t tiles = scan_tiles(a.channels, a.groups), waves = tiles * a.slots, blocks = scan_group_blocks(a.per);
+  const int64_t tiles = scan_tiles(a.channels, a.groups), blocks = scan_group_blocks(a.per);
   if (a.tokens > a.chunk) {
-    hipLaunchKernelGGL((scan_grad_local_kernel<E, N>), dim3((unsigned)((waves + 3) / 4)), dim3(256), 0, stream, a,
-                       (int)tiles, waves);
+    const int64_t parts = tiles * scan_slots(a.tokens, a.seqs, a.part);
+    const dim3 grid((unsigned)((parts + 3) / 4));
+    if (a.z.ptr)
+      hipLaunchKernelGGL((scan_grad_local_kernel<E, N, true>), grid, dim3(256), 0, stream, a, (int)tiles, parts);
+    else
+      hipLaunchKernelGGL((scan_grad_local_kernel<E, N, false>), grid, dim3(256), 0, stream, a, (int)tiles, parts);
     const int64_t threads = (int64_t)a.seqs * a.channels * N;
     hipLaunchKernelGGL(scan_grad_carry_kernel, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, stream, a, N,
                        threads);
