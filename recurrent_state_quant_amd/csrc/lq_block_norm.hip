@@ -156,10 +156,14 @@ __global__ __launch_bounds__(norm_threads<LANES>()) void block_norm_kernel(const
 // Workgroups of the backward pass take rows in turn and hold their weight gradients
 // in LDS, each lane's own columns for each row of a workgroup: in registers they
 // would take the room of a third wave a SIMD.
-constexpr int kBlockNormBlocks = 512;
+// Three workgroups of 256 threads a CU where a lane has one piece, two with two
+// pieces, one of 512 threads.
+static int64_t norm_most_blocks(int dim) {
+  return dim <= 512 ? 768 : dim <= 1024 ? 512 : dim <= 2048 ? 768 : dim <= 4096 ? 512 : 256;
+}
 
 template <class E, class S, int LANES, int R>
-__global__ __launch_bounds__(norm_threads<LANES>(), 2) void block_norm_backward_kernel(const BlockNormArgs A, int64_t rows) {
+__global__ __launch_bounds__(norm_threads<LANES>(), R == 1 ? 3 : 2) void block_norm_backward_kernel(const BlockNormArgs A, int64_t rows) {
   constexpr int threads = norm_threads<LANES>(), per = threads / LANES;
   __shared__ float2 sh[LANES > 64 ? 2 * (LANES / 64) : 1];
   __shared__ float sum[per][2][LANES * R * 8];
@@ -385,7 +389,7 @@ static int norm_lanes(int dim) { return dim <= 128 ? 16 : dim <= 1024 ? 64 : dim
 int64_t block_norm_blocks(int64_t rows, int dim) {
   const int lanes = norm_lanes(dim), per = lanes < 256 ? 256 / lanes : 1;
   const int64_t b = (rows + per - 1) / per;
-  return b < kBlockNormBlocks ? b : kBlockNormBlocks;
+  return b < norm_most_blocks(dim) ? b : norm_most_blocks(dim);
 }
 
 template <class E, class S, int LANES, int R>

@@ -108,10 +108,17 @@ __global__ __launch_bounds__(256) void conv_kernel(const ConvArgs A, int tiles, 
   float w[K][V], b[V], win[K - 1][V];
   conv_weights<V, K>(A, c, w, b);
   int in = -1;  // the sequence that `win` is of
+  Vec<E, V> next[kConvAhead];
+  const auto load = [&](int t) {
+#pragma unroll
+    for (int u = 0; u < kConvAhead; ++u) next[u] = vec_load<E, V>(at<const E>(A.x, min(t + u, t1 - 1), 0) + c);
+  };
+  load(t0);
   for (int t = t0; t < t1; t += kConvAhead) {
     Vec<E, V> raw[kConvAhead];
 #pragma unroll
-    for (int u = 0; u < kConvAhead; ++u) raw[u] = vec_load<E, V>(at<const E>(A.x, min(t + u, t1 - 1), 0) + c);
+    for (int u = 0; u < kConvAhead; ++u) raw[u] = next[u];
+    if (t + kConvAhead < t1) load(t + kConvAhead);
 #pragma unroll
     for (int u = 0; u < kConvAhead; ++u) {
       const int tt = t + u;
@@ -206,14 +213,24 @@ __global__ __launch_bounds__(256) void conv_backward_kernel(const ConvArgs A, in
       int in = -1;  // the sequence that `win` and `acc` are of
       const int stop = (int)min((int64_t)t1 + K - 1, A.tokens);
       bool open = true;
+      Vec<E, V> nx[kConvAhead], ng[kConvAhead];
+      const auto load = [&](int t) {
+#pragma unroll
+        for (int u = 0; u < kConvAhead; ++u) {
+          const int tt = min(t + u, stop - 1);
+          nx[u] = vec_load<E, V>(at<const E>(A.x, tt, 0) + c);
+          ng[u] = vec_load<E, V>(at<const E>(A.dy, tt, 0) + c);
+        }
+      };
+      load(t0);
       for (int t = t0; t < stop && open; t += kConvAhead) {
         Vec<E, V> rx[kConvAhead], rg[kConvAhead];
 #pragma unroll
         for (int u = 0; u < kConvAhead; ++u) {
-          const int tt = min(t + u, stop - 1);
-          rx[u] = vec_load<E, V>(at<const E>(A.x, tt, 0) + c);
-          rg[u] = vec_load<E, V>(at<const E>(A.dy, tt, 0) + c);
+          rx[u] = nx[u];
+          rg[u] = ng[u];
         }
+        if (t + kConvAhead < stop) load(t + kConvAhead);
 #pragma unroll
         for (int u = 0; u < kConvAhead; ++u) {
           const int tt = t + u;
@@ -376,10 +393,11 @@ static hipError_t conv_step(const ConvArgs &a, hipStream_t stream) {
 template <class E, int V, int K>
 static hipError_t conv_backward(const ConvArgs &a, hipStream_t stream) {
   const int tiles = (a.channels + 64 * V - 1) / (64 * V);
-  const int64_t blocks = conv_grad_blocks(a.tokens);
+  const int run = conv_grad_run(a.tokens, a.channels);
+  const int64_t blocks = conv_grad_blocks(a.tokens, run);
   if (blocks)
     hipLaunchKernelGGL((conv_backward_kernel<E, V, K>), dim3((unsigned)(blocks * tiles)), dim3(256), 0, stream, a, tiles,
-                       conv_grad_run(a.tokens));
+                       run);
   if (a.dw || a.dbias)
     hipLaunchKernelGGL(conv_weight_kernel, dim3((unsigned)(((int64_t)(K + 1) * a.channels + 255) / 256)), dim3(256), 0,
                        stream, a, blocks);

@@ -32,17 +32,18 @@ struct ConvArgs {
 };
 
 // Tokens of a run of the backward pass: a block takes four runs of the same
-// channels and joins their weight gradients.  Runs grow once there are 256
-// blocks of them, so the joined sums stay few.
+// channels and joins their weight gradients.  Longer runs share more of the tokens
+// around them, once there are waves enough for three a SIMD (64 channels of four
+// values a wave); and grow once there are 256 blocks of them, so that the joined
+// sums stay few.
 constexpr int kConvRunLeast = 32, kConvRunMost = 4096;
 constexpr int64_t kConvBlocks = 256;
-inline int conv_grad_run(int64_t tokens) {
-  int run = kConvRunLeast;
-  while (run < kConvRunMost && tokens > int64_t(run) * 4 * kConvBlocks) run *= 2;
+inline int64_t conv_grad_blocks(int64_t tokens, int64_t run) { return (tokens + 4 * run - 1) / (4 * run); }
+inline int conv_grad_run(int64_t tokens, int64_t channels) {
+  int run = tokens / (2 * kConvRunLeast) * ((channels + 255) / 256) >= 3072 ? 2 * kConvRunLeast : kConvRunLeast;
+  while (run < kConvRunMost && conv_grad_blocks(tokens, run) > kConvBlocks) run *= 2;
   return run;
 }
-inline int64_t conv_grad_blocks(int64_t tokens, int64_t run) { return (tokens + 4 * run - 1) / (4 * run); }
-inline int64_t conv_grad_blocks(int64_t tokens) { return conv_grad_blocks(tokens, conv_grad_run(tokens)); }
 // The most blocks of any call with at most these tokens
 inline int64_t conv_grad_most(int64_t tokens) {
   const int64_t few = conv_grad_blocks(tokens, kConvRunLeast), many = conv_grad_blocks(tokens, kConvRunMost);

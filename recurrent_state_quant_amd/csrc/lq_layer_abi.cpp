@@ -316,7 +316,7 @@ int leapquant_conv_backward(const lq_conv *cv, const int32_t *cu_seqlens, const 
   bl.add_out(dense(dweight, int64_t(cv->channels) * cv->width * 4));
   bl.add_out(dense(dbias, int64_t(cv->channels) * 4));
   if (dweight || dbias) {
-    const int64_t need = conv_space(cv, lq::conv_grad_blocks(cv->tokens));
+    const int64_t need = conv_space(cv, lq::conv_grad_blocks(cv->tokens, lq::conv_grad_run(cv->tokens, cv->channels)));
     if (need) {
       if (!workspace) return LQ_ERR_NULL;
       if (!aligned(workspace, 16)) return LQ_ERR_ALIGN;

@@ -316,33 +316,33 @@ __global__ __launch_bounds__(256, scan_grad_waves(N)) void scan_grad_kernel(cons
   part[(N + 1) * width + ch.c] = dbias;
 }
 
-// dB and dC: the blocks' sums over the channels, added in order; thread (token,
-// group, state of B or C)
+// The sums of the workgroups and chunks, added in order, in one launch.  The first
+// `blocks_bc` workgroups: dB and dC over the workgroups of a group, thread (token,
+// group, state of B or C).  The others: dA, dD and dbias over the chunks, workgroup
+// (64 channels, state), wave (a share of the slots).
 template <class E>
-__global__ __launch_bounds__(256) void scan_grad_bc_kernel(const ScanArgs A, int states, int blocks_group, int64_t threads) {
-  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (id >= threads) return;
-  const int n = (int)(id % (2 * states)), g = (int)(id / (2 * states) % A.groups);
-  const int64_t t = id / (2 * states) / A.groups;
-  const int lo = A.cu[0], hi = A.cu[A.seqs];
-  if (t < lo || t >= hi) return;  // of no sequence
-  float x = 0.f;
-#pragma unroll 4
-  for (int b = 0; b < blocks_group; ++b)
-    x += A.part_bc[(((int64_t)g * blocks_group + b) * A.tokens + t) * 2 * states + n];
-  if (n < states)
-    at<E>(A.dB, t, g)[n] = from_f<E>(x);
-  else
-    at<E>(A.dC, t, g)[n - states] = from_f<E>(x);
-}
-
-// dA, dD and dbias: the chunks' sums, added in order.  Workgroup (64 channels,
-// state), wave (a share of the slots).
-__global__ __launch_bounds__(512) void scan_grad_sum_kernel(const ScanArgs A, int states) {
+__global__ __launch_bounds__(512) void scan_grad_sum_kernel(const ScanArgs A, int states, int blocks_group,
+                                                            int64_t blocks_bc) {
   __shared__ float sh[8][64];
+  if (blockIdx.x < blocks_bc) {
+    const int64_t id = (int64_t)blockIdx.x * 512 + threadIdx.x;
+    const int n = (int)(id % (2 * states)), g = (int)(id / (2 * states) % A.groups);
+    const int64_t t = id / (2 * states) / A.groups;
+    if (t < A.cu[0] || t >= A.cu[A.seqs] || t >= A.tokens) return;  // of no sequence
+    float x = 0.f;
+#pragma unroll 4
+    for (int b = 0; b < blocks_group; ++b)
+      x += A.part_bc[(((int64_t)g * blocks_group + b) * A.tokens + t) * 2 * states + n];
+    if (n < states)
+      at<E>(A.dB, t, g)[n] = from_f<E>(x);
+    else
+      at<E>(A.dC, t, g)[n - states] = from_f<E>(x);
+    return;
+  }
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int tiles = (A.channels + 63) >> 6, k = blockIdx.x / tiles;
-  const int64_t width = A.channels, c = (int64_t)(blockIdx.x % tiles) * 64 + lane;
+  const int64_t block = blockIdx.x - blocks_bc;
+  const int tiles = (A.channels + 63) >> 6, k = (int)(block / tiles);
+  const int64_t width = A.channels, c = (block % tiles) * 64 + lane;
   float x = 0.f;
   if (c < width) {
 #pragma unroll 8
@@ -381,11 +381,10 @@ static hipError_t scan_back(const ScanArgs &a, hipStream_t stream) {
     hipLaunchKernelGGL((scan_grad_kernel<E, N, true>), grid, dim3(256), 0, stream, a, (int)blocks);
   else
     hipLaunchKernelGGL((scan_grad_kernel<E, N, false>), grid, dim3(256), 0, stream, a, (int)blocks);
-  const int64_t threads = a.tokens * a.groups * 2 * N;
-  if (threads)
-    hipLaunchKernelGGL((scan_grad_bc_kernel<E>), dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, stream, a, N,
-                       (int)blocks, threads);
-  hipLaunchKernelGGL(scan_grad_sum_kernel, dim3((unsigned)((a.channels + 63) / 64 * (N + 2))), dim3(512), 0, stream, a, N);
+  const int64_t blocks_bc = (a.tokens * a.groups * 2 * N + 511) / 512;
+  const int64_t blocks_sum = (int64_t)((a.channels + 63) / 64) * (N + 2);
+  hipLaunchKernelGGL((scan_grad_sum_kernel<E>), dim3((unsigned)(blocks_bc + blocks_sum)), dim3(512), 0, stream, a, N,
+                     (int)blocks, blocks_bc);
   return hipGetLastError();
 }
 template <class E>
