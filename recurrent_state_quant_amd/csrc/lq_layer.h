@@ -53,7 +53,7 @@ inline int64_t conv_grad_most(int64_t tokens) {
 struct ScanArgs {
   int64_t tokens, slots;
   int seqs, channels, groups, per;  // per: channels of a group
-  int chunk;                        // tokens of a chunk, a multiple of 16
+  int chunk;                        // tokens of a chunk, a multiple of 8
   int part;                         // tokens of a chunk from zero: chunk, or half of it
   int softplus;
   const int32_t *cu;
@@ -61,7 +61,7 @@ struct ScanArgs {
   const float *A, *skip, *bias;
   const float *S0;  // [seqs][channels][states] or nullptr (zeros)
   float *S;         // or nullptr
-  float *check;     // [sub slots][states][channels] or nullptr: the state before every kSub(states)-th token of a sequence
+  float *check;     // [scan_checks][states][channels] or nullptr: the states before every kScanSub-th token of a sequence
   float *carry;     // [part slots][states][channels]  of sequences with several: the state before (backward: gradient behind)
   float *sum;       // [part slots][channels]          the sum of a part's steps
   // step
@@ -76,12 +76,11 @@ struct ScanArgs {
   float *part_a;   // [slots][states + 2][channels]
 };
 
-// Tokens whose states the gradient holds in registers at once: 8 x 16 or 4 x 32
-// values a channel.
-constexpr int scan_sub_shift(int states) { return states > 8 ? 2 : 3; }
-inline int64_t scan_checks(int64_t tokens, int64_t seqs, int states) {
-  return (tokens >> scan_sub_shift(states)) + seqs;
-}
+// Tokens whose states the gradient holds in registers at once, and so how often
+// the forward pass keeps a state.  Twice as many would halve the kept states'
+// memory, but leave room for one wave a SIMD with 16 states.
+constexpr int kScanSub = 4;
+inline int64_t scan_checks(int64_t tokens, int64_t seqs) { return tokens / kScanSub + seqs; }
 
 // Waves take 64 channels of one group and one chunk of tokens.
 inline int64_t scan_tiles(int channels, int groups) {
@@ -120,7 +119,7 @@ inline int scan_forward_chunk(int64_t tokens, int64_t seqs, int channels, int gr
 }
 // Of the gradient; its chunks from zero are half as long, as their kernel has
 // room for more waves.
-constexpr int scan_grad_waves(int states) { return states > 16 ? 1 : 2; }
+constexpr int scan_grad_waves(int states) { return states > 16 ? 1 : states > 8 ? 2 : 3; }
 inline int scan_grad_chunk(int64_t tokens, int64_t seqs, int channels, int groups, int states) {
   return scan_chunk_tokens(tokens, seqs, groups * scan_group_blocks(channels / groups), kScanPart,
                            scan_grad_waves(states), 0.7);

@@ -98,7 +98,7 @@ int64_t scan_space(const lq_scan *sc, bool save, char *base, lq::ScanArgs *a) {
     used += (bytes + 15) / 16 * 16;
   };
   if (!save && sc->tokens <= lq::kScanLeast) return 0;  // no sequence has two chunks
-  if (save) take(&a->check, lq::scan_checks(sc->tokens, sc->seqs, sc->states) * state);
+  if (save) take(&a->check, lq::scan_checks(sc->tokens, sc->seqs) * state);
   take(&a->carry, slots * state);
   take(&a->sum, slots * channels * 4);
   if (save) {

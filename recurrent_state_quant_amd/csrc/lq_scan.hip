@@ -41,7 +41,6 @@ __global__ __launch_bounds__(256, scan_forward_waves(N)) void scan_kernel(const 
   }
   const float bias = A.bias ? A.bias[ch.c] : 0.f, skip = OUT && A.skip ? A.skip[ch.c] : 0.f;
   const bool save = OUT && A.check;
-  constexpr int shift = scan_sub_shift(N), sub = 1 << shift;
   E rx[kScanAhead], rd[kScanAhead], rz[kScanAhead];
   const auto load = [&](int t) {
     const ScanArgs &P = scan_args();
@@ -84,8 +83,8 @@ __global__ __launch_bounds__(256, scan_forward_waves(N)) void scan_kernel(const 
       const int next = min(tt + 1, k.t1 - 1);
       B.load(A.B, next, ch.g);
       if (OUT) C.load(A.C, next, ch.g);
-      if (OUT && u % sub == 0 && save && tt < k.t1) {
-        const int64_t s = (k.start >> shift) + k.i + ((tt - k.start) >> shift);
+      if (OUT && u % kScanSub == 0 && save && tt < k.t1) {
+        const int64_t s = k.start / kScanSub + k.i + (tt - k.start) / kScanSub;
         if (ch.on) scan_store_cols<N>(A.check + s * N * width, width, ch.c, h);
       }
       // past the chunk's end: a step of zero

@@ -10,9 +10,9 @@
 //
 // As forward, a lane holds a channel and a wave 64 channels and a chunk; the
 // gradients behind every chunk come from the chunks' own, begun from zero, as the
-// states do.  The forward pass left the state before every 8th token (4th with
-// 32 states): a run of tokens is computed again from it, its states stay in
-// registers, and the run is taken backwards.
+// states do.  The forward pass left the states before every fourth token: such a run
+// is computed again from them, its states stay in registers, and it is taken
+// backwards.
 #include "lq_scan_device.h"
 
 namespace lq {
@@ -145,7 +145,7 @@ __device__ __forceinline__ int fold_place(int lane) {
 // meet in LDS after every run of tokens.
 template <class E, int N, bool GATE>
 __global__ __launch_bounds__(256, scan_grad_waves(N)) void scan_grad_kernel(const ScanArgs A, int blocks_group) {
-  constexpr int shift = scan_sub_shift(N), sub = 1 << shift, Q = N / 2;  // Q: fours of sums, dB's and dC's
+  constexpr int sub = kScanSub, Q = N / 2;  // Q: fours of sums, dB's and dC's
   __shared__ float sh[2][sub][16][2 * N + 4];
   const int lane = threadIdx.x & 63, w4 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int blocks = A.groups * blocks_group;
@@ -166,13 +166,13 @@ __global__ __launch_bounds__(256, scan_grad_waves(N)) void scan_grad_kernel(cons
         scan_load_rows<N>(A.dS, k.i * width + ch.c, g);
     }
     const float bias = A.bias ? A.bias[ch.c] : 0.f, skip = A.skip ? A.skip[ch.c] : 0.f;
-    const int len = k.t1 - k.t0, runs = (len + sub - 1) >> shift;
-    const int64_t first = (k.start >> shift) + k.i + ((k.t0 - k.start) >> shift);
+    const int len = k.t1 - k.t0, runs = (len + sub - 1) / sub;
+    const int64_t first = k.start / sub + k.i + (k.t0 - k.start) / sub;
     const int place = fold_place(lane);
     E rx[sub], rd[sub], ry[sub], rz[sub];
     float start[N];  // the states before the run's tokens
     const auto load = [&](int r) {
-      const int t = k.t0 + (r << shift);
+      const int t = k.t0 + r * sub;
       const ScanArgs &P = scan_args();
       const E *x = at<const E>(P.x, t, 0), *dt = at<const E>(P.dt, t, 0), *dy = at<const E>(P.dy, t, 0);
       const E *z = GATE ? at<const E>(P.z, t, 0) : x;
@@ -198,7 +198,7 @@ __global__ __launch_bounds__(256, scan_grad_waves(N)) void scan_grad_kernel(cons
       load_start(runs - 1);
     }
     for (int r = runs - 1; r >= 0; --r) {
-      const int t = k.t0 + (r << shift), n_t = min(sub, k.t1 - t);
+      const int t = k.t0 + r * sub, n_t = min(sub, k.t1 - t);
       float fx[sub], fd[sub], fy[sub], fz[sub], slope[sub], hist[sub][N];
 #pragma unroll
       for (int u = 0; u < sub; ++u) {
@@ -247,7 +247,7 @@ __global__ __launch_bounds__(256, scan_grad_waves(N)) void scan_grad_kernel(cons
         float d = fd[u];
         // the decays again, but for those used next: keeping the run's would cost 32
         // registers more
-        if (u + 2 != sub || N != 16) asm("" : "+v"(d));
+        if (u + 2 != sub || N > 16) asm("" : "+v"(d));
         const float xd = d * fx[u];
         float s = 0.f, dp = fy[u];
         if (GATE) {
