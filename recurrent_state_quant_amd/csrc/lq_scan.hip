@@ -9,18 +9,32 @@
 // chunks take three launches: every chunk's states from zero and the sum of its
 // steps (the whole chunk decays by e^(A sum)), the states before every chunk
 // from these, and the tokens again from there.
+//
+// Bound by vector instructions in the first and the third launch (73 to 82 % of
+// the issue slots taken): with 16 states a token and channel take 16 exponentials,
+// of two slots each, in both, and 32 to 48 products and sums.  One prompt of 4,096
+// tokens x 4,096 channels in bf16: 62 + 8 + 82 us.  16,384 tokens x 4,096 of 24
+// sequences in fp16: 217 + 22 + 324.  8,192 x 2,048 of four, states kept for the
+// gradient: 65 + 14 + 104.  One launch that hands the states from chunk to chunk
+// would halve the exponentials of a chunk only where the chunks ran one after the
+// other, and so few waves do not fill the chip.  Keeping the steps of the first
+// launch for the third would save it 7 us of the 89 it then took of the prompt,
+// and cost reading and writing them.
 #include "lq_scan_device.h"
 
 namespace lq {
 
-constexpr int kScanAhead = 8;  // tokens whose inputs are loaded together
 
 // kScanOut, kScanGated: the chunks' outputs from the states before them (gated
-// by z); kScanLocal: the chunks' states from zero.
+// by z); kScanLocal: the chunks' states from zero.  Where there are outputs, four
+// tokens' inputs are loaded together, which leaves room for a wave a SIMD more than
+// eight do (324 us for 336 of 16,384 tokens x 4,096 channels, 82 for 83 of 4,096 x
+// 4,096); where there are none, eight (206 us for 214).
 enum { kScanLocal, kScanOut, kScanGated };
 template <class E, int N, int MODE>
 __global__ __launch_bounds__(256, scan_forward_waves(N)) void scan_kernel(const ScanArgs A, int tiles, int64_t waves) {
   constexpr bool OUT = MODE != kScanLocal, GATE = MODE == kScanGated;
+  constexpr int ahead = OUT ? 4 : 8;  // tokens whose inputs are loaded together
   const int lane = threadIdx.x & 63;
   const int64_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) + (int64_t)blockIdx.x * 4;
   if (wave >= waves) return;  // whole waves; the waves share nothing
@@ -29,10 +43,10 @@ __global__ __launch_bounds__(256, scan_forward_waves(N)) void scan_kernel(const 
   if (!k.any || (!OUT && k.c + 1 >= k.chunks)) return;  // nothing comes behind the last chunk
   const ScanTile ch = scan_tile(A, tile / tg, tile % tg, lane);
   const int64_t width = A.channels;
-  float a2[N], h[N], sum = 0.f;
+  float a2[N], sum = 0.f;
+  ScanState<N> h;
   scan_decays<N>(A, ch.c, a2);
-#pragma unroll
-  for (int n = 0; n < N; ++n) h[n] = 0.f;
+  scan_zero<N>(h);
   if (OUT) {
     if (k.chunks > 1)
       scan_load_cols<N>(A.carry + scan_first_part(A, k) * N * width, width, ch.c, h);
@@ -41,48 +55,51 @@ __global__ __launch_bounds__(256, scan_forward_waves(N)) void scan_kernel(const 
   }
   const float bias = A.bias ? A.bias[ch.c] : 0.f, skip = OUT && A.skip ? A.skip[ch.c] : 0.f;
   const bool save = OUT && A.check;
-  E rx[kScanAhead], rd[kScanAhead], rz[kScanAhead];
+  E rx[ahead], rd[ahead], rz[ahead];
+  ScanLanes<E, N> rb[ahead];
   const auto load = [&](int t) {
     const ScanArgs &P = scan_args();
     const E *x = at<const E>(P.x, t, 0), *dt = at<const E>(P.dt, t, 0), *z = GATE ? at<const E>(P.z, t, 0) : x;
+    const E *b = at<const E>(P.B, t, ch.g);
 #pragma unroll
-    for (int u = 0; u < kScanAhead; ++u) {
+    for (int u = 0; u < ahead; ++u) {
       rx[u] = lane_load(x, ch.c);
       rd[u] = lane_load(dt, ch.c);
+      rb[u].load(b, lane);
       if (GATE) rz[u] = lane_load(z, ch.c);
       if (t + u + 1 < k.t1) {
         x += P.x.ts;
         dt += P.dt.ts;
+        b += P.B.ts;
         if (GATE) z += P.z.ts;
       }
     }
   };
-  // the output's row: reading the arguments for each token would wait for the rows
-  // of B and C on their way
+  // the output's row: reading the arguments for each token would wait for the row
+  // of C on its way
   E *y = OUT ? at<E>(A.y, k.t0, 0) : nullptr;
-  ScanRow<E, N> B, C;
+  ScanRow<E, N> C;
   if (k.t0 < k.t1) {
     load(k.t0);
-    B.load(A.B, k.t0, ch.g);
     if (OUT) C.load(A.C, k.t0, ch.g);
   }
-  for (int t = k.t0; t < k.t1; t += kScanAhead) {
-    float fx[kScanAhead], fd[kScanAhead], fz[kScanAhead];
+  for (int t = k.t0; t < k.t1; t += ahead) {
+    float fx[ahead], fd[ahead], fz[ahead], fb[ahead][ScanLanes<E, N>::rows];
 #pragma unroll
-    for (int u = 0; u < kScanAhead; ++u) {
+    for (int u = 0; u < ahead; ++u) {
+#pragma unroll
+      for (int r = 0; r < ScanLanes<E, N>::rows; ++r) fb[u][r] = to_f(rb[u].e[r]);
       fx[u] = to_f(rx[u]);
       fd[u] = to_f(rd[u]) + bias;
       fz[u] = GATE ? to_f(rz[u]) : 0.f;
     }
-    if (t + kScanAhead < k.t1) load(t + kScanAhead);
+    if (t + ahead < k.t1) load(t + ahead);
 #pragma unroll
-    for (int u = 0; u < kScanAhead; ++u) {
+    for (int u = 0; u < ahead; ++u) {
       __builtin_amdgcn_sched_barrier(0);
       const int tt = t + u;
-      const ScanRow<E, N> b = B, cc = C;
-      const int next = min(tt + 1, k.t1 - 1);
-      B.load(A.B, next, ch.g);
-      if (OUT) C.load(A.C, next, ch.g);
+      const ScanRow<E, N> cc = C;
+      if (OUT) C.load(A.C, min(tt + 1, k.t1 - 1), ch.g);
       if (OUT && u % kScanSub == 0 && save && tt < k.t1) {
         const int64_t s = k.start / kScanSub + k.i + (tt - k.start) / kScanSub;
         if (ch.on) scan_store_cols<N>(A.check + s * N * width, width, ch.c, h);
@@ -92,13 +109,14 @@ __global__ __launch_bounds__(256, scan_forward_waves(N)) void scan_kernel(const 
       const float d = in ? scan_step(A, fd[u]) : 0.f, x = in ? fx[u] : 0.f, dx = d * x;
       sum += d;
 #pragma unroll
-      for (int n = 0; n < N; ++n) h[n] = fmaf(__builtin_amdgcn_exp2f(d * a2[n]), h[n], scan_times<E>(dx, b[n]));
+      for (int n = 0; n < N; ++n) h[n >> 2][n & 3] *= __builtin_amdgcn_exp2f(d * a2[n]);
+      scan_add_outer<N>(h, fb[u], dx);
       if (OUT) {
         float p0 = skip * x, p1 = 0.f;
 #pragma unroll
         for (int n = 0; n < N; n += 2) {
-          p0 = fmaf(cc[n], h[n], p0);
-          p1 = fmaf(cc[n + 1], h[n + 1], p1);
+          p0 = fmaf(cc[n], h[n >> 2][n & 3], p0);
+          p1 = fmaf(cc[n + 1], h[n >> 2][(n & 3) + 1], p1);
         }
         float p = p0 + p1;
         if (GATE) p *= fz[u] * sigmoid_for<E>(fz[u]);
@@ -155,8 +173,9 @@ __global__ __launch_bounds__(256) void scan_carry_kernel(const ScanArgs A, int s
 }
 
 // One token of each row.  Four states a lane, the lanes of a channel side by
-// side, so that the states move in whole lines; bound by reading and writing
-// them.
+// side, so that the states move in whole lines.  Bound by reading and writing
+// them, past the caches, as a step's states are not read again before the next: 256
+// rows x 4,096 channels x 16 states 30 to 33 us, 4.3 to 4.7 TB/s.
 template <class E, int N>
 __global__ __launch_bounds__(256) void scan_step_kernel(const ScanArgs A, int64_t blocks_row) {
   constexpr int lanes = N / 4;

@@ -32,6 +32,32 @@ __device__ __forceinline__ float scan_step(const ScanArgs &A, float v, float &sl
   return softplus_of(v, e);
 }
 
+// Element c of a row whose address is the same for the wave: the address stays
+// in scalar registers (it is hidden from the compiler, which would otherwise add
+// it to the lane's offset first, in vector registers), the lane's offset is one
+// register for all rows (of at most 2^20 elements).
+template <class T> using lane_bits = std::conditional_t<sizeof(T) == 4, uint32_t, uint16_t>;
+template <class T>
+__device__ __forceinline__ uintptr_t row_address(T *row) {
+  uintptr_t p = reinterpret_cast<uintptr_t>(row);
+  asm("" : "+s"(p));
+  return p;
+}
+template <class T>
+__device__ __forceinline__ T lane_load(const T *row, int c) {
+  typedef const char __attribute__((address_space(1))) *bytes;
+  typedef const lane_bits<T> __attribute__((address_space(1))) *global;
+  const uint32_t off = (uint32_t)c * (uint32_t)sizeof(T);
+  return __builtin_bit_cast(T, *(global)((bytes)row_address(row) + off));
+}
+template <class T>
+__device__ __forceinline__ void lane_store(T *row, int c, T x) {
+  typedef char __attribute__((address_space(1))) *bytes;
+  typedef lane_bits<T> __attribute__((address_space(1))) *global;
+  const uint32_t off = (uint32_t)c * (uint32_t)sizeof(T);
+  *(global)((bytes)row_address(row) + off) = __builtin_bit_cast(lane_bits<T>, x);
+}
+
 // A row of B or C: N values that are the same for the whole wave, through the
 // scalar cache (the address is made of wave-uniform values), so that they cost
 // the vector units nothing but their use as an operand.
@@ -51,6 +77,7 @@ template <class E, int N> struct ScanRow {
       return to_f(__builtin_bit_cast(E, (uint16_t)(w[n >> 1] >> (16 * (n & 1)))));
   }
 };
+
 // x b, as a fused product and sum with zero for fp16: that instruction takes an
 // fp16 operand as it is
 template <class E>
@@ -58,6 +85,35 @@ __device__ __forceinline__ float scan_times(float x, float b) {
   if constexpr (std::is_same_v<E, F16>) return fmaf(x, b, 0.f);
   return x * b;
 }
+
+// The same row as a matrix operand: lane l holds value l mod 16 (N = 8: mod 8) of
+// each sixteen.  s[n] += row[n] x for every lane's own x is then one instruction
+// for four n: sixteen products of a 4 x 1 block and a 1 x 4 block, the columns of
+// block b the lanes 4 b .. 4 b + 3 with their x, and the four rows, broadcast from
+// block q of every group of blocks, the values 4 q .. 4 q + 3.  The sum is in
+// fp32, one rounding a value.  These instructions run beside other waves' vector
+// instructions, of which each token has 16 fewer (of some 95 with 16 states): the
+// chunks' outputs of 8,192 tokens x 2,048 channels 113 -> 104 us, of 16,384 x
+// 4,096 340 -> 324, their states from zero 243 -> 217.  The sum over n of C_n h_n
+// done likewise is slower (116 us of 8,192 x 2,048): four times the instructions,
+// each waiting for the last.  In the gradient's main kernel it spills (452 us for
+// 285).
+template <class E, int N> struct ScanLanes {
+  static constexpr int rows = (N + 15) / 16, period = N < 16 ? N : 16;
+  E e[rows];
+  __device__ __forceinline__ void load(const E *row, int lane) {
+#pragma unroll
+    for (int r = 0; r < rows; ++r) e[r] = lane_load(row + 16 * r, lane & (period - 1));
+  }
+};
+template <int N> using ScanState = floatx4[N / 4];
+template <int N, int Q = 0>
+__device__ __forceinline__ void scan_add_outer(ScanState<N> &s, const float (&row)[(N + 15) / 16], float x) {
+  constexpr int broadcast = N < 16 ? 1 : 2, block = Q & ((1 << broadcast) - 1);
+  s[Q] = __builtin_amdgcn_mfma_f32_4x4x1f32(row[Q / 4], x, s[Q], broadcast, block, 0);
+  if constexpr (Q + 1 < N / 4) scan_add_outer<N, Q + 1>(s, row, x);
+}
+
 // A wave's channels: 64 of one group, one a lane.
 struct ScanTile {
   int g;        // group
@@ -94,31 +150,6 @@ __device__ __forceinline__ ScanChunk scan_chunk(const ScanArgs &A, int chunk, in
   return k;
 }
 
-// Element c of a row whose address is the same for the wave: the address stays
-// in scalar registers (it is hidden from the compiler, which would otherwise add
-// it to the lane's offset first, in vector registers), the lane's offset is one
-// register for all rows (of at most 2^20 elements).
-template <class T> using lane_bits = std::conditional_t<sizeof(T) == 4, uint32_t, uint16_t>;
-template <class T>
-__device__ __forceinline__ uintptr_t row_address(T *row) {
-  uintptr_t p = reinterpret_cast<uintptr_t>(row);
-  asm("" : "+s"(p));
-  return p;
-}
-template <class T>
-__device__ __forceinline__ T lane_load(const T *row, int c) {
-  typedef const char __attribute__((address_space(1))) *bytes;
-  typedef const lane_bits<T> __attribute__((address_space(1))) *global;
-  const uint32_t off = (uint32_t)c * (uint32_t)sizeof(T);
-  return __builtin_bit_cast(T, *(global)((bytes)row_address(row) + off));
-}
-template <class T>
-__device__ __forceinline__ void lane_store(T *row, int c, T x) {
-  typedef char __attribute__((address_space(1))) *bytes;
-  typedef lane_bits<T> __attribute__((address_space(1))) *global;
-  const uint32_t off = (uint32_t)c * (uint32_t)sizeof(T);
-  *(global)((bytes)row_address(row) + off) = __builtin_bit_cast(lane_bits<T>, x);
-}
 // The kernel's arguments (its first) read again where they are used: pointers
 // and strides of a dozen arrays do not stay in scalar registers that way.
 __device__ __forceinline__ const ScanArgs &scan_args() {
@@ -126,45 +157,48 @@ __device__ __forceinline__ const ScanArgs &scan_args() {
   asm("" : "+s"(p));
   return *(const ScanArgs *)(const ScanArgs __attribute__((address_space(4))) *)p;
 }
-// The slot of the chunks from zero (M of them in one of k's) that chunk k begins
-// with, and ends with.
+// The slots of the first and the last of the chunks from zero (one or two) that
+// chunk k is made of.
 __device__ __forceinline__ int64_t scan_first_part(const ScanArgs &A, const ScanChunk &k) {
   return k.start / A.part + k.i + (int64_t)k.c * (A.chunk / A.part);
 }
 __device__ __forceinline__ int64_t scan_last_part(const ScanArgs &A, const ScanChunk &k) {
   return k.start / A.part + k.i + (k.t1 - k.start + A.part - 1) / A.part - 1;
 }
+
 // A channel's states from or to [states][channels] or [channels][states]
 template <int N>
-__device__ __forceinline__ void scan_load_cols(const float *p, int64_t channels, int c, float (&h)[N]) {
+__device__ __forceinline__ void scan_load_cols(const float *p, int64_t channels, int c, ScanState<N> &h) {
 #pragma unroll
-  for (int n = 0; n < N; ++n) h[n] = lane_load(p + n * channels, c);
+  for (int n = 0; n < N; ++n) h[n >> 2][n & 3] = lane_load(p + n * channels, c);
 }
 template <int N>
-__device__ __forceinline__ void scan_store_cols(float *p, int64_t channels, int c, const float (&h)[N]) {
+__device__ __forceinline__ void scan_store_cols(float *p, int64_t channels, int c, const ScanState<N> &h) {
 #pragma unroll
-  for (int n = 0; n < N; ++n) lane_store(p + n * channels, c, h[n]);
+  for (int n = 0; n < N; ++n) lane_store(p + n * channels, c, (float)h[n >> 2][n & 3]);
 }
 template <int N>
-__device__ __forceinline__ void scan_load_rows(const float *p, int64_t row, float (&h)[N]) {
+__device__ __forceinline__ void scan_load_rows(const float *p, int64_t row, ScanState<N> &h) {
 #pragma unroll
-  for (int n = 0; n < N; n += 4) {
-    const float4 v = *reinterpret_cast<const float4 *>(p + row * N + n);
-    h[n] = v.x; h[n + 1] = v.y; h[n + 2] = v.z; h[n + 3] = v.w;
-  }
+  for (int q = 0; q < N / 4; ++q) h[q] = *reinterpret_cast<const floatx4 *>(p + row * N + 4 * q);
 }
 template <int N>
-__device__ __forceinline__ void scan_store_rows(float *p, int64_t row, const float (&h)[N]) {
+__device__ __forceinline__ void scan_store_rows(float *p, int64_t row, const ScanState<N> &h) {
 #pragma unroll
-  for (int n = 0; n < N; n += 4)
-    *reinterpret_cast<float4 *>(p + row * N + n) = make_float4(h[n], h[n + 1], h[n + 2], h[n + 3]);
+  for (int q = 0; q < N / 4; ++q) *reinterpret_cast<floatx4 *>(p + row * N + 4 * q) = h[q];
+}
+template <int N>
+__device__ __forceinline__ void scan_zero(ScanState<N> &h) {
+#pragma unroll
+  for (int q = 0; q < N / 4; ++q) h[q] = floatx4{0.f, 0.f, 0.f, 0.f};
 }
 // decays as exponents of two: e^(d A) = 2^(d A log2 e)
 template <int N>
 __device__ __forceinline__ void scan_decays(const ScanArgs &A, int c, float (&a2)[N]) {
-  scan_load_rows<N>(A.A, c, a2);
+  ScanState<N> a;
+  scan_load_rows<N>(A.A, c, a);
 #pragma unroll
-  for (int n = 0; n < N; ++n) a2[n] *= kLog2e;
+  for (int n = 0; n < N; ++n) a2[n] = a[n >> 2][n & 3] * kLog2e;
 }
 
 }  // namespace lq

@@ -13,13 +13,22 @@
 // states do.  The forward pass left the states before every fourth token: such a run
 // is computed again from them, its states stay in registers, and it is taken
 // backwards.
+//
+// Bound by vector instructions (73 % of the issue slots taken, at two waves a SIMD
+// with 16 states): each token's decays are computed twice, and with the sums over
+// the channels a state takes some 20 instructions.  8,192 tokens x 2,048 channels x
+// 16 states in bf16: chunks from zero 75 us, between them 13, main kernel 285, the
+// sums of its workgroups 7.  Without any sums over channels the main kernel took
+// 256 us, without its loads of kept states, of B and C or of the inputs 246 to 252,
+// without its stores 239, all of 294 then.  1,021 tokens x 1,111 channels x 8
+// states in fp32: 10 + 8 + 29 + 4.
 #include "lq_scan_device.h"
 
 namespace lq {
 
 // The chunks' gradients behind from zero: what comes out of their first token.
 template <class E, int N, bool GATE>
-__global__ __launch_bounds__(256, 4) void scan_grad_local_kernel(const ScanArgs A, int tiles, int64_t waves) {
+__global__ __launch_bounds__(256, N > 16 ? 3 : 4) void scan_grad_local_kernel(const ScanArgs A, int tiles, int64_t waves) {
   const int lane = threadIdx.x & 63;
   const int64_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) + (int64_t)blockIdx.x * 4;
   if (wave >= waves) return;
@@ -28,35 +37,39 @@ __global__ __launch_bounds__(256, 4) void scan_grad_local_kernel(const ScanArgs 
   if (!k.any || k.c == 0) return;  // nothing comes before the first chunk
   const ScanTile ch = scan_tile(A, tile / tg, tile % tg, lane);
   const int64_t width = A.channels;
-  float a2[N], g[N], sum = 0.f;
+  float a2[N], sum = 0.f;
+  ScanState<N> g;
   scan_decays<N>(A, ch.c, a2);
-#pragma unroll
-  for (int n = 0; n < N; ++n) g[n] = 0.f;
+  scan_zero<N>(g);
   const float bias = A.bias ? A.bias[ch.c] : 0.f;
   constexpr int ahead = 8;
   E rd[ahead], ry[ahead], rz[ahead];
+  ScanLanes<E, N> rc[ahead];
   const auto load = [&](int t) {  // tokens t, t - 1 ..
     const ScanArgs &P = scan_args();
     const E *dt = at<const E>(P.dt, t, 0), *dy = at<const E>(P.dy, t, 0), *z = GATE ? at<const E>(P.z, t, 0) : dy;
+    const E *cc = at<const E>(P.C, t, ch.g);
 #pragma unroll
     for (int u = 0; u < ahead; ++u) {
       rd[u] = lane_load(dt, ch.c);
       ry[u] = lane_load(dy, ch.c);
+      rc[u].load(cc, lane);
       if (GATE) rz[u] = lane_load(z, ch.c);
       if (t - u > k.t0) {
         dt -= P.dt.ts;
         dy -= P.dy.ts;
+        cc -= P.C.ts;
         if (GATE) z -= P.z.ts;
       }
     }
   };
-  ScanRow<E, N> C;
   load(k.t1 - 1);
-  C.load(A.C, k.t1 - 1, ch.g);
   for (int t = k.t1 - 1; t >= k.t0; t -= ahead) {
-    float fd[ahead], fy[ahead], fz[ahead];
+    float fd[ahead], fy[ahead], fz[ahead], fc[ahead][ScanLanes<E, N>::rows];
 #pragma unroll
     for (int u = 0; u < ahead; ++u) {
+#pragma unroll
+      for (int r = 0; r < ScanLanes<E, N>::rows; ++r) fc[u][r] = to_f(rc[u].e[r]);
       fd[u] = to_f(rd[u]) + bias;
       fy[u] = to_f(ry[u]);
       fz[u] = GATE ? to_f(rz[u]) : 0.f;
@@ -65,14 +78,13 @@ __global__ __launch_bounds__(256, 4) void scan_grad_local_kernel(const ScanArgs 
 #pragma unroll
     for (int u = 0; u < ahead; ++u) {
       __builtin_amdgcn_sched_barrier(0);
-      const ScanRow<E, N> cc = C;
-      C.load(A.C, max(t - u - 1, k.t0), ch.g);
       const bool in = t - u >= k.t0;  // before the chunk's beginning: a step of zero
       const float d = in ? scan_step(A, fd[u]) : 0.f;
       const float dp = !in ? 0.f : GATE ? fy[u] * (fz[u] * sigmoid_for<E>(fz[u])) : fy[u];
       sum += d;
+      scan_add_outer<N>(g, fc[u], dp);
 #pragma unroll
-      for (int n = 0; n < N; ++n) g[n] = __builtin_amdgcn_exp2f(d * a2[n]) * fmaf(cc[n], dp, g[n]);
+      for (int n = 0; n < N; ++n) g[n >> 2][n & 3] *= __builtin_amdgcn_exp2f(d * a2[n]);
     }
   }
   if (!ch.on) return;
@@ -120,9 +132,9 @@ __global__ __launch_bounds__(256) void scan_grad_carry_kernel(const ScanArgs A, 
 
 // Sums of many registers over the 16 lanes of a row at once: two registers become
 // one, in which half of the lanes go on with the one and half with the other.
-// Three instructions a step, 90 for 32 sums (8,192 tokens x 2,048 channels 296 us;
-// with four-lane sums by products of ones on the matrix pipe 350, whose
-// instructions wait for it and for one another).
+// Three instructions a step, 90 for 32 sums.  8,192 tokens x 2,048 channels take
+// 285 us; with four-lane sums by products with ones on the matrix pipe, whose
+// instructions wait for it and for one another, 350 for 296 then.
 template <int CTRL>
 __device__ __forceinline__ float fold2(float a, float b, bool high) {
   return (high ? b : a) + dpp<CTRL>(high ? a : b);
@@ -154,9 +166,10 @@ __global__ __launch_bounds__(256, scan_grad_waves(N)) void scan_grad_kernel(cons
   const ScanChunk k = scan_chunk(A, A.chunk, slot, lane);
   const ScanTile ch = scan_tile(A, group, tile, lane);
   const int64_t width = A.channels;
-  float a2[N], g[N], dA[N], dskip = 0.f, dbias = 0.f;
-#pragma unroll
-  for (int n = 0; n < N; ++n) g[n] = dA[n] = 0.f;
+  float a2[N], dskip = 0.f, dbias = 0.f;
+  ScanState<N> g, dA;
+  scan_zero<N>(g);
+  scan_zero<N>(dA);
   if (k.any) {
     scan_decays<N>(A, ch.c, a2);
     if (ch.on) {
@@ -170,7 +183,7 @@ __global__ __launch_bounds__(256, scan_grad_waves(N)) void scan_grad_kernel(cons
     const int64_t first = k.start / sub + k.i + (k.t0 - k.start) / sub;
     const int place = fold_place(lane);
     E rx[sub], rd[sub], ry[sub], rz[sub];
-    float start[N];  // the states before the run's tokens
+    ScanState<N> start;  // the states before the run's tokens
     const auto load = [&](int r) {
       const int t = k.t0 + r * sub;
       const ScanArgs &P = scan_args();
@@ -208,7 +221,7 @@ __global__ __launch_bounds__(256, scan_grad_waves(N)) void scan_grad_kernel(cons
         fz[u] = GATE ? to_f(rz[u]) : 0.f;
       }
 #pragma unroll
-      for (int n = 0; n < N; ++n) hist[0][n] = start[n];
+      for (int n = 0; n < N; ++n) hist[0][n] = start[n >> 2][n & 3];
       if (r > 0) load(r - 1);
       // the output rows of the run's last token, and the way to the one before:
       // reading them for each token would wait for the rows of B and C on their way
@@ -245,8 +258,8 @@ __global__ __launch_bounds__(256, scan_grad_waves(N)) void scan_grad_kernel(cons
           C.load(A.C, min(t + u - 1, k.t1 - 1), ch.g);
         }
         float d = fd[u];
-        // the decays again, but for those used next: keeping the run's would cost 32
-        // registers more
+        // the decays again, but for those used next: keeping the run's spills (643 us
+        // for 294 of 8,192 tokens x 2,048 channels)
         if (u + 2 != sub || N > 16) asm("" : "+v"(d));
         const float xd = d * fx[u];
         float s = 0.f, dp = fy[u];
@@ -265,14 +278,14 @@ __global__ __launch_bounds__(256, scan_grad_waves(N)) void scan_grad_kernel(cons
             const float a = __builtin_amdgcn_exp2f(d * a2[n]), ah = a * hist[u][n];
             const float h = u + 1 < sub ? hist[u + 1 < sub ? u + 1 : u][n] : fmaf(xd, b[n], ah);
             p = fmaf(cc[n], h, p);
-            const float gn = fmaf(cc[n], dp, g[n]);
+            const float gn = fmaf(cc[n], dp, g[q][m]);
             gb = fmaf(gn, b[n], gb);
             const float e = gn * ah;
             ea = fmaf(e, a2[n], ea);
-            dA[n] = fmaf(e, d, dA[n]);
+            dA[q][m] = fmaf(e, d, dA[q][m]);
             vb[m] = gn * xd;
             vc[m] = dp * h;
-            g[n] = gn * a;
+            g[q][m] = gn * a;
           }
           fold[q] = fold4(vb, lane);
           fold[N / 4 + q] = fold4(vc, lane);
