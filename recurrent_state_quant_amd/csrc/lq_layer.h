@@ -61,8 +61,8 @@ struct ScanArgs {
   const float *A, *skip, *bias;
   const float *S0;  // [seqs][channels][states] or nullptr (zeros)
   float *S;         // or nullptr
-  float *check;     // [scan_checks][states][channels] or nullptr: the states before every kScanSub-th token of a sequence
-  float *carry;     // [part slots][states][channels]  of sequences with several: the state before (backward: gradient behind)
+  float *check;     // [scan_checks][states / 4][channels][4] or nullptr: the states before every kScanSub-th token of a sequence
+  float *carry;     // [part slots][states / 4][channels][4]  of sequences with several: the state before (backward: gradient behind)
   float *sum;       // [part slots][channels]          the sum of a part's steps
   // step
   const int32_t *which;  // [rows] or nullptr
@@ -72,7 +72,7 @@ struct ScanArgs {
   float *dA, *dskip, *dbias;
   const float *dS;
   float *dS0;
-  float *part_bc;  // [groups * blocks][tokens][2 * states]
+  float *part_bc;  // [tiles][tokens][2 * states]
   float *part_a;   // [slots][states + 2][channels]
 };
 
@@ -110,8 +110,6 @@ inline int scan_chunk_tokens(int64_t tokens, int64_t seqs, int64_t workgroups, i
   }
   return best;
 }
-// Blocks of four waves that share a group (backward)
-inline int64_t scan_group_blocks(int per) { return (per + 255) / 256; }
 // Waves of the forward kernel that a SIMD holds
 constexpr int scan_forward_waves(int states) { return states > 16 ? 3 : states > 8 ? 5 : 6; }
 inline int scan_forward_chunk(int64_t tokens, int64_t seqs, int channels, int groups, int states) {
@@ -121,7 +119,7 @@ inline int scan_forward_chunk(int64_t tokens, int64_t seqs, int channels, int gr
 // room for more waves.
 constexpr int scan_grad_waves(int states) { return states > 16 ? 1 : states > 8 ? 2 : 3; }
 inline int scan_grad_chunk(int64_t tokens, int64_t seqs, int channels, int groups, int states) {
-  return scan_chunk_tokens(tokens, seqs, groups * scan_group_blocks(channels / groups), kScanPart,
+  return scan_chunk_tokens(tokens, seqs, (scan_tiles(channels, groups) + 3) / 4, kScanPart,
                            scan_grad_waves(states), 0.7);
 }
 

@@ -74,14 +74,12 @@ int check_scan(const lq_scan *sc, bool step) {
     const int64_t blocks = (int64_t(sc->channels) * (sc->states / 4) + 255) / 256;
     return sc->tokens > kMaxGrid / blocks ? LQ_ERR_SHAPE : LQ_OK;
   }
-  // the grids: chunks (at least one a sequence, four waves a workgroup; with the
-  // gradient a workgroup for each 256 channels of a group), the states of all
-  // sequences, and the gradient's sums of B and C
+  // the grids: chunks (at least one a sequence, four waves a workgroup), the
+  // states of all sequences, and the gradient's sums of B and C
   const int64_t tiles = lq::scan_tiles(sc->channels, sc->groups);
   const int64_t slots = lq::scan_slots(sc->tokens, sc->seqs, lq::kScanPart);
-  if (slots > kMaxGrid / (sc->groups * lq::scan_group_blocks(sc->channels / sc->groups))) return LQ_ERR_SHAPE;
   if (slots > kMaxGrid / ((tiles + 3) / 4)) return LQ_ERR_SHAPE;
-  if (int64_t(sc->channels) * sc->states > (kMaxGrid * 256) / sc->seqs) return LQ_ERR_SHAPE;
+  if (sc->seqs > kMaxGrid / ((int64_t(sc->channels) * sc->states + 255) / 256)) return LQ_ERR_SHAPE;
   if (sc->tokens > (kMaxGrid * 256) / (int64_t(sc->groups) * 2 * sc->states)) return LQ_ERR_SHAPE;
   return LQ_OK;
 }
@@ -102,7 +100,7 @@ int64_t scan_space(const lq_scan *sc, bool save, char *base, lq::ScanArgs *a) {
   take(&a->carry, slots * state);
   take(&a->sum, slots * channels * 4);
   if (save) {
-    take(&a->part_bc, sc->groups * lq::scan_group_blocks(sc->channels / sc->groups) * sc->tokens * 2 * sc->states * 4);
+    take(&a->part_bc, lq::scan_tiles(sc->channels, sc->groups) * sc->tokens * 2 * sc->states * 4);
     take(&a->part_a, slots * (sc->states + 2) * channels * 4);
   }
   return used;

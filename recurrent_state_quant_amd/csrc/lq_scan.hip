@@ -30,10 +30,10 @@ namespace lq {
 // tokens' inputs are loaded together, which leaves room for a wave a SIMD more than
 // eight do (324 us for 336 of 16,384 tokens x 4,096 channels, 82 for 83 of 4,096 x
 // 4,096); where there are none, eight (206 us for 214).
-enum { kScanLocal, kScanOut, kScanGated };
+enum { kScanLocal = 0, kScanOut = 1, kScanGated = 2, kScanSave = 4 };
 template <class E, int N, int MODE>
 __global__ __launch_bounds__(256, scan_forward_waves(N)) void scan_kernel(const ScanArgs A, int tiles, int64_t waves) {
-  constexpr bool OUT = MODE != kScanLocal, GATE = MODE == kScanGated;
+  constexpr bool OUT = MODE & kScanOut, GATE = MODE & kScanGated, SAVE = MODE & kScanSave;
   constexpr int ahead = OUT ? 4 : 8;  // tokens whose inputs are loaded together
   const int lane = threadIdx.x & 63;
   const int64_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) + (int64_t)blockIdx.x * 4;
@@ -49,12 +49,14 @@ __global__ __launch_bounds__(256, scan_forward_waves(N)) void scan_kernel(const 
   scan_zero<N>(h);
   if (OUT) {
     if (k.chunks > 1)
-      scan_load_cols<N>(A.carry + scan_first_part(A, k) * N * width, width, ch.c, h);
+      scan_load_fours<N>(A.carry + scan_first_part(A, k) * N * width, width, ch.c, h);
     else if (A.S0)
       scan_load_rows<N>(A.S0, k.i * width + ch.c, h);
   }
   const float bias = A.bias ? A.bias[ch.c] : 0.f, skip = OUT && A.skip ? A.skip[ch.c] : 0.f;
-  const bool save = OUT && A.check;
+  float *check = SAVE ? A.check + (k.start / kScanSub + k.i + (k.t0 - k.start) / kScanSub) * N * width : nullptr;
+  const int row_bytes = (int)(width * sizeof(E));
+  const uint32_t off_y = lane_offset(ch.on, ch.c, sizeof(E)), off_s = lane_offset(ch.on, ch.c, 16);
   E rx[ahead], rd[ahead], rz[ahead];
   ScanLanes<E, N> rb[ahead];
   const auto load = [&](int t) {
@@ -78,10 +80,11 @@ __global__ __launch_bounds__(256, scan_forward_waves(N)) void scan_kernel(const 
   // the output's row: reading the arguments for each token would wait for the row
   // of C on its way
   E *y = OUT ? at<E>(A.y, k.t0, 0) : nullptr;
+  const E *row = OUT ? at<const E>(A.C, k.t0, ch.g) : nullptr;
   ScanRow<E, N> C;
   if (k.t0 < k.t1) {
     load(k.t0);
-    if (OUT) C.load(A.C, k.t0, ch.g);
+    if (OUT) C.load(row);
   }
   for (int t = k.t0; t < k.t1; t += ahead) {
     float fx[ahead], fd[ahead], fz[ahead], fb[ahead][ScanLanes<E, N>::rows];
@@ -99,10 +102,13 @@ __global__ __launch_bounds__(256, scan_forward_waves(N)) void scan_kernel(const 
       __builtin_amdgcn_sched_barrier(0);
       const int tt = t + u;
       const ScanRow<E, N> cc = C;
-      if (OUT) C.load(A.C, min(tt + 1, k.t1 - 1), ch.g);
-      if (OUT && u % kScanSub == 0 && save && tt < k.t1) {
-        const int64_t s = k.start / kScanSub + k.i + (tt - k.start) / kScanSub;
-        if (ch.on) scan_store_cols<N>(A.check + s * N * width, width, ch.c, h);
+      if (OUT) {
+        row += tt + 1 < k.t1 ? A.C.ts : 0;
+        C.load(row);
+      }
+      if (SAVE && u % kScanSub == 0) {
+        scan_store_fours<N>(check, (int)width, tt < k.t1, off_s, h);
+        check += N * width;
       }
       // past the chunk's end: a step of zero
       const bool in = tt < k.t1;
@@ -120,14 +126,14 @@ __global__ __launch_bounds__(256, scan_forward_waves(N)) void scan_kernel(const 
         }
         float p = p0 + p1;
         if (GATE) p *= fz[u] * sigmoid_for<E>(fz[u]);
-        if (ch.on && in) lane_store(y, ch.c, from_f<E>(p));
+        lane_store(y, in ? row_bytes : 0, off_y, from_f<E>(p));
         y += A.y.ts;
       }
     }
   }
   if (!ch.on) return;
   if (!OUT) {
-    scan_store_cols<N>(A.carry + (int64_t)slot * N * width, width, ch.c, h);
+    scan_store_fours<N>(A.carry + (int64_t)slot * N * width, (int)width, true, off_s, h);
     A.sum[slot * width + ch.c] = sum;
   } else if (A.S && k.c + 1 >= k.chunks) {
     scan_store_rows<N>(A.S, k.i * width + ch.c, h);
@@ -135,26 +141,17 @@ __global__ __launch_bounds__(256, scan_forward_waves(N)) void scan_kernel(const 
 }
 
 // The states before every chunk of the sequences with several, over the chunks'
-// states from zero: thread (sequence, state, channel).  S0 is copied before the
-// first chunk, as S may lie over it.
-constexpr int kCarryAhead = 16;
-__global__ __launch_bounds__(256) void scan_carry_kernel(const ScanArgs A, int states, int64_t threads) {
-  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (id >= threads) return;
-  const int64_t width = A.channels, c = id % width, n = id / width % states, i = id / width / states;
-  const auto offset = [&](int64_t s) {
-    const int o = A.cu[s];
-    return o < 0 ? 0 : (o > A.tokens ? (int)A.tokens : o);
-  };
-  const int start = offset(i), end = max(start, offset(i + 1));
-  const int chunks = (end - start + A.part - 1) / A.part;
-  if (chunks < 2) return;
-  const int64_t slot = start / A.part + i;
-  const float a2 = A.A[c * states + n] * kLog2e;
-  float h = A.S0 ? A.S0[(i * width + c) * states + n] : 0.f;
-  float *carry = A.carry + (slot * states + n) * width + c;
-  const float *sum = A.sum + slot * width + c;
-  const int64_t step = states * width;
+// states from zero: blocks of a sequence, thread (four states, channel, one of
+// them).  S0 is copied before the first chunk, as S may lie over it.
+__global__ __launch_bounds__(256) void scan_carry_kernel(const ScanArgs A, int states, int blocks) {
+  const ScanCarry t = scan_carry(A, states, blocks);
+  if (!t.any) return;
+  const int chunks = t.chunks;
+  const int64_t width = A.channels, step = states * width;
+  const float a2 = A.A[t.state] * kLog2e;
+  float h = A.S0 ? A.S0[t.i * step + t.state] : 0.f;
+  float *carry = A.carry + t.at;
+  const float *sum = A.sum + t.at_sum;
   for (int k = 0; k < chunks; k += kCarryAhead) {
     float v[kCarryAhead], s[kCarryAhead];
 #pragma unroll
@@ -230,12 +227,16 @@ static hipError_t scan_run(const ScanArgs &a, bool step, hipStream_t stream) {
     const int64_t parts = tiles * scan_slots(a.tokens, a.seqs, a.part);
     hipLaunchKernelGGL((scan_kernel<E, N, kScanLocal>), dim3((unsigned)((parts + 3) / 4)), dim3(256), 0, stream, a,
                        (int)tiles, parts);
-    const int64_t threads = (int64_t)a.seqs * a.channels * N;
-    hipLaunchKernelGGL(scan_carry_kernel, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, stream, a, N, threads);
+    const int blocks = (a.channels * N + 255) / 256;
+    hipLaunchKernelGGL(scan_carry_kernel, dim3((unsigned)(a.seqs * (int64_t)blocks)), dim3(256), 0, stream, a, N, blocks);
   }
   const dim3 grid((unsigned)((waves + 3) / 4));
-  if (a.z.ptr)
-    hipLaunchKernelGGL((scan_kernel<E, N, kScanGated>), grid, dim3(256), 0, stream, a, (int)tiles, waves);
+  if (a.z.ptr && a.check)
+    hipLaunchKernelGGL((scan_kernel<E, N, kScanOut | kScanGated | kScanSave>), grid, dim3(256), 0, stream, a, (int)tiles, waves);
+  else if (a.z.ptr)
+    hipLaunchKernelGGL((scan_kernel<E, N, kScanOut | kScanGated>), grid, dim3(256), 0, stream, a, (int)tiles, waves);
+  else if (a.check)
+    hipLaunchKernelGGL((scan_kernel<E, N, kScanOut | kScanSave>), grid, dim3(256), 0, stream, a, (int)tiles, waves);
   else
     hipLaunchKernelGGL((scan_kernel<E, N, kScanOut>), grid, dim3(256), 0, stream, a, (int)tiles, waves);
   return hipGetLastError();

@@ -50,12 +50,19 @@ __device__ __forceinline__ T lane_load(const T *row, int c) {
   const uint32_t off = (uint32_t)c * (uint32_t)sizeof(T);
   return __builtin_bit_cast(T, *(global)((bytes)row_address(row) + off));
 }
+// Stores of lanes that may have nothing to store, without a branch: one around
+// them would leave the compiler with an unknown number of stores in flight, and so
+// waiting for all of them wherever it needs a load that came before.  `bytes` is
+// the row's length, or 0 for a row that is not stored; lanes of no channel have an
+// offset behind it.
+__device__ __forceinline__ uint32_t lane_offset(bool on, int c, int size) { return on ? (uint32_t)c * size : ~0u; }
 template <class T>
-__device__ __forceinline__ void lane_store(T *row, int c, T x) {
-  typedef char __attribute__((address_space(1))) *bytes;
-  typedef lane_bits<T> __attribute__((address_space(1))) *global;
-  const uint32_t off = (uint32_t)c * (uint32_t)sizeof(T);
-  *(global)((bytes)row_address(row) + off) = __builtin_bit_cast(lane_bits<T>, x);
+__device__ __forceinline__ void lane_store(T *row, int bytes, uint32_t off, T x) {
+  const auto r = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void *>(row_address(row)), (short)0, bytes, 0x00020000);
+  if constexpr (sizeof(T) == 2)
+    __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(lane_bits<T>, x), r, (int)off, 0, 0);
+  else
+    __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(lane_bits<T>, x), r, (int)off, 0, 0);
 }
 
 // A row of B or C: N values that are the same for the whole wave, through the
@@ -64,9 +71,9 @@ __device__ __forceinline__ void lane_store(T *row, int c, T x) {
 template <class E, int N> struct ScanRow {
   static constexpr int words = N * (int)sizeof(E) / 4;
   uint32_t w[words];
-  __device__ __forceinline__ void load(const Rows &r, int t, int g) {
+  __device__ __forceinline__ void load(const E *row) {
     typedef const uint32_t __attribute__((address_space(4))) *scalars;
-    const scalars p = (scalars)(uintptr_t)at<const E>(r, t, g);
+    const scalars p = (scalars)(uintptr_t)row;
 #pragma unroll
     for (int i = 0; i < words; ++i) w[i] = p[i];
   }
@@ -166,16 +173,29 @@ __device__ __forceinline__ int64_t scan_last_part(const ScanArgs &A, const ScanC
   return k.start / A.part + k.i + (k.t1 - k.start + A.part - 1) / A.part - 1;
 }
 
-// A channel's states from or to [states][channels] or [channels][states]
+// A channel's states from or to [states / 4][channels][4], which a wave reads and
+// writes in whole lines with four instructions for 16 states, or [channels][states]
 template <int N>
-__device__ __forceinline__ void scan_load_cols(const float *p, int64_t channels, int c, ScanState<N> &h) {
+__device__ __forceinline__ void scan_load_fours(const float *p, int64_t channels, int c, ScanState<N> &h) {
+  typedef const char __attribute__((address_space(1))) *bytes;
+  typedef const floatx4 __attribute__((address_space(1))) *global;
+  const uint32_t off = (uint32_t)c * 16;
 #pragma unroll
-  for (int n = 0; n < N; ++n) h[n >> 2][n & 3] = lane_load(p + n * channels, c);
+  for (int q = 0; q < N / 4; ++q) {
+    h[q] = *(global)((bytes)row_address(p) + off);
+    p += 4 * channels;
+  }
 }
 template <int N>
-__device__ __forceinline__ void scan_store_cols(float *p, int64_t channels, int c, const ScanState<N> &h) {
+__device__ __forceinline__ void scan_store_fours(float *p, int channels, bool any, uint32_t off, const ScanState<N> &h) {
+  typedef unsigned int u4 __attribute__((ext_vector_type(4)));
+  const int bytes = any ? channels * 16 : 0;
 #pragma unroll
-  for (int n = 0; n < N; ++n) lane_store(p + n * channels, c, (float)h[n >> 2][n & 3]);
+  for (int q = 0; q < N / 4; ++q) {
+    const auto r = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void *>(row_address(p)), (short)0, bytes, 0x00020000);
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4, h[q]), r, (int)off, 0, 0);
+    p += 4 * (int64_t)channels;
+  }
 }
 template <int N>
 __device__ __forceinline__ void scan_load_rows(const float *p, int64_t row, ScanState<N> &h) {
@@ -192,6 +212,30 @@ __device__ __forceinline__ void scan_zero(ScanState<N> &h) {
 #pragma unroll
   for (int q = 0; q < N / 4; ++q) h[q] = floatx4{0.f, 0.f, 0.f, 0.f};
 }
+// What a thread of the launches between the chunks takes: a state of a channel of
+// a sequence of several chunks
+constexpr int kCarryAhead = 16;  // chunks whose states are loaded together
+struct ScanCarry {
+  bool any;
+  int i, chunks;
+  int state;           // channel * states + n
+  int64_t at, at_sum;  // of the first chunk's states in ScanArgs::carry, of its steps in sum
+};
+__device__ __forceinline__ ScanCarry scan_carry(const ScanArgs &A, int states, int blocks) {
+  ScanCarry r{};
+  r.i = blockIdx.x / blocks;
+  const int id = blockIdx.x % blocks * 256 + threadIdx.x;
+  const int start = seq_offset(A.cu, A.tokens, r.i), end = max(start, seq_offset(A.cu, A.tokens, r.i + 1));
+  r.chunks = (end - start + A.part - 1) / A.part;
+  r.any = id < A.channels * states && r.chunks > 1;
+  const int four = id / (4 * A.channels), c = id % (4 * A.channels) >> 2;
+  const int64_t slot = start / A.part + r.i;
+  r.state = c * states + 4 * four + (id & 3);
+  r.at = slot * A.channels * states + id;
+  r.at_sum = slot * A.channels + c;
+  return r;
+}
+
 // decays as exponents of two: e^(d A) = 2^(d A log2 e)
 template <int N>
 __device__ __forceinline__ void scan_decays(const ScanArgs &A, int c, float (&a2)[N]) {

@@ -88,31 +88,22 @@ __global__ __launch_bounds__(256, N > 16 ? 3 : 4) void scan_grad_local_kernel(co
     }
   }
   if (!ch.on) return;
-  scan_store_cols<N>(A.carry + (int64_t)slot * N * width, width, ch.c, g);
+  scan_store_fours<N>(A.carry + (int64_t)slot * N * width, (int)width, true, lane_offset(true, ch.c, 16), g);
   A.sum[slot * width + ch.c] = sum;
 }
 
 // The gradients behind every chunk of the sequences with several, over the
-// chunks' own: thread (sequence, state, channel), the last chunk first.  dS is
-// copied behind the last chunk, as dS0 may lie over it.
-constexpr int kCarryAhead = 16;
-__global__ __launch_bounds__(256) void scan_grad_carry_kernel(const ScanArgs A, int states, int64_t threads) {
-  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (id >= threads) return;
-  const int64_t width = A.channels, c = id % width, n = id / width % states, i = id / width / states;
-  const auto offset = [&](int64_t s) {
-    const int o = A.cu[s];
-    return o < 0 ? 0 : (o > A.tokens ? (int)A.tokens : o);
-  };
-  const int start = offset(i), end = max(start, offset(i + 1));
-  const int chunks = (end - start + A.part - 1) / A.part;
-  if (chunks < 2) return;
-  const int64_t slot = start / A.part + i;
-  const float a2 = A.A[c * states + n] * kLog2e;
-  float g = A.dS ? A.dS[(i * width + c) * states + n] : 0.f;
-  float *carry = A.carry + (slot * states + n) * width + c;
-  const float *sum = A.sum + slot * width + c;
-  const int64_t step = states * width;
+// chunks' own, as the states forward, the last chunk first.  dS is copied behind
+// the last chunk, as dS0 may lie over it.
+__global__ __launch_bounds__(256) void scan_grad_carry_kernel(const ScanArgs A, int states, int blocks) {
+  const ScanCarry t = scan_carry(A, states, blocks);
+  if (!t.any) return;
+  const int chunks = t.chunks;
+  const int64_t width = A.channels, step = states * width;
+  const float a2 = A.A[t.state] * kLog2e;
+  float g = A.dS ? A.dS[t.i * step + t.state] : 0.f;
+  float *carry = A.carry + t.at;
+  const float *sum = A.sum + t.at_sum;
   for (int k = chunks - 1; k >= 0; k -= kCarryAhead) {
     float v[kCarryAhead], s[kCarryAhead];
 #pragma unroll
@@ -135,36 +126,38 @@ __global__ __launch_bounds__(256) void scan_grad_carry_kernel(const ScanArgs A, 
 // Three instructions a step, 90 for 32 sums.  8,192 tokens x 2,048 channels take
 // 285 us; with four-lane sums by products with ones on the matrix pipe, whose
 // instructions wait for it and for one another, 350 for 296 then.
-template <int CTRL>
-__device__ __forceinline__ float fold2(float a, float b, bool high) {
-  return (high ? b : a) + dpp<CTRL>(high ? a : b);
+// Lanes with bits 3 and 2 of (0, 0), (1, 0), (0, 1), (1, 1) come to hold the sums of
+// v[0], v[1], v[2], v[3] over the four lanes with the same bits 1 and 0.  (All lanes
+// are active; the s_nops keep the two cycles between writing a register and
+// reading it across lanes.)
+__device__ __forceinline__ float fold4(const float (&v)[4]) {
+  float x, y, r;
+  asm("s_nop 1\n"
+      "v_add_f32_dpp %0, %3, %3 row_ror:8 row_mask:0xf bank_mask:0xf\n"
+      "v_add_f32_dpp %1, %5, %5 row_ror:8 row_mask:0xf bank_mask:0xf\n"
+      "v_add_f32_dpp %0, %4, %4 row_ror:8 row_mask:0xf bank_mask:0xc\n"
+      "v_add_f32_dpp %1, %6, %6 row_ror:8 row_mask:0xf bank_mask:0xc\n"
+      "s_nop 1\n"
+      "v_add_f32_dpp %2, %0, %0 row_half_mirror row_mask:0xf bank_mask:0xf\n"
+      "v_add_f32_dpp %2, %1, %1 row_half_mirror row_mask:0xf bank_mask:0xa"
+      : "=&v"(x), "=&v"(y), "=&v"(r)
+      : "v"(v[0]), "v"(v[1]), "v"(v[2]), "v"(v[3]));
+  return r;
 }
-// Afterwards lanes with bits 3 and 2 of (0, 0), (1, 0), (0, 1), (1, 1) hold a, b, c, d.
-__device__ __forceinline__ float fold4(const float (&v)[4], int lane) {
-  const float x = fold2<0x128>(v[0], v[1], lane & 8), y = fold2<0x128>(v[2], v[3], lane & 8);  // row_ror:8
-  return fold2<0x141>(x, y, lane & 4);  // row_half_mirror
-}
-// Four of those: the sum of a row in every lane, number fold_place.
-__device__ __forceinline__ float fold16(const float (&v)[4], int lane) {
-  const float x = fold2<0x4E>(v[0], v[1], lane & 2), y = fold2<0x4E>(v[2], v[3], lane & 2);  // quad_perm [2,3,0,1]
-  return fold2<0xB1>(x, y, lane & 1);  // quad_perm [1,0,3,2]
-}
-__device__ __forceinline__ int fold_place(int lane) {
-  return 8 * (lane & 1) + 4 * (lane >> 1 & 1) + 2 * (lane >> 2 & 1) + (lane >> 3 & 1);
-}
+__device__ __forceinline__ int fold_place(int lane) { return 2 * (lane >> 2 & 1) + (lane >> 3 & 1); }
 
 // A block's four waves share a group and a chunk: their sums over the channels
 // meet in LDS after every run of tokens.
 template <class E, int N, bool GATE>
-__global__ __launch_bounds__(256, scan_grad_waves(N)) void scan_grad_kernel(const ScanArgs A, int blocks_group) {
-  constexpr int sub = kScanSub, Q = N / 2;  // Q: fours of sums, dB's and dC's
-  __shared__ float sh[2][sub][16][2 * N + 4];
+__global__ __launch_bounds__(256, scan_grad_waves(N)) void scan_grad_kernel(const ScanArgs A, int tiles, int64_t waves) {
+  constexpr int sub = kScanSub, row = 2 * N + 4, Q = N / 2;  // Q: fours of sums, dB's and dC's
+  __shared__ float sh[4][sub][16][row];
   const int lane = threadIdx.x & 63, w4 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int blocks = A.groups * blocks_group;
-  const int slot = blockIdx.x / blocks, gb = blockIdx.x % blocks;
-  const int group = gb / blocks_group, tile = gb % blocks_group * 4 + w4;
+  const int64_t wave = w4 + (int64_t)blockIdx.x * 4;
+  if (wave >= waves) return;
+  const int slot = (int)(wave / tiles), tile = (int)(wave % tiles), tg = (A.per + 63) >> 6, group = tile / tg;
   const ScanChunk k = scan_chunk(A, A.chunk, slot, lane);
-  const ScanTile ch = scan_tile(A, group, tile, lane);
+  const ScanTile ch = scan_tile(A, group, tile % tg, lane);
   const int64_t width = A.channels;
   float a2[N], dskip = 0.f, dbias = 0.f;
   ScanState<N> g, dA;
@@ -174,14 +167,15 @@ __global__ __launch_bounds__(256, scan_grad_waves(N)) void scan_grad_kernel(cons
     scan_decays<N>(A, ch.c, a2);
     if (ch.on) {
       if (k.chunks > 1)
-        scan_load_cols<N>(A.carry + scan_last_part(A, k) * N * width, width, ch.c, g);
+        scan_load_fours<N>(A.carry + scan_last_part(A, k) * N * width, width, ch.c, g);
       else if (A.dS)
         scan_load_rows<N>(A.dS, k.i * width + ch.c, g);
     }
     const float bias = A.bias ? A.bias[ch.c] : 0.f, skip = A.skip ? A.skip[ch.c] : 0.f;
     const int len = k.t1 - k.t0, runs = (len + sub - 1) / sub;
     const int64_t first = k.start / sub + k.i + (k.t0 - k.start) / sub;
-    const int place = fold_place(lane);
+    const int place = fold_place(lane), row_bytes = (int)(width * sizeof(E));
+    const uint32_t off = lane_offset(ch.on, ch.c, sizeof(E));
     E rx[sub], rd[sub], ry[sub], rz[sub];
     ScanState<N> start;  // the states before the run's tokens
     const auto load = [&](int r) {
@@ -204,7 +198,7 @@ __global__ __launch_bounds__(256, scan_grad_waves(N)) void scan_grad_kernel(cons
       }
     };
     const auto load_start = [&](int r) {
-      scan_load_cols<N>(scan_args().check + (first + r) * N * width, width, ch.c, start);
+      scan_load_fours<N>(scan_args().check + (first + r) * N * width, width, ch.c, start);
     };
     if (runs) {
       load(runs - 1);
@@ -222,7 +216,6 @@ __global__ __launch_bounds__(256, scan_grad_waves(N)) void scan_grad_kernel(cons
       }
 #pragma unroll
       for (int n = 0; n < N; ++n) hist[0][n] = start[n >> 2][n & 3];
-      if (r > 0) load(r - 1);
       // the output rows of the run's last token, and the way to the one before:
       // reading them for each token would wait for the rows of B and C on their way
       const ScanArgs &P = scan_args();
@@ -230,8 +223,12 @@ __global__ __launch_bounds__(256, scan_grad_waves(N)) void scan_grad_kernel(cons
       E *out_x = at<E>(P.dx, t + sub - 1, 0), *out_t = at<E>(P.ddt, t + sub - 1, 0);
       E *out_z = GATE ? at<E>(P.dz, t + sub - 1, 0) : nullptr;
       asm volatile("" : "+s"(step_x), "+s"(step_t), "+s"(step_z), "+s"(out_x), "+s"(out_t), "+s"(out_z));
+      // the rows of B and C, of the tokens forwards and back
+      const E *row_b = at<const E>(P.B, t, group), *row_c = at<const E>(P.C, t + n_t - 1, group);
+      int64_t step_b = P.B.ts, step_c = P.C.ts;
+      asm volatile("" : "+s"(step_b), "+s"(step_c), "+s"(row_b), "+s"(row_c));
       ScanRow<E, N> B, C;
-      B.load(A.B, t, ch.g);
+      B.load(row_b);
 #pragma unroll
       for (int u = 0; u < sub; ++u) {
         fd[u] = scan_step(A, fd[u], slope[u]);
@@ -241,8 +238,9 @@ __global__ __launch_bounds__(256, scan_grad_waves(N)) void scan_grad_kernel(cons
       for (int u = 0; u + 1 < sub; ++u) {
         __builtin_amdgcn_sched_barrier(0);
         const ScanRow<E, N> b = B;
-        B.load(A.B, min(t + u + 1, k.t1 - 1), ch.g);
-        if (u + 2 == sub) C.load(A.C, min(t + u + 1, k.t1 - 1), ch.g);
+        row_b += u + 1 < n_t ? step_b : 0;
+        B.load(row_b);
+        if (u + 2 == sub) C.load(row_c);
         const float dx = fd[u] * fx[u];
 #pragma unroll
         for (int n = 0; n < N; ++n)
@@ -251,11 +249,16 @@ __global__ __launch_bounds__(256, scan_grad_waves(N)) void scan_grad_kernel(cons
 #pragma unroll
       for (int u = sub - 1; u >= 0; --u) {
         __builtin_amdgcn_sched_barrier(0);
-        if (u == 1 && r > 0) load_start(r - 1);  // into the registers of the tokens that are done
+        if (u == 1 && r > 0) {  // into the registers of the tokens that are done
+          load(r - 1);
+          load_start(r - 1);
+        }
         const ScanRow<E, N> b = B, cc = C;
         if (u > 0) {
-          B.load(A.B, min(t + u - 1, k.t1 - 1), ch.g);
-          C.load(A.C, min(t + u - 1, k.t1 - 1), ch.g);
+          row_b -= u < n_t ? step_b : 0;
+          row_c -= u < n_t ? step_c : 0;
+          B.load(row_b);
+          C.load(row_c);
         }
         float d = fd[u];
         // the decays again, but for those used next: keeping the run's spills (643 us
@@ -275,48 +278,54 @@ __global__ __launch_bounds__(256, scan_grad_waves(N)) void scan_grad_kernel(cons
 #pragma unroll
           for (int m = 0; m < 4; ++m) {
             const int n = 4 * q + m;
-            const float a = __builtin_amdgcn_exp2f(d * a2[n]), ah = a * hist[u][n];
-            const float h = u + 1 < sub ? hist[u + 1 < sub ? u + 1 : u][n] : fmaf(xd, b[n], ah);
+            const float a = __builtin_amdgcn_exp2f(d * a2[n]);
+            const float h = u + 1 < sub ? hist[u + 1 < sub ? u + 1 : u][n] : fmaf(a, hist[u][n], xd * b[n]);
             p = fmaf(cc[n], h, p);
             const float gn = fmaf(cc[n], dp, g[q][m]);
             gb = fmaf(gn, b[n], gb);
-            const float e = gn * ah;
+            g[q][m] = gn * a;
+            const float e = g[q][m] * hist[u][n];
             ea = fmaf(e, a2[n], ea);
             dA[q][m] = fmaf(e, d, dA[q][m]);
             vb[m] = gn * xd;
             vc[m] = dp * h;
-            g[q][m] = gn * a;
           }
-          fold[q] = fold4(vb, lane);
-          fold[N / 4 + q] = fold4(vc, lane);
+          fold[q] = fold4(vb);
+          fold[N / 4 + q] = fold4(vc);
         }
 #pragma unroll
         for (int q = 0; q < Q; q += 4) {
-          const float four[4] = {fold[q], fold[q + 1], fold[q + 2], fold[q + 3]};
-          sh[r & 1][u][w4 * 4 + (lane >> 4)][4 * q + place] = fold16(four, lane);
+          const floatx4 four = {fold[q], fold[q + 1], fold[q + 2], fold[q + 3]};
+          *reinterpret_cast<floatx4 *>(&sh[w4][u][(lane >> 4) * 4 + (lane & 3)][place * Q + q]) = four;
         }
         const float ddt = fmaf(gb, fx[u], ea * kLn2) * slope[u];
         const float dz = fy[u] * p * (s * fmaf(fz[u], 1.f - s, 1.f));
         dskip = fmaf(dp, fx[u], dskip);
         dbias += u < n_t ? ddt : 0.f;
-        if (ch.on && u < n_t) {
-          lane_store(out_x, ch.c, from_f<E>(fmaf(gb, d, skip * dp)));
-          lane_store(out_t, ch.c, from_f<E>(ddt));
-          if (GATE) lane_store(out_z, ch.c, from_f<E>(dz));
-        }
+        const int bytes = u < n_t ? row_bytes : 0;
+        lane_store(out_x, bytes, off, from_f<E>(fmaf(gb, d, skip * dp)));
+        lane_store(out_t, bytes, off, from_f<E>(ddt));
+        if (GATE) lane_store(out_z, bytes, off, from_f<E>(dz));
         out_x -= step_x;
         out_t -= step_t;
         if (GATE) out_z -= step_z;
       }
-      __syncthreads();  // (the other half of `sh` is written next)
-      // two lanes a sum, eight of its sixteen shares each
-      for (int v = threadIdx.x; v < n_t * 4 * N; v += 256) {
-        const int u = v / (4 * N), n = v % (4 * N) / 2, m0 = (v & 1) * 8;
-        float y = 0.f;
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      // sixteen lanes a token, the sixteen shares of their sums in order
+      constexpr int V = N / 8;
+      const int u = lane >> 4, n = (lane & 15) * V;
+      float y[V];
 #pragma unroll
-        for (int m = 0; m < 8; ++m) y += sh[r & 1][u][m0 + m][n];
-        y += dpp<0xB1>(y);
-        if (!(v & 1)) A.part_bc[((int64_t)gb * A.tokens + t + u) * 2 * N + n] = y;
+      for (int e = 0; e < V; ++e) {
+        y[e] = sh[w4][u][0][n + e];
+#pragma unroll
+        for (int i = 1; i < 16; ++i) y[e] += sh[w4][u][i][n + e];
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      if (u < n_t) {
+        float *to = A.part_bc + ((int64_t)tile * A.tokens + t + u) * 2 * N + n;
+#pragma unroll
+        for (int e = 0; e < V; ++e) to[e] = y[e];
       }
     }
     if (A.dS0 && k.c == 0 && ch.on) scan_store_rows<N>(A.dS0, k.i * width + ch.c, g);
@@ -324,7 +333,8 @@ __global__ __launch_bounds__(256, scan_grad_waves(N)) void scan_grad_kernel(cons
   if (!ch.on) return;
   // (slots without a chunk: zeros)
   float *part = A.part_a + (int64_t)slot * (N + 2) * width;
-  scan_store_cols<N>(part, width, ch.c, dA);
+#pragma unroll
+  for (int n = 0; n < N; ++n) part[n * width + ch.c] = dA[n >> 2][n & 3];
   part[N * width + ch.c] = dskip;
   part[(N + 1) * width + ch.c] = dbias;
 }
@@ -334,7 +344,7 @@ __global__ __launch_bounds__(256, scan_grad_waves(N)) void scan_grad_kernel(cons
 // group, state of B or C).  The others: dA, dD and dbias over the chunks, workgroup
 // (64 channels, state), wave (a share of the slots).
 template <class E>
-__global__ __launch_bounds__(512) void scan_grad_sum_kernel(const ScanArgs A, int states, int blocks_group,
+__global__ __launch_bounds__(512) void scan_grad_sum_kernel(const ScanArgs A, int states, int tiles_group,
                                                             int64_t blocks_bc) {
   __shared__ float sh[8][64];
   if (blockIdx.x < blocks_bc) {
@@ -343,13 +353,14 @@ __global__ __launch_bounds__(512) void scan_grad_sum_kernel(const ScanArgs A, in
     const int64_t t = id / (2 * states) / A.groups;
     if (t < A.cu[0] || t >= A.cu[A.seqs] || t >= A.tokens) return;  // of no sequence
     float x = 0.f;
-#pragma unroll 4
-    for (int b = 0; b < blocks_group; ++b)
-      x += A.part_bc[(((int64_t)g * blocks_group + b) * A.tokens + t) * 2 * states + n];
-    if (n < states)
-      at<E>(A.dB, t, g)[n] = from_f<E>(x);
+#pragma unroll 8
+    for (int b = 0; b < tiles_group; ++b)
+      x += A.part_bc[(((int64_t)g * tiles_group + b) * A.tokens + t) * 2 * states + n];
+    const int half = states / 2, s = 4 * (n % half) + n / half;
+    if (s < states)
+      at<E>(A.dB, t, g)[s] = from_f<E>(x);
     else
-      at<E>(A.dC, t, g)[n - states] = from_f<E>(x);
+      at<E>(A.dC, t, g)[s - states] = from_f<E>(x);
     return;
   }
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
@@ -377,7 +388,7 @@ __global__ __launch_bounds__(512) void scan_grad_sum_kernel(const ScanArgs A, in
 
 template <class E, int N>
 static hipError_t scan_back(const ScanArgs &a, hipStream_t stream) {
-  const int64_t tiles = scan_tiles(a.channels, a.groups), blocks = scan_group_blocks(a.per);
+  const int64_t tiles = scan_tiles(a.channels, a.groups), waves = tiles * a.slots;
   if (a.tokens > a.chunk) {
     const int64_t parts = tiles * scan_slots(a.tokens, a.seqs, a.part);
     const dim3 grid((unsigned)((parts + 3) / 4));
@@ -385,19 +396,19 @@ static hipError_t scan_back(const ScanArgs &a, hipStream_t stream) {
       hipLaunchKernelGGL((scan_grad_local_kernel<E, N, true>), grid, dim3(256), 0, stream, a, (int)tiles, parts);
     else
       hipLaunchKernelGGL((scan_grad_local_kernel<E, N, false>), grid, dim3(256), 0, stream, a, (int)tiles, parts);
-    const int64_t threads = (int64_t)a.seqs * a.channels * N;
-    hipLaunchKernelGGL(scan_grad_carry_kernel, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, stream, a, N,
-                       threads);
+    const int blocks = (a.channels * N + 255) / 256;
+    hipLaunchKernelGGL(scan_grad_carry_kernel, dim3((unsigned)(a.seqs * (int64_t)blocks)), dim3(256), 0, stream, a, N,
+                       blocks);
   }
-  const dim3 grid((unsigned)(a.slots * a.groups * blocks));
+  const dim3 grid((unsigned)((waves + 3) / 4));
   if (a.z.ptr)
-    hipLaunchKernelGGL((scan_grad_kernel<E, N, true>), grid, dim3(256), 0, stream, a, (int)blocks);
+    hipLaunchKernelGGL((scan_grad_kernel<E, N, true>), grid, dim3(256), 0, stream, a, (int)tiles, waves);
   else
-    hipLaunchKernelGGL((scan_grad_kernel<E, N, false>), grid, dim3(256), 0, stream, a, (int)blocks);
+    hipLaunchKernelGGL((scan_grad_kernel<E, N, false>), grid, dim3(256), 0, stream, a, (int)tiles, waves);
   const int64_t blocks_bc = (a.tokens * a.groups * 2 * N + 511) / 512;
   const int64_t blocks_sum = (int64_t)((a.channels + 63) / 64) * (N + 2);
   hipLaunchKernelGGL((scan_grad_sum_kernel<E>), dim3((unsigned)(blocks_bc + blocks_sum)), dim3(512), 0, stream, a, N,
-                     (int)blocks, blocks_bc);
+                     (int)(tiles / a.groups), blocks_bc);
   return hipGetLastError();
 }
 template <class E>
