@@ -119,7 +119,7 @@ inline int scan_forward_chunk(int64_t tokens, int64_t seqs, int channels, int gr
 // room for more waves.
 constexpr int scan_grad_waves(int states) { return states > 16 ? 1 : states > 8 ? 2 : 3; }
 inline int scan_grad_chunk(int64_t tokens, int64_t seqs, int channels, int groups, int states) {
-  return scan_chunk_tokens(tokens, seqs, (scan_tiles(channels, groups) + 3) / 4, kScanPart,
+  return scan_chunk_tokens(tokens, seqs, (scan_tiles(channels, groups) + 3) / 4, 8,
                            scan_grad_waves(states), 0.7);
 }
 

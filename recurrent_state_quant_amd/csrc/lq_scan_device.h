@@ -85,13 +85,6 @@ template <class E, int N> struct ScanRow {
   }
 };
 
-// x b, as a fused product and sum with zero for fp16: that instruction takes an
-// fp16 operand as it is
-template <class E>
-__device__ __forceinline__ float scan_times(float x, float b) {
-  if constexpr (std::is_same_v<E, F16>) return fmaf(x, b, 0.f);
-  return x * b;
-}
 
 // The same row as a matrix operand: lane l holds value l mod 16 (N = 8: mod 8) of
 // each sixteen.  s[n] += row[n] x for every lane's own x is then one instruction

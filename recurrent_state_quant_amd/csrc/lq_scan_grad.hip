@@ -177,20 +177,25 @@ __global__ __launch_bounds__(256, scan_grad_waves(N)) void scan_grad_kernel(cons
     const int place = fold_place(lane), row_bytes = (int)(width * sizeof(E));
     const uint32_t off = lane_offset(ch.on, ch.c, sizeof(E));
     E rx[sub], rd[sub], ry[sub], rz[sub];
+    ScanLanes<E, N> rb[sub - 1], rc[sub];
     ScanState<N> start;  // the states before the run's tokens
     const auto load = [&](int r) {
       const int t = k.t0 + r * sub;
       const ScanArgs &P = scan_args();
       const E *x = at<const E>(P.x, t, 0), *dt = at<const E>(P.dt, t, 0), *dy = at<const E>(P.dy, t, 0);
-      const E *z = GATE ? at<const E>(P.z, t, 0) : x;
+      const E *z = GATE ? at<const E>(P.z, t, 0) : x, *b = at<const E>(P.B, t, group), *cc = at<const E>(P.C, t, group);
 #pragma unroll
       for (int u = 0; u < sub; ++u) {
         rx[u] = lane_load(x, ch.c);
+        if (u + 1 < sub) rb[u].load(b, lane);
+        rc[u].load(cc, lane);
         rd[u] = lane_load(dt, ch.c);
         ry[u] = lane_load(dy, ch.c);
         if (GATE) rz[u] = lane_load(z, ch.c);
         if (t + u + 1 < k.t1) {
           x += P.x.ts;
+          b += P.B.ts;
+          cc += P.C.ts;
           dt += P.dt.ts;
           dy += P.dy.ts;
           if (GATE) z += P.z.ts;
@@ -206,16 +211,23 @@ __global__ __launch_bounds__(256, scan_grad_waves(N)) void scan_grad_kernel(cons
     }
     for (int r = runs - 1; r >= 0; --r) {
       const int t = k.t0 + r * sub, n_t = min(sub, k.t1 - t);
-      float fx[sub], fd[sub], fy[sub], fz[sub], slope[sub], hist[sub][N];
+      float fx[sub], fd[sub], fy[sub], fz[sub], slope[sub];
+      float fb[sub - 1][ScanLanes<E, N>::rows], fc[sub][ScanLanes<E, N>::rows];
+      ScanState<N> hist[sub];
 #pragma unroll
       for (int u = 0; u < sub; ++u) {
+#pragma unroll
+        for (int i = 0; i < ScanLanes<E, N>::rows; ++i) {
+          fc[u][i] = to_f(rc[u].e[i]);
+          if (u + 1 < sub) fb[u][i] = to_f(rb[u].e[i]);
+        }
         fx[u] = ch.on ? to_f(rx[u]) : 0.f;
         fd[u] = to_f(rd[u]) + bias;
         fy[u] = ch.on ? to_f(ry[u]) : 0.f;
         fz[u] = GATE ? to_f(rz[u]) : 0.f;
       }
 #pragma unroll
-      for (int n = 0; n < N; ++n) hist[0][n] = start[n >> 2][n & 3];
+      for (int q = 0; q < N / 4; ++q) hist[0][q] = start[q];
       // the output rows of the run's last token, and the way to the one before:
       // reading them for each token would wait for the rows of B and C on their way
       const ScanArgs &P = scan_args();
@@ -224,11 +236,12 @@ __global__ __launch_bounds__(256, scan_grad_waves(N)) void scan_grad_kernel(cons
       E *out_z = GATE ? at<E>(P.dz, t + sub - 1, 0) : nullptr;
       asm volatile("" : "+s"(step_x), "+s"(step_t), "+s"(step_z), "+s"(out_x), "+s"(out_t), "+s"(out_z));
       // the rows of B and C, of the tokens forwards and back
-      const E *row_b = at<const E>(P.B, t, group), *row_c = at<const E>(P.C, t + n_t - 1, group);
+      const E *row_b = at<const E>(P.B, t + n_t - 1, group), *row_c = at<const E>(P.C, t + n_t - 1, group);
       int64_t step_b = P.B.ts, step_c = P.C.ts;
       asm volatile("" : "+s"(step_b), "+s"(step_c), "+s"(row_b), "+s"(row_c));
       ScanRow<E, N> B, C;
       B.load(row_b);
+      C.load(row_c);
 #pragma unroll
       for (int u = 0; u < sub; ++u) {
         fd[u] = scan_step(A, fd[u], slope[u]);
@@ -237,14 +250,10 @@ __global__ __launch_bounds__(256, scan_grad_waves(N)) void scan_grad_kernel(cons
 #pragma unroll
       for (int u = 0; u + 1 < sub; ++u) {
         __builtin_amdgcn_sched_barrier(0);
-        const ScanRow<E, N> b = B;
-        row_b += u + 1 < n_t ? step_b : 0;
-        B.load(row_b);
-        if (u + 2 == sub) C.load(row_c);
-        const float dx = fd[u] * fx[u];
 #pragma unroll
         for (int n = 0; n < N; ++n)
-          hist[u + 1][n] = fmaf(__builtin_amdgcn_exp2f(fd[u] * a2[n]), hist[u][n], scan_times<E>(dx, b[n]));
+          hist[u + 1][n >> 2][n & 3] = __builtin_amdgcn_exp2f(fd[u] * a2[n]) * hist[u][n >> 2][n & 3];
+        scan_add_outer<N>(hist[u + 1], fb[u], fd[u] * fx[u]);
       }
 #pragma unroll
       for (int u = sub - 1; u >= 0; --u) {
@@ -272,6 +281,7 @@ __global__ __launch_bounds__(256, scan_grad_waves(N)) void scan_grad_kernel(cons
         }
         float p = skip * fx[u], gb = 0.f, ea = 0.f;
         float fold[Q];
+        scan_add_outer<N>(g, fc[u], dp);
 #pragma unroll
         for (int q = 0; q < N / 4; ++q) {
           float vb[4], vc[4];
@@ -279,12 +289,12 @@ __global__ __launch_bounds__(256, scan_grad_waves(N)) void scan_grad_kernel(cons
           for (int m = 0; m < 4; ++m) {
             const int n = 4 * q + m;
             const float a = __builtin_amdgcn_exp2f(d * a2[n]);
-            const float h = u + 1 < sub ? hist[u + 1 < sub ? u + 1 : u][n] : fmaf(a, hist[u][n], xd * b[n]);
+            const float h = u + 1 < sub ? hist[u + 1 < sub ? u + 1 : u][q][m] : fmaf(a, hist[u][q][m], xd * b[n]);
             p = fmaf(cc[n], h, p);
-            const float gn = fmaf(cc[n], dp, g[q][m]);
+            const float gn = g[q][m];
             gb = fmaf(gn, b[n], gb);
             g[q][m] = gn * a;
-            const float e = g[q][m] * hist[u][n];
+            const float e = g[q][m] * hist[u][q][m];
             ea = fmaf(e, a2[n], ea);
             dA[q][m] = fmaf(e, d, dA[q][m]);
             vb[m] = gn * xd;
