@@ -72,7 +72,7 @@ struct ScanArgs {
   float *dA, *dskip, *dbias;
   const float *dS;
   float *dS0;
-  float *part_bc;  // [tiles][tokens][2 * states]
+  float *part_bc;  // [tiles][tokens][2 * states], in the order of the gradient's kernel
   float *part_a;   // [slots][states + 2][channels]
 };
 
@@ -95,12 +95,13 @@ inline int64_t scan_slots(int64_t tokens, int64_t seqs, int chunk) { return toke
 // rounds.  So the time is (chunk + what a wave's beginning takes, in tokens) times
 // the rounds' w + stall, and the best length one that fills the CUs evenly: 4,096
 // tokens x 64 waves took 98 us forward in chunks of 72 (3.6 waves a SIMD), 105 of
-// 80 (3.3).
+// 80 (3.3); the gradient of 8,192 tokens x 32 waves of four sequences takes 251 us in
+// chunks of 136, 261 of 40 or 144, 296 of 96, 328 of 128.
 constexpr int kScanPart = 16, kScanLeast = 32, kScanMost = 512, kScanBegin = 12, kScanCus = 256;
-inline int scan_chunk_tokens(int64_t tokens, int64_t seqs, int64_t workgroups, int step, int most, double stall) {
+inline int scan_chunk_tokens(int64_t tokens, int64_t seqs, int64_t workgroups, int most, double stall) {
   int best = kScanLeast;
   double least = 0;
-  for (int chunk = kScanLeast; chunk <= kScanMost; chunk += step) {
+  for (int chunk = kScanLeast; chunk <= kScanMost; chunk += 8) {
     // (half a chunk more for each sequence, as its last one is partly full)
     const int64_t each = ((tokens / chunk + (seqs + 1) / 2) * workgroups + kScanCus - 1) / kScanCus;
     const int64_t rounds = each / most, rest = each % most;
@@ -113,14 +114,13 @@ inline int scan_chunk_tokens(int64_t tokens, int64_t seqs, int64_t workgroups, i
 // Waves of the forward kernel that a SIMD holds
 constexpr int scan_forward_waves(int states) { return states > 16 ? 3 : states > 8 ? 5 : 6; }
 inline int scan_forward_chunk(int64_t tokens, int64_t seqs, int channels, int groups, int states) {
-  return scan_chunk_tokens(tokens, seqs, (scan_tiles(channels, groups) + 3) / 4, 8, scan_forward_waves(states), 1.4);
+  return scan_chunk_tokens(tokens, seqs, (scan_tiles(channels, groups) + 3) / 4, scan_forward_waves(states), 1.4);
 }
 // Of the gradient; its chunks from zero are half as long, as their kernel has
 // room for more waves.
 constexpr int scan_grad_waves(int states) { return states > 16 ? 1 : states > 8 ? 2 : 3; }
 inline int scan_grad_chunk(int64_t tokens, int64_t seqs, int channels, int groups, int states) {
-  return scan_chunk_tokens(tokens, seqs, (scan_tiles(channels, groups) + 3) / 4, 8,
-                           scan_grad_waves(states), 0.7);
+  return scan_chunk_tokens(tokens, seqs, (scan_tiles(channels, groups) + 3) / 4, scan_grad_waves(states), 0.7);
 }
 
 struct BlockNormArgs {

@@ -85,7 +85,6 @@ template <class E, int N> struct ScanRow {
   }
 };
 
-
 // The same row as a matrix operand: lane l holds value l mod 16 (N = 8: mod 8) of
 // each sixteen.  s[n] += row[n] x for every lane's own x is then one instruction
 // for four n: sixteen products of a 4 x 1 block and a 1 x 4 block, the columns of
@@ -96,8 +95,7 @@ template <class E, int N> struct ScanRow {
 // chunks' outputs of 8,192 tokens x 2,048 channels 113 -> 104 us, of 16,384 x
 // 4,096 340 -> 324, their states from zero 243 -> 217.  The sum over n of C_n h_n
 // done likewise is slower (116 us of 8,192 x 2,048): four times the instructions,
-// each waiting for the last.  In the gradient's main kernel it spills (452 us for
-// 285).
+// each waiting for the last.  The gradient's main kernel takes 249 us for 258.
 template <class E, int N> struct ScanLanes {
   static constexpr int rows = (N + 15) / 16, period = N < 16 ? N : 16;
   E e[rows];

@@ -14,14 +14,12 @@
 // is computed again from them, its states stay in registers, and it is taken
 // backwards.
 //
-// Bound by vector instructions (73 % of the issue slots taken, at two waves a SIMD
-// with 16 states): each token's decays are computed twice, and with the sums over
-// the channels a state takes some 20 instructions.  8,192 tokens x 2,048 channels x
-// 16 states in bf16: chunks from zero 75 us, between them 13, main kernel 285, the
-// sums of its workgroups 7.  Without any sums over channels the main kernel took
-// 256 us, without its loads of kept states, of B and C or of the inputs 246 to 252,
-// without its stores 239, all of 294 then.  1,021 tokens x 1,111 channels x 8
-// states in fp32: 10 + 8 + 29 + 4.
+// Bound by vector instructions (of the time that waves are resident, 93 % of the
+// issue slots are taken, at two waves a SIMD with 16 states): each token's decays
+// are computed twice, and with the sums over the channels a state takes some 20
+// instructions.  8,192 tokens x 2,048 channels x 16 states in bf16: chunks from zero
+// 75 us, between them 11, main kernel 249, the sums of its waves 9.  1,021 tokens x
+// 1,111 channels x 8 states in fp32: 10 + 6 + 27 + 4.
 #include "lq_scan_device.h"
 
 namespace lq {
@@ -123,9 +121,14 @@ __global__ __launch_bounds__(256) void scan_grad_carry_kernel(const ScanArgs A, 
 
 // Sums of many registers over the 16 lanes of a row at once: two registers become
 // one, in which half of the lanes go on with the one and half with the other.
-// Three instructions a step, 90 for 32 sums.  8,192 tokens x 2,048 channels take
-// 285 us; with four-lane sums by products with ones on the matrix pipe, whose
-// instructions wait for it and for one another, 350 for 296 then.
+// Two instructions a step: a masked add writes the one's sum into half of the lanes
+// of the other's.  The last two steps would need three, as the mask is of four
+// lanes; the sixteen lanes that are left a sum meet in LDS.  8,192 tokens x 2,048
+// channels with all four steps by selects, three instructions each, 281 us for 256;
+// four-lane sums by products with ones on the matrix pipe, whose instructions wait
+// for it and for one another, 350 for 296; the values through LDS, a lane adding
+// four sums over eight channels, 302 for 290: fewer instructions, but waits that two
+// waves a SIMD do not hide.
 // Lanes with bits 3 and 2 of (0, 0), (1, 0), (0, 1), (1, 1) come to hold the sums of
 // v[0], v[1], v[2], v[3] over the four lanes with the same bits 1 and 0.  (All lanes
 // are active; the s_nops keep the two cycles between writing a register and
@@ -146,8 +149,9 @@ __device__ __forceinline__ float fold4(const float (&v)[4]) {
 }
 __device__ __forceinline__ int fold_place(int lane) { return 2 * (lane >> 2 & 1) + (lane >> 3 & 1); }
 
-// A block's four waves share a group and a chunk: their sums over the channels
-// meet in LDS after every run of tokens.
+// The waves share nothing (a workgroup whose waves met after every run of tokens, to
+// write a fourth of the sums, was no faster): each writes its sums over its channels
+// for every token, as fold4 places them, sum 4 q + place at place * states / 2 + q.
 template <class E, int N, bool GATE>
 __global__ __launch_bounds__(256, scan_grad_waves(N)) void scan_grad_kernel(const ScanArgs A, int tiles, int64_t waves) {
   constexpr int sub = kScanSub, row = 2 * N + 4, Q = N / 2;  // Q: fours of sums, dB's and dC's
@@ -245,7 +249,7 @@ __global__ __launch_bounds__(256, scan_grad_waves(N)) void scan_grad_kernel(cons
 #pragma unroll
       for (int u = 0; u < sub; ++u) {
         fd[u] = scan_step(A, fd[u], slope[u]);
-        if (u >= n_t) fd[u] = fy[u] = 0.f;  // past the chunk's end: a step of zero that nothing comes of
+        if (u >= n_t) fd[u] = fx[u] = fy[u] = fz[u] = 0.f;  // past the chunk's end: a step of zero that nothing comes of
       }
 #pragma unroll
       for (int u = 0; u + 1 < sub; ++u) {
@@ -270,7 +274,7 @@ __global__ __launch_bounds__(256, scan_grad_waves(N)) void scan_grad_kernel(cons
           C.load(row_c);
         }
         float d = fd[u];
-        // the decays again, but for those used next: keeping the run's spills (643 us
+        // the decays again, but for those used next: keeping the run's spilled (643 us
         // for 294 of 8,192 tokens x 2,048 channels)
         if (u + 2 != sub || N > 16) asm("" : "+v"(d));
         const float xd = d * fx[u];
@@ -349,9 +353,9 @@ __global__ __launch_bounds__(256, scan_grad_waves(N)) void scan_grad_kernel(cons
   part[(N + 1) * width + ch.c] = dbias;
 }
 
-// The sums of the workgroups and chunks, added in order, in one launch.  The first
-// `blocks_bc` workgroups: dB and dC over the workgroups of a group, thread (token,
-// group, state of B or C).  The others: dA, dD and dbias over the chunks, workgroup
+// The sums of the waves and chunks, added in order, in one launch.  The first
+// `blocks_bc` workgroups: dB and dC over the waves of a group, thread (token, group,
+// place).  The others: dA, dD and dbias over the chunks, workgroup
 // (64 channels, state), wave (a share of the slots).
 template <class E>
 __global__ __launch_bounds__(512) void scan_grad_sum_kernel(const ScanArgs A, int states, int tiles_group,
