@@ -236,8 +236,8 @@ __global__ __launch_bounds__(256, scan_grad_waves(N)) void scan_grad_kernel(cons
       // reading them for each token would wait for the rows of B and C on their way
       const ScanArgs &P = scan_args();
       int64_t step_x = P.dx.ts, step_t = P.ddt.ts, step_z = GATE ? P.dz.ts : 0;
-      E *out_x = at<E>(P.dx, t + sub - 1, 0), *out_t = at<E>(P.ddt, t + sub - 1, 0);
-      E *out_z = GATE ? at<E>(P.dz, t + sub - 1, 0) : nullptr;
+      E *out_x = at<E>(P.dx, t + n_t - 1, 0), *out_t = at<E>(P.ddt, t + n_t - 1, 0);
+      E *out_z = GATE ? at<E>(P.dz, t + n_t - 1, 0) : nullptr;
       asm volatile("" : "+s"(step_x), "+s"(step_t), "+s"(step_z), "+s"(out_x), "+s"(out_t), "+s"(out_z));
       // the rows of B and C, of the tokens forwards and back
       const E *row_b = at<const E>(P.B, t + n_t - 1, group), *row_c = at<const E>(P.C, t + n_t - 1, group);
@@ -247,10 +247,7 @@ __global__ __launch_bounds__(256, scan_grad_waves(N)) void scan_grad_kernel(cons
       B.load(row_b);
       C.load(row_c);
 #pragma unroll
-      for (int u = 0; u < sub; ++u) {
-        fd[u] = scan_step(A, fd[u], slope[u]);
-        if (u >= n_t) fd[u] = fx[u] = fy[u] = fz[u] = 0.f;  // past the chunk's end: a step of zero that nothing comes of
-      }
+      for (int u = 0; u < sub; ++u) fd[u] = scan_step(A, fd[u], slope[u]);
 #pragma unroll
       for (int u = 0; u + 1 < sub; ++u) {
         __builtin_amdgcn_sched_barrier(0);
@@ -266,10 +263,11 @@ __global__ __launch_bounds__(256, scan_grad_waves(N)) void scan_grad_kernel(cons
           load(r - 1);
           load_start(r - 1);
         }
+        if (u >= n_t) continue;  // past the chunk's end
         const ScanRow<E, N> b = B, cc = C;
         if (u > 0) {
-          row_b -= u < n_t ? step_b : 0;
-          row_c -= u < n_t ? step_c : 0;
+          row_b -= step_b;
+          row_c -= step_c;
           B.load(row_b);
           C.load(row_c);
         }
@@ -315,11 +313,10 @@ __global__ __launch_bounds__(256, scan_grad_waves(N)) void scan_grad_kernel(cons
         const float ddt = fmaf(gb, fx[u], ea * kLn2) * slope[u];
         const float dz = fy[u] * p * (s * fmaf(fz[u], 1.f - s, 1.f));
         dskip = fmaf(dp, fx[u], dskip);
-        dbias += u < n_t ? ddt : 0.f;
-        const int bytes = u < n_t ? row_bytes : 0;
-        lane_store(out_x, bytes, off, from_f<E>(fmaf(gb, d, skip * dp)));
-        lane_store(out_t, bytes, off, from_f<E>(ddt));
-        if (GATE) lane_store(out_z, bytes, off, from_f<E>(dz));
+        dbias += ddt;
+        lane_store(out_x, row_bytes, off, from_f<E>(fmaf(gb, d, skip * dp)));
+        lane_store(out_t, row_bytes, off, from_f<E>(ddt));
+        if (GATE) lane_store(out_z, row_bytes, off, from_f<E>(dz));
         out_x -= step_x;
         out_t -= step_t;
         if (GATE) out_z -= step_z;

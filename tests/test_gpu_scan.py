@@ -426,3 +426,32 @@ def test_refusals_on_the_device():
     S = z(2 * 32 * 8 + 8)
     with pytest.raises(lq.LeapQuantError):   # states that overlap in part
         lq.leapquant_scan_forward(plan, **ok, S0=S[:512].view(2, 32, 8), S=S[8:].view(2, 32, 8))
+
+
+@pytest.mark.parametrize("N", [8, 16, 32])
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+def test_a_last_input_that_is_not_finite(value, N):
+    """It enters the results where the formula has it, and the gradient of A not at all: a step decays the state before
+    it.  The sequences end 1, 2, 3 and 4 tokens into a run of the gradient's."""
+    cu, c = [0, 5, 11, 18, 26], 70
+    x = make(cu, 26, c, N, 1, F32, seed=60 + N)
+    for end in cu[1:]:
+        x["x"][end - 1, [3, 69]] = value
+    d = dev(x)
+    plan, y, S = forward(cu, d, save=True)
+    ref, top = reference(cu, x)
+    got = backward(plan, cu, d)
+    assert torch.isfinite(ref["A"]).all() and torch.isfinite(got["A"]).all()
+    check(got["A"], ref["A"], 9 * 8 + 2 * N + c + 160 + 26, "dA", top["A"])
+    for t, r in ((y, ref["y"]), (S, ref["S"]), (got["x"], ref["x"]), (got["dt"], ref["dt"]), (got["z"], ref["z"]),
+                 (got["B"], ref["B"]), (got["C"], ref["C"]), (got["S0"], ref["S0"]), (got["bias"], ref["bias"])):
+        assert torch.equal(torch.isfinite(t.cpu()), torch.isfinite(r))
+
+
+def test_many_waves_of_a_group():
+    """Sums of B's and C's gradients over channels of several waves and groups, the last wave partly full."""
+    cu = [0, 37, 90]
+    x = make(cu, 90, 2 * 333, 16, 2, F32, seed=70)
+    d = dev(x)
+    plan, y, S = forward(cu, d, save=True)
+    check_all(cu, d, x, y, S, backward(plan, cu, d))
