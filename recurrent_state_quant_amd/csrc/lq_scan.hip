@@ -98,26 +98,26 @@ __global__ __launch_bounds__(256, scan_forward_waves(N)) void scan_kernel(const 
       fz[u] = GATE ? to_f(rz[u]) : 0.f;
     }
     if (t + ahead < k.t1) load(t + ahead);
+    scan_steps<E>(A, fd);
 #pragma unroll
     for (int u = 0; u < ahead; ++u) {
       __builtin_amdgcn_sched_barrier(0);
       const int tt = t + u;
+      if (tt >= k.t1) break;
       const ScanRow<E, N> cc = C;
       if (OUT) {
         row += tt + 1 < k.t1 ? A.C.ts : 0;
         C.load(row);
       }
       if (SAVE && u % kScanSub == 0) {
-        scan_store_fours<N>(check, (int)width, tt < k.t1, off_s, h);
+        scan_store_fours<N>(check, (int)width, off_s, h);
         check += N * width;
       }
-      // past the chunk's end: a step of zero
-      const bool in = tt < k.t1;
-      const float d = in ? scan_step(A, fd[u]) : 0.f, x = in ? fx[u] : 0.f, dx = d * x;
+      const float d = fd[u], x = fx[u];
       sum += d;
 #pragma unroll
       for (int n = 0; n < N; ++n) h[n >> 2][n & 3] *= __builtin_amdgcn_exp2f(d * a2[n]);
-      scan_add_outer<N>(h, fb[u], dx);
+      scan_add_outer<N>(h, fb[u], d * x);
       if (OUT) {
         float p0 = skip * x, p1 = 0.f;
 #pragma unroll
@@ -127,14 +127,14 @@ __global__ __launch_bounds__(256, scan_forward_waves(N)) void scan_kernel(const 
         }
         float p = p0 + p1;
         if (GATE) p *= fz[u] * sigmoid_for<E>(fz[u]);
-        lane_store(y, in ? row_bytes : 0, off_y, from_f<E>(p));
+        lane_store(y, row_bytes, off_y, from_f<E>(p));
         y += A.y.ts;
       }
     }
   }
   if (!ch.on) return;
   if (!OUT) {
-    scan_store_fours<N>(A.carry + (int64_t)slot * N * width, (int)width, true, off_s, h);
+    scan_store_fours<N>(A.carry + (int64_t)slot * N * width, (int)width, off_s, h);
     A.sum[slot * width + ch.c] = sum;
   } else if (A.S && k.c + 1 >= k.chunks) {
     scan_store_rows<N>(A.S, k.i * width + ch.c, h);
@@ -192,7 +192,9 @@ __global__ __launch_bounds__(256) void scan_step_kernel(const ScanArgs A, int64_
   float b[4], cc[4];
   load4(at<const E>(A.B, row, g) + n, b);
   load4(at<const E>(A.C, row, g) + n, cc);
-  const float d = scan_step(A, v), dx = d * x, d2 = d * kLog2e;
+  float steps[1] = {v};
+  scan_steps<E>(A, steps);
+  const float d = steps[0], dx = d * x, d2 = d * kLog2e;
   vf4 h;
   h.x = fmaf(__builtin_amdgcn_exp2f(d2 * a.x), h0.x, dx * b[0]);
   h.y = fmaf(__builtin_amdgcn_exp2f(d2 * a.y), h0.y, dx * b[1]);

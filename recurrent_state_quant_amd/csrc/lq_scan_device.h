@@ -19,17 +19,34 @@ __device__ __forceinline__ float softplus_of(float v, float e) {
   p = fmaf(p * q, r, r);
   return fmaf(2.f, p, fmaxf(v, 0.f));
 }
-// the step of a token and channel from its input v
-__device__ __forceinline__ float scan_step(const ScanArgs &A, float v) {
-  return A.softplus ? softplus_of(v, exp_full(-fabsf(v))) : v;
+// e^-|v|.  For inputs of 16 bits without the rest of the exponent's product, |v|
+// 2^-24 of it: their own steps are 2^15 times that, and the sum with the bias in v
+// rounds by as much.
+template <class E>
+__device__ __forceinline__ float scan_exp(float v) {
+  if constexpr (sizeof(E) == 4) return exp_full(-fabsf(v));
+  return __builtin_amdgcn_exp2f(-kLog2e * fabsf(v));
 }
-// The same with the step's derivative by v.
-__device__ __forceinline__ float scan_step(const ScanArgs &A, float v, float &slope) {
-  slope = 1.f;
-  if (!A.softplus) return v;
-  const float e = exp_full(-fabsf(v)), s = __builtin_amdgcn_rcpf(1.f + e);
-  slope = v >= 0.f ? s : e * s;
-  return softplus_of(v, e);
+// The steps of a lane's tokens from their inputs v (in one branch: one a token
+// would keep the tokens' instructions apart)
+template <class E, int K>
+__device__ __forceinline__ void scan_steps(const ScanArgs &A, float (&v)[K]) {
+  if (!A.softplus) return;
+#pragma unroll
+  for (int u = 0; u < K; ++u) v[u] = softplus_of(v[u], scan_exp<E>(v[u]));
+}
+// The same with the steps' derivatives by v.
+template <class E, int K>
+__device__ __forceinline__ void scan_steps(const ScanArgs &A, float (&v)[K], float (&slope)[K]) {
+#pragma unroll
+  for (int u = 0; u < K; ++u) slope[u] = 1.f;
+  if (!A.softplus) return;
+#pragma unroll
+  for (int u = 0; u < K; ++u) {
+    const float e = scan_exp<E>(v[u]), s = __builtin_amdgcn_rcpf(1.f + e);
+    slope[u] = v[u] >= 0.f ? s : e * s;
+    v[u] = softplus_of(v[u], e);
+  }
 }
 
 // Element c of a row whose address is the same for the wave: the address stays
@@ -53,8 +70,7 @@ __device__ __forceinline__ T lane_load(const T *row, int c) {
 // Stores of lanes that may have nothing to store, without a branch: one around
 // them would leave the compiler with an unknown number of stores in flight, and so
 // waiting for all of them wherever it needs a load that came before.  `bytes` is
-// the row's length, or 0 for a row that is not stored; lanes of no channel have an
-// offset behind it.
+// the row's length; lanes of no channel have an offset behind it.
 __device__ __forceinline__ uint32_t lane_offset(bool on, int c, int size) { return on ? (uint32_t)c * size : ~0u; }
 template <class T>
 __device__ __forceinline__ void lane_store(T *row, int bytes, uint32_t off, T x) {
@@ -178,12 +194,11 @@ __device__ __forceinline__ void scan_load_fours(const float *p, int64_t channels
   }
 }
 template <int N>
-__device__ __forceinline__ void scan_store_fours(float *p, int channels, bool any, uint32_t off, const ScanState<N> &h) {
+__device__ __forceinline__ void scan_store_fours(float *p, int channels, uint32_t off, const ScanState<N> &h) {
   typedef unsigned int u4 __attribute__((ext_vector_type(4)));
-  const int bytes = any ? channels * 16 : 0;
 #pragma unroll
   for (int q = 0; q < N / 4; ++q) {
-    const auto r = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void *>(row_address(p)), (short)0, bytes, 0x00020000);
+    const auto r = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void *>(row_address(p)), (short)0, channels * 16, 0x00020000);
     __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4, h[q]), r, (int)off, 0, 0);
     p += 4 * (int64_t)channels;
   }

@@ -73,12 +73,12 @@ __global__ __launch_bounds__(256, N > 16 ? 3 : 4) void scan_grad_local_kernel(co
       fz[u] = GATE ? to_f(rz[u]) : 0.f;
     }
     if (t - ahead >= k.t0) load(t - ahead);
+    scan_steps<E>(A, fd);
 #pragma unroll
     for (int u = 0; u < ahead; ++u) {
       __builtin_amdgcn_sched_barrier(0);
-      const bool in = t - u >= k.t0;  // before the chunk's beginning: a step of zero
-      const float d = in ? scan_step(A, fd[u]) : 0.f;
-      const float dp = !in ? 0.f : GATE ? fy[u] * (fz[u] * sigmoid_for<E>(fz[u])) : fy[u];
+      if (t - u < k.t0) break;
+      const float d = fd[u], dp = GATE ? fy[u] * (fz[u] * sigmoid_for<E>(fz[u])) : fy[u];
       sum += d;
       scan_add_outer<N>(g, fc[u], dp);
 #pragma unroll
@@ -86,7 +86,7 @@ __global__ __launch_bounds__(256, N > 16 ? 3 : 4) void scan_grad_local_kernel(co
     }
   }
   if (!ch.on) return;
-  scan_store_fours<N>(A.carry + (int64_t)slot * N * width, (int)width, true, lane_offset(true, ch.c, 16), g);
+  scan_store_fours<N>(A.carry + (int64_t)slot * N * width, (int)width, lane_offset(true, ch.c, 16), g);
   A.sum[slot * width + ch.c] = sum;
 }
 
@@ -246,8 +246,7 @@ __global__ __launch_bounds__(256, scan_grad_waves(N)) void scan_grad_kernel(cons
       ScanRow<E, N> B, C;
       B.load(row_b);
       C.load(row_c);
-#pragma unroll
-      for (int u = 0; u < sub; ++u) fd[u] = scan_step(A, fd[u], slope[u]);
+      scan_steps<E>(A, fd, slope);
 #pragma unroll
       for (int u = 0; u + 1 < sub; ++u) {
         __builtin_amdgcn_sched_barrier(0);
