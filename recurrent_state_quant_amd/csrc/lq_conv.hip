@@ -9,16 +9,17 @@
 // Bound by memory traffic.  A lane holds the weights and the last K - 1 inputs of
 // 16 bytes of channels in registers and walks a run of tokens, so that every input
 // is read once but for the K - 1 around a run.  With width 4 in bf16, 16,384 tokens
-// x 8,192 channels of 24 sequences take 119 to 124 us (4.35 to 4.5 TB/s of input
-// and output), 8,192 x 6,144 44 us forward (4.6 TB/s) and 74 + 5 backward (4.1 TB/s
-// of two inputs and an output).  Loads and stores past the caches gain nothing
+// x 8,192 channels of 24 sequences take 118 us (4.6 TB/s of input and output), 8,192
+// x 6,144 43 us forward (4.7 TB/s) and 72 + 5 backward (4.2 TB/s of two inputs and an
+// output).  Loads and stores past the caches gain nothing
 // (48 us for 43 of inputs that are cached).
 #include "lq_layer_device.h"
 
 namespace lq {
 
-constexpr int kConvRun = 32;  // tokens of a wave, forward
-constexpr int kConvAhead = 8;  // rows loaded together
+// Rows loaded together: eight take 44 for 43 us of 8,192 tokens x 6,144 channels
+// forward and, at the same three waves a SIMD, 76 for 72 backward.
+constexpr int kConvAhead = 4;
 
 // The sequence of a token: tokens [s, e) of sequence i (i = -1: none yet)
 struct ConvSeq {
@@ -83,10 +84,10 @@ __device__ __forceinline__ void conv_shift(float (&win)[K - 1][V], const float (
   }
 }
 
-// A wave takes 64 V channels and a run of tokens, whatever sequences they are
-// of; the waves behind the runs take a sequence each and write its last inputs.
+// A wave takes 64 V channels and a run of tokens, whatever sequences they are of;
+// the waves behind the runs take a sequence each and write its last inputs.
 template <class E, int V, int K>
-__global__ __launch_bounds__(256) void conv_kernel(const ConvArgs A, int tiles, int64_t runs, int64_t waves) {
+__global__ __launch_bounds__(256) void conv_kernel(const ConvArgs A, int tiles, int run_tokens, int64_t runs, int64_t waves) {
   const int lane = threadIdx.x & 63;
   const int64_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) + (int64_t)blockIdx.x * 4;
   if (wave >= waves) return;  // whole waves; the waves share nothing
@@ -110,7 +111,7 @@ __global__ __launch_bounds__(256) void conv_kernel(const ConvArgs A, int tiles, 
     }
     return;
   }
-  const int t0 = (int)(run * kConvRun), t1 = (int)min((int64_t)t0 + kConvRun, A.tokens);
+  const int t0 = (int)(run * run_tokens), t1 = (int)min((int64_t)t0 + run_tokens, A.tokens);
   ConvSeq q = conv_seq(A, seq_search(A.cu, A.tokens, A.seqs, 1, 0, t0, lane));
   if (!on) return;
   float w[K][V], b[V], win[K - 1][V];
@@ -199,7 +200,7 @@ __device__ __forceinline__ void conv_back(bool silu, const float (&v)[V], float 
 // tokens still add.  The waves' weight gradients meet in LDS, the blocks' are
 // added by a second launch, all in a fixed order.
 template <class E, int V, int K>
-__global__ __launch_bounds__(256) void conv_backward_kernel(const ConvArgs A, int tiles, int run_tokens) {
+__global__ __launch_bounds__(256, sizeof(E) == 2 ? 3 : 2) void conv_backward_kernel(const ConvArgs A, int tiles, int run_tokens) {
   __shared__ float sh[4][K + 1][64 * V];
   const int lane = threadIdx.x & 63, w4 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t block = blockIdx.x / tiles;
@@ -383,11 +384,12 @@ __global__ __launch_bounds__(256) void conv_weight_kernel(const ConvArgs A, int6
 template <class E, int V, int K>
 static hipError_t conv_forward(const ConvArgs &a, hipStream_t stream) {
   const int tiles = (a.channels + 64 * V - 1) / (64 * V);
-  const int64_t runs = (a.tokens + kConvRun - 1) / kConvRun;
+  const int run = conv_run_tokens(a.tokens, tiles, 4);
+  const int64_t runs = (a.tokens + run - 1) / run;
   const int64_t waves = (runs + (a.X ? a.seqs : 0)) * tiles;
   if (waves)
-    hipLaunchKernelGGL((conv_kernel<E, V, K>), dim3((unsigned)((waves + 3) / 4)), dim3(256), 0, stream, a, tiles, runs,
-                       waves);
+    hipLaunchKernelGGL((conv_kernel<E, V, K>), dim3((unsigned)((waves + 3) / 4)), dim3(256), 0, stream, a, tiles, run,
+                       runs, waves);
   return hipGetLastError();
 }
 template <class E, int V, int K>

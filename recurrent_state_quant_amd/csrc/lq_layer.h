@@ -31,16 +31,22 @@ struct ConvArgs {
   float *part;  // [blocks of runs][width + 1][channels]
 };
 
-// Tokens of a run of the backward pass: a block takes four runs of the same
-// channels and joins their weight gradients.  Longer runs share more of the tokens
-// around them, once there are waves enough for three a SIMD (64 channels of four
-// values a wave): runs of 64 take 74 us of 8,192 tokens x 6,144 channels, of 32 83.
-// And they grow once there are 256 blocks of them, so that the joined sums stay few.
+// Tokens of a wave's run.  Longer runs share more of the tokens around them, once
+// there are waves enough of them, `least` a SIMD.  Forward four: runs of 64 take 118
+// us of 16,384 tokens x 16 tiles of channels, of 32 123 (four waves a SIMD with 64);
+// but 97 for 85 us of 8,192 x 24 tiles (three), 49 for 43 of 8,192 x 12.  Backward
+// three (256 channels a tile): 74 for 83 us of 8,192 x 24 tiles.
 constexpr int kConvRunLeast = 32, kConvRunMost = 4096;
-constexpr int64_t kConvBlocks = 256, kConvWaves = 12 * 256;
+constexpr int64_t kConvBlocks = 256, kSimds = 4 * 256;
+inline int conv_run_tokens(int64_t tokens, int64_t tiles, int least) {
+  return tokens / (2 * kConvRunLeast) * tiles >= least * kSimds ? 2 * kConvRunLeast : kConvRunLeast;
+}
+// Of the backward pass: a block takes four runs of the same channels and joins their
+// weight gradients, and runs grow once there are 256 blocks of them, so that the
+// joined sums stay few.
 inline int64_t conv_grad_blocks(int64_t tokens, int64_t run) { return (tokens + 4 * run - 1) / (4 * run); }
 inline int conv_grad_run(int64_t tokens, int64_t channels) {
-  int run = tokens / (2 * kConvRunLeast) * ((channels + 255) / 256) >= kConvWaves ? 2 * kConvRunLeast : kConvRunLeast;
+  int run = conv_run_tokens(tokens, (channels + 255) / 256, 3);
   while (run < kConvRunMost && conv_grad_blocks(tokens, run) > kConvBlocks) run *= 2;
   return run;
 }
