@@ -103,18 +103,30 @@ inline int64_t scan_slots(int64_t tokens, int64_t seqs, int chunk) { return toke
 // tokens x 64 waves took 98 us forward in chunks of 72 (3.6 waves a SIMD), 105 of
 // 80 (3.3); the gradient of 8,192 tokens x 32 waves of four sequences takes 251 us in
 // chunks of 136, 261 of 40 or 144, 296 of 96, 328 of 128.
-constexpr int kScanPart = 16, kScanLeast = 32, kScanMost = 512, kScanBegin = 12, kScanCus = 256;
+// A call whose sequences may have several chunks takes two launches more, 25 tokens'
+// time, and every chunk of a sequence lengthens the chain between them by 0.3
+// of a token's; one that needs no chunks from zero takes 0.6 of the rest.  (200 tokens x
+// 1,024 channels in chunks of 8 17.6 us, of 16 20.4, of 32 31.6.)  Chunks below 32
+// tokens are for calls that do not fill the chip: at most `scan_few` of them, which
+// bounds the workspace.
+constexpr int kScanLeast = 8, kScanShort = 32, kScanMost = 512, kScanBegin = 12, kScanCus = 256;
+inline int64_t scan_few(int64_t workgroups, int most) { return kScanCus * most / workgroups; }
 inline int scan_chunk_tokens(int64_t tokens, int64_t seqs, int64_t workgroups, int most, double stall) {
-  int best = kScanLeast;
+  int best = kScanShort;
   double least = 0;
-  for (int chunk = kScanLeast; chunk <= kScanMost; chunk += 8) {
+  const auto look = [&](int chunk) {
+    if (chunk < kScanShort && scan_slots(tokens, seqs, chunk) > scan_few(workgroups, most)) return int64_t(2);
     // (half a chunk more for each sequence, as its last one is partly full)
     const int64_t each = ((tokens / chunk + (seqs + 1) / 2) * workgroups + kScanCus - 1) / kScanCus;
     const int64_t rounds = each / most, rest = each % most;
-    const double time = (chunk + kScanBegin) * (rounds * (most + stall) + (rest ? rest + stall : 0));
-    if (chunk == kScanLeast || time < least) least = time, best = chunk;
-    if (each <= 1) break;
-  }
+    double time = (chunk + kScanBegin) * (rounds * (most + stall) + (rest ? rest + stall : 0));
+    time = tokens > chunk ? time + 25 + 0.3 * tokens / seqs / chunk : 0.6 * time;
+    if (least == 0 || time < least) least = time, best = chunk;
+    return each;
+  };
+  for (int chunk = kScanLeast; chunk <= kScanMost; chunk += 8)
+    if (look(chunk) <= 1) break;
+  if (tokens <= kScanMost) look(tokens <= kScanLeast ? kScanLeast : (int)(tokens + 7) / 8 * 8);
   return best;
 }
 // Waves of the forward kernel that a SIMD holds
@@ -122,11 +134,27 @@ constexpr int scan_forward_waves(int states) { return states > 16 ? 3 : states >
 inline int scan_forward_chunk(int64_t tokens, int64_t seqs, int channels, int groups, int states) {
   return scan_chunk_tokens(tokens, seqs, (scan_tiles(channels, groups) + 3) / 4, scan_forward_waves(states), 1.4);
 }
-// Of the gradient; its chunks from zero are half as long, as their kernel has
-// room for more waves.
+// Of the gradient; its chunks from zero are half as long where chunks fill the chip,
+// as their kernel has room for more waves (1,021 tokens x 1,111 channels, which do
+// not: 65.4 for 67.7 us with whole ones).
 constexpr int scan_grad_waves(int states) { return states > 16 ? 1 : states > 8 ? 2 : 3; }
 inline int scan_grad_chunk(int64_t tokens, int64_t seqs, int channels, int groups, int states) {
   return scan_chunk_tokens(tokens, seqs, (scan_tiles(channels, groups) + 3) / 4, scan_grad_waves(states), 0.7);
+}
+inline int scan_grad_part(int chunk) { return chunk >= kScanShort ? chunk / 2 : chunk; }
+// The most slots, of chunks or of those from zero, of any call with at most these
+// tokens and sequences
+inline int64_t scan_most_slots(int64_t tokens, int64_t seqs, int channels, int groups, int states, bool grad) {
+  const int64_t workgroups = (scan_tiles(channels, groups) + 3) / 4;
+  const int64_t all = scan_slots(tokens, seqs, kScanLeast);
+  int64_t few = scan_few(workgroups, scan_forward_waves(states)), many = scan_slots(tokens, seqs, kScanShort);
+  if (grad) {
+    const int64_t back = scan_few(workgroups, scan_grad_waves(states));
+    if (back > few) few = back;
+    many = scan_slots(tokens, seqs, scan_grad_part(kScanShort));
+  }
+  if (few > all) few = all;
+  return few > many ? few : many;
 }
 
 struct BlockNormArgs {

@@ -77,7 +77,7 @@ int check_scan(const lq_scan *sc, bool step) {
   // the grids: chunks (at least one a sequence, four waves a workgroup), the
   // states of all sequences, and the gradient's sums of B and C
   const int64_t tiles = lq::scan_tiles(sc->channels, sc->groups);
-  const int64_t slots = lq::scan_slots(sc->tokens, sc->seqs, lq::kScanPart);
+  const int64_t slots = lq::scan_most_slots(sc->tokens, sc->seqs, sc->channels, sc->groups, sc->states, true);
   if (slots > kMaxGrid / ((tiles + 3) / 4)) return LQ_ERR_SHAPE;
   if (sc->seqs > kMaxGrid / ((int64_t(sc->channels) * sc->states + 255) / 256)) return LQ_ERR_SHAPE;
   if (sc->tokens > (kMaxGrid * 256) / (int64_t(sc->groups) * 2 * sc->states)) return LQ_ERR_SHAPE;
@@ -89,7 +89,7 @@ int check_scan(const lq_scan *sc, bool step) {
 // sequences never need less.
 int64_t scan_space(const lq_scan *sc, bool save, char *base, lq::ScanArgs *a) {
   const int64_t channels = sc->channels, state = channels * sc->states * 4;
-  const int64_t slots = lq::scan_slots(sc->tokens, sc->seqs, save ? lq::kScanPart : lq::kScanLeast);
+  const int64_t slots = lq::scan_most_slots(sc->tokens, sc->seqs, sc->channels, sc->groups, sc->states, save);
   int64_t used = 0;
   const auto take = [&](auto **p, int64_t bytes) {
     if (base) *p = reinterpret_cast<std::remove_reference_t<decltype(*p)>>(base + used);
@@ -159,7 +159,7 @@ int scan_chunks(const lq_scan *sc, const int32_t *cu, void *ws, int64_t ws_bytes
   a->cu = cu;
   a->chunk = (back ? lq::scan_grad_chunk : lq::scan_forward_chunk)(sc->tokens, sc->seqs, sc->channels, sc->groups,
                                                                   sc->states);
-  a->part = back ? a->chunk / 2 : a->chunk;
+  a->part = back ? lq::scan_grad_part(a->chunk) : a->chunk;
   a->slots = lq::scan_slots(sc->tokens, sc->seqs, a->chunk);
   const int64_t need = scan_need(sc, save);
   if (need) {

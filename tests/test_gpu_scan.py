@@ -455,3 +455,14 @@ def test_many_waves_of_a_group():
     d = dev(x)
     plan, y, S = forward(cu, d, save=True)
     check_all(cu, d, x, y, S, backward(plan, cu, d))
+
+
+@pytest.mark.parametrize("tokens", [1, 7, 8, 9, 15, 16, 17, 23, 25, 31, 32, 33, 39, 41, 63, 65, 100, 129, 200])
+def test_lengths_around_the_chunks(tokens):
+    """One sequence of every form: in one chunk, in chunks of a few tokens, in longer ones."""
+    x = make([0, tokens], tokens, 72, 16, 1, F32, seed=80 + tokens, slow=-1.0)
+    d = dev(x)
+    plan, y, S = forward([0, tokens], d, save=True)
+    check_all([0, tokens], d, x, y, S, backward(plan, [0, tokens], d))
+    y2, S2 = forward([0, tokens], d)[1:]
+    assert torch.equal(y, y2) and torch.equal(S, S2)

@@ -236,7 +236,7 @@ def test_scan_workspace_covers_smaller_calls(lib, channels, groups):
                 y=_rows(1, channels))
     for save in (0, 1):
         size = lambda t, s: lib.leapquant_scan_workspace(_by(_sc(tokens=t, seqs=s, **kw)), save)  # noqa: E731
-        for most in (1, 32, 33, 700, 5000, 70000):
+        for most in (1, 8, 9, 32, 33, 100, 700, 5000, 70000):
             for t in {1, 31, most // 3, most // 2, most - 1, most}:
                 if 0 < t <= most:
                     for s in (1, 3):
@@ -244,7 +244,7 @@ def test_scan_workspace_covers_smaller_calls(lib, channels, groups):
                         ws = _addr(9) if size(most, 3) else None
                         assert _scan(lib, _sc(tokens=t, seqs=s, **kw), save, ws=ws, nbytes=size(most, 3), S0=None, S=None,
                                      **rows) == L.LQ_ERR_ALIAS, (most, t, s)
-    assert lib.leapquant_scan_workspace(_by(_sc(tokens=32)), 0) == 0 < lib.leapquant_scan_workspace(_by(_sc(tokens=33)), 0)
+    assert lib.leapquant_scan_workspace(_by(_sc(tokens=8)), 0) == 0 < lib.leapquant_scan_workspace(_by(_sc(tokens=9)), 0)
 
 
 # ---------------------------------------------------------------- block norm
