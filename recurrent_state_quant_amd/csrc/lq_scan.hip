@@ -10,12 +10,12 @@
 // steps (the whole chunk decays by e^(A sum)), the states before every chunk
 // from these, and the tokens again from there.
 //
-// Bound by vector instructions in the first and the third launch (73 to 82 % of
+// Bound by vector instructions in the first and the third launch (82 % of
 // the issue slots taken): with 16 states a token and channel take 16 exponentials,
 // of two slots each, in both, and 32 to 48 products and sums.  One prompt of 4,096
-// tokens x 4,096 channels in bf16: 62 + 10 + 82 us.  16,384 tokens x 4,096 of 24
-// sequences in fp16: 214 + 28 + 314.  8,192 x 2,048 of four, states kept for the
-// gradient: 65 + 13 + 94.  One launch that hands the states from chunk to chunk
+// tokens x 4,096 channels in bf16: 60 + 8 + 84 us.  16,384 tokens x 4,096 of 24
+// sequences in fp16: 217 + 28 + 317.  8,192 x 2,048 of four, states kept for the
+// gradient: 65 + 14 + 97.  One launch that hands the states from chunk to chunk
 // would halve the exponentials of a chunk only where the chunks ran one after the
 // other, and so few waves do not fill the chip.  Keeping the steps of the first
 // launch for the third would save it 7 us of the 89 it then took of the prompt,

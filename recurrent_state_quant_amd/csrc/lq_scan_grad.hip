@@ -18,8 +18,8 @@
 // issue slots are taken, at two waves a SIMD with 16 states): each token's decays
 // are computed twice, and with the sums over the channels a state takes some 20
 // instructions.  8,192 tokens x 2,048 channels x 16 states in bf16: chunks from zero
-// 75 us, between them 11, main kernel 249, the sums of its waves 9.  1,021 tokens x
-// 1,111 channels x 8 states in fp32: 10 + 6 + 27 + 4.
+// 71 us, between them 11, main kernel 255, the sums of its waves 9.  1,021 tokens x
+// 1,111 channels x 8 states in fp32: 10 + 5 + 22 + 4.
 #include "lq_scan_device.h"
 
 namespace lq {
