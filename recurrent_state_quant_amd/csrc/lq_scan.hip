@@ -10,9 +10,9 @@
 // steps (the whole chunk decays by e^(A sum)), the states before every chunk
 // from these, and the tokens again from there.
 //
-// Bound by vector instructions in the first and the third launch (82 % of
-// the issue slots taken): with 16 states a token and channel take 16 exponentials,
-// of two slots each, in both, and 32 to 48 products and sums.  One prompt of 4,096
+// Bound by vector instructions in the first and the third launch (82 % of the issue
+// slots taken): with 16 states a token and channel take 16 exponentials, of two slots
+// each, in both, and 32 to 48 products and sums.  One prompt of 4,096
 // tokens x 4,096 channels in bf16: 60 + 8 + 84 us.  16,384 tokens x 4,096 of 24
 // sequences in fp16: 217 + 28 + 317.  8,192 x 2,048 of four, states kept for the
 // gradient: 65 + 14 + 97.  One launch that hands the states from chunk to chunk
@@ -24,13 +24,12 @@
 
 namespace lq {
 
-
-// kScanOut, kScanGated: the chunks' outputs from the states before them (gated
-// by z, with the states kept for the gradient); kScanLocal: the chunks' states from
-// zero.  Where there are outputs, four
-// tokens' inputs are loaded together, which leaves room for a wave a SIMD more than
-// eight do (324 us for 336 of 16,384 tokens x 4,096 channels, 82 for 83 of 4,096 x
-// 4,096); where there are none, eight (206 us for 214).
+// kScanOut: the chunks' outputs from the states before them (kScanGated: gated by z,
+// kScanSave: with the states kept for the gradient); kScanLocal: the chunks' states
+// from zero.  Where there are outputs, four tokens' inputs are loaded together, which
+// leaves room for a wave a SIMD more than eight do (324 us for 336 of 16,384 tokens x
+// 4,096 channels, 82 for 83 of 4,096 x 4,096); where there are none, eight (206 us
+// for 214).
 enum { kScanLocal = 0, kScanOut = 1, kScanGated = 2, kScanSave = 4 };
 template <class E, int N, int MODE>
 __global__ __launch_bounds__(256, scan_forward_waves(N)) void scan_kernel(const ScanArgs A, int tiles, int64_t waves) {

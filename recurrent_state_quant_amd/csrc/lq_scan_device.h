@@ -70,8 +70,9 @@ __device__ __forceinline__ T lane_load(const T *row, int c) {
 // Stores of lanes that may have nothing to store, without a branch: one around
 // them would leave the compiler with an unknown number of stores in flight, and so
 // waiting for all of them wherever it needs a load that came before.  `bytes` is
-// the row's length; lanes of no channel have an offset behind it.
-__device__ __forceinline__ uint32_t lane_offset(bool on, int c, int size) { return on ? (uint32_t)c * size : ~0u; }
+// the row's length, at most 2^24; lanes of no channel have an offset behind it (and
+// far enough from 2^32 that nothing wraps).
+__device__ __forceinline__ uint32_t lane_offset(bool on, int c, int size) { return on ? (uint32_t)c * size : 1u << 30; }
 template <class T>
 __device__ __forceinline__ void lane_store(T *row, int bytes, uint32_t off, T x) {
   const auto r = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void *>(row_address(row)), (short)0, bytes, 0x00020000);
