@@ -13,9 +13,9 @@
 // Bound by vector instructions in the first and the third launch (82 % of the issue
 // slots taken): with 16 states a token and channel take 16 exponentials, of two slots
 // each, in both, and 32 to 48 products and sums.  One prompt of 4,096
-// tokens x 4,096 channels in bf16: 60 + 8 + 84 us.  16,384 tokens x 4,096 of 24
-// sequences in fp16: 217 + 28 + 317.  8,192 x 2,048 of four, states kept for the
-// gradient: 65 + 14 + 97.  One launch that hands the states from chunk to chunk
+// tokens x 4,096 channels in bf16: 59 + 8 + 82 us.  16,384 tokens x 4,096 of 24
+// sequences in fp16: 204 + 28 + 298.  8,192 x 2,048 of four, states kept for the
+// gradient: 63 + 14 + 98.  One launch that hands the states from chunk to chunk
 // would halve the exponentials of a chunk only where the chunks ran one after the
 // other, and so few waves do not fill the chip.  Keeping the steps of the first
 // launch for the third would save it 7 us of the 89 it then took of the prompt,
@@ -95,6 +95,15 @@ __global__ __launch_bounds__(256, scan_forward_waves(N)) void scan_kernel(const 
       fx[u] = to_f(rx[u]);
       fd[u] = to_f(rd[u]) + bias;
       fz[u] = GATE ? to_f(rz[u]) : 0.f;
+    }
+    // converted before the next loads begin, which take the same registers: converted
+    // where they are used they would be copied (84 for 82 us of the prompt above)
+#pragma unroll
+    for (int u = 0; u < ahead; ++u) {
+      asm volatile("" : "+v"(fx[u]), "+v"(fd[u]));
+      if (GATE) asm volatile("" : "+v"(fz[u]));
+#pragma unroll
+      for (int r = 0; r < ScanLanes<E, N>::rows; ++r) asm volatile("" : "+v"(fb[u][r]));
     }
     if (t + ahead < k.t1) load(t + ahead);
     scan_steps<E>(A, fd);

@@ -18,7 +18,7 @@
 // issue slots are taken, at two waves a SIMD with 16 states): each token's decays
 // are computed twice, and with the sums over the channels a state takes some 20
 // instructions.  8,192 tokens x 2,048 channels x 16 states in bf16: chunks from zero
-// 71 us, between them 11, main kernel 255, the sums of its waves 9.  1,021 tokens x
+// 69 us, between them 11, main kernel 252, the sums of its waves 9.  1,021 tokens x
 // 1,111 channels x 8 states in fp32: 10 + 5 + 22 + 4.
 #include "lq_scan_device.h"
 
@@ -71,6 +71,14 @@ __global__ __launch_bounds__(256, N > 16 ? 3 : 4) void scan_grad_local_kernel(co
       fd[u] = to_f(rd[u]) + bias;
       fy[u] = to_f(ry[u]);
       fz[u] = GATE ? to_f(rz[u]) : 0.f;
+    }
+    // (as forward: converted before the next loads begin)
+#pragma unroll
+    for (int u = 0; u < ahead; ++u) {
+      asm volatile("" : "+v"(fd[u]), "+v"(fy[u]));
+      if (GATE) asm volatile("" : "+v"(fz[u]));
+#pragma unroll
+      for (int r = 0; r < ScanLanes<E, N>::rows; ++r) asm volatile("" : "+v"(fc[u][r]));
     }
     if (t - ahead >= k.t0) load(t - ahead);
     scan_steps<E>(A, fd);
