@@ -637,7 +637,8 @@ int leapquant_scan_backward(const lq_scan *sc, const int32_t *cu_seqlens, const 
  * With heads of 128 values, out_norm and a SiLU gate it is the gated norm of a
  * recurrence's outputs; with one head of the model's width, res and y it joins
  * a block to the residual stream and norms it for the next one.  y is made of h
- * before h is rounded.  Values below 2^60. */
+ * before h is rounded.  Values of a, z, res and h below 2^60, gradients below
+ * 2^50. */
 typedef struct lq_block_norm {
   int64_t tokens;          /* >= 0                                             */
   int32_t heads;           /* rows of a token, >= 1                            */

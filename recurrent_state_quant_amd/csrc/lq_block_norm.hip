@@ -57,6 +57,17 @@ __device__ __forceinline__ float row_sum(float x, float2 *sh, int &turn) {
 template <int LANES>
 constexpr int norm_threads() { return LANES > 256 ? LANES : 256; }
 
+// Values up to 2^60 have squares whose sum over 8,192 of them is 2^133.  So rows of
+// more than 128 values sum those of x 2^-7, and 2^14 comes back with the reciprocal of
+// their number: powers of two, so that nothing rounds otherwise.
+template <int LANES>
+constexpr float norm_root() { return LANES > 16 ? 0x1p-7f : 1.f; }
+template <int LANES>
+__device__ __forceinline__ float row_root(float squares, float inv, float eps) {
+  constexpr float up = 1.f / (norm_root<LANES>() * norm_root<LANES>());
+  return 1.f / sqrtf(fmaf(squares, inv * up, eps));
+}
+
 // A row's arguments as a lane uses them
 struct BlockRow {
   int64_t t;
@@ -90,6 +101,7 @@ __global__ __launch_bounds__(norm_threads<LANES>()) void block_norm_kernel(const
   __shared__ float2 sh[LANES > 64 ? 2 * (LANES / 64) : 1];
   int turn = 0;
   constexpr int per = norm_threads<LANES>() / LANES;
+  constexpr float down = norm_root<LANES>() * norm_root<LANES>();
   const BlockRow b = block_row<LANES>(A, (int64_t)blockIdx.x * per + threadIdx.x / LANES, rows);
   const bool gate = A.gate, res = A.res.ptr;
   Raw8<E> ra[R], rz[R];
@@ -108,12 +120,12 @@ __global__ __launch_bounds__(norm_threads<LANES>()) void block_norm_kernel(const
     raw_floats(x[r], ra[r]);
     if (b.col + r * LANES * 8 < A.dim) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(x[r][e], x[r][e], ss);
+      for (int e = 0; e < 8; ++e) ss = fmaf(x[r][e] * down, x[r][e], ss);
     }
   }
   const float inv = 1.f / (float)A.dim;
   if (A.out_norm) {
-    const float m = 1.f / sqrtf(fmaf(row_sum<LANES>(ss, sh, turn), inv, A.eps));
+    const float m = row_root<LANES>(row_sum<LANES>(ss, sh, turn), inv, A.eps);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       float w[8];
@@ -138,12 +150,12 @@ __global__ __launch_bounds__(norm_threads<LANES>()) void block_norm_kernel(const
     for (int e = 0; e < 8; ++e) x[r][e] = res ? fmaf(A.scale, x[r][e], s[e]) : A.scale * x[r][e];
     if (col < A.dim) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(x[r][e], x[r][e], ss);
+      for (int e = 0; e < 8; ++e) ss = fmaf(x[r][e] * down, x[r][e], ss);
       if (A.h.ptr && b.on) store8(at<S>(A.h, b.t, b.h) + col, x[r]);
     }
   }
   if (!A.y.ptr) return;
-  const float m = 1.f / sqrtf(fmaf(row_sum<LANES>(ss, sh, turn), inv, A.eps));
+  const float m = row_root<LANES>(row_sum<LANES>(ss, sh, turn), inv, A.eps);
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     const int col = b.col + r * LANES * 8;
@@ -172,6 +184,7 @@ __global__ __launch_bounds__(norm_threads<LANES>(), R == 1 ? 3 : 2) void block_n
   __shared__ float sum[per][2][LANES * R * 8];
   int turn = 0;
   const bool gate = A.gate, silu = A.gate == 1, res = A.res.ptr, dy = A.dy.ptr, dh = A.dh.ptr;
+  constexpr float root = norm_root<LANES>(), down = root * root;
   const float inv = 1.f / (float)A.dim;
   const int group = threadIdx.x / LANES;
   const auto add = [&](int p, int r, const float (&x)[8]) {
@@ -220,7 +233,7 @@ __global__ __launch_bounds__(norm_threads<LANES>(), R == 1 ? 3 : 2) void block_n
       rh[r] = nh[r];
     }
     if (row0 + step < rows) load(row0 + step + group);
-    float ma = 1.f, x[R][8], n[R][8], sg[R][8];  // h; the normed a; 1 / (1 + e^-z)
+    float ma = 1.f, x[R][8], n[R][8], sg[R][8];  // h root; the normed a; 1 / (1 + e^-z)
     if (A.out_norm) {
       float ss = 0.f;
 #pragma unroll
@@ -229,9 +242,9 @@ __global__ __launch_bounds__(norm_threads<LANES>(), R == 1 ? 3 : 2) void block_n
         float a[8];
         raw_floats(a, ra[r]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(a[e], a[e], ss);
+        for (int e = 0; e < 8; ++e) ss = fmaf(a[e] * down, a[e], ss);
       }
-      ma = 1.f / sqrtf(fmaf(row_sum<LANES>(ss, sh, turn), inv, A.eps));
+      ma = row_root<LANES>(row_sum<LANES>(ss, sh, turn), inv, A.eps);
     }
     float ss = 0.f, hg = 0.f;
 #pragma unroll
@@ -245,7 +258,7 @@ __global__ __launch_bounds__(norm_threads<LANES>(), R == 1 ? 3 : 2) void block_n
         for (int e = 0; e < 8; ++e) n[r][e] *= ma * w[e];
       }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[r][e] = A.scale * n[r][e];
+      for (int e = 0; e < 8; ++e) x[r][e] = A.scale * root * n[r][e];
       if (gate) {
         float z[8];
         raw_floats(z, rz[r]);
@@ -263,7 +276,7 @@ __global__ __launch_bounds__(norm_threads<LANES>(), R == 1 ? 3 : 2) void block_n
         if (res) {
           raw_floats(g, rr[r]);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[r][e] += g[e];
+          for (int e = 0; e < 8; ++e) x[r][e] = fmaf(root, g[e], x[r][e]);
         }
         block_weights(A.wi, col, A.dim, w);
         raw_floats(g, ry[r]);
@@ -277,8 +290,8 @@ __global__ __launch_bounds__(norm_threads<LANES>(), R == 1 ? 3 : 2) void block_n
     float mh = 0.f, c = 0.f;
     if (dy) {
       row_sums<LANES>(ss, hg, sh, turn);
-      mh = 1.f / sqrtf(fmaf(ss, inv, A.eps));
-      c = hg * inv * mh * mh;
+      mh = row_root<LANES>(ss, inv, A.eps);
+      c = hg * (inv / down) * mh * mh;
     }
     float dn[R][8], ag = 0.f;
 #pragma unroll
@@ -297,7 +310,7 @@ __global__ __launch_bounds__(norm_threads<LANES>(), R == 1 ? 3 : 2) void block_n
         for (int e = 0; e < 8; ++e) H[e] = fmaf(mh, fmaf(-x[r][e], c, w[e] * g[e]), H[e]);
         if (A.dwi && b.on) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) g[e] *= x[r][e] * mh;
+          for (int e = 0; e < 8; ++e) g[e] *= x[r][e] * (mh / root);
           add(1, r, g);
         }
       }
