@@ -79,7 +79,7 @@ struct ScanArgs {
   const float *dS;
   float *dS0;
   float *part_bc;  // [tiles][tokens][2 * states], in the order of the gradient's kernel
-  float *part_a;   // [slots][states + 2][channels]
+  float *part_a;   // [chunk slots][states + 2][channels]
 };
 
 // Tokens whose states the gradient holds in registers at once, and so how often
@@ -142,19 +142,24 @@ inline int scan_grad_chunk(int64_t tokens, int64_t seqs, int channels, int group
   return scan_chunk_tokens(tokens, seqs, (scan_tiles(channels, groups) + 3) / 4, scan_grad_waves(states), 0.7);
 }
 inline int scan_grad_part(int chunk) { return chunk >= kScanShort ? chunk / 2 : chunk; }
-// The most slots, of chunks or of those from zero, of any call with at most these
-// tokens and sequences
+// The most slots of any call with at most these tokens and sequences, of chunks of
+// `least` tokens and more, or shorter ones of calls that do not fill the chip
+inline int64_t scan_most_of(int64_t tokens, int64_t seqs, int64_t workgroups, int waves, int least) {
+  const int64_t all = scan_slots(tokens, seqs, kScanLeast), many = scan_slots(tokens, seqs, least);
+  const int64_t few = scan_few(workgroups, waves);
+  return few > all ? all : few > many ? few : many;
+}
+// Of the gradient's chunks,
+inline int64_t scan_most_chunks(int64_t tokens, int64_t seqs, int channels, int groups, int states) {
+  return scan_most_of(tokens, seqs, (scan_tiles(channels, groups) + 3) / 4, scan_grad_waves(states), kScanShort);
+}
+// and of the forward pass's, with `grad` also the gradient's and those from zero
 inline int64_t scan_most_slots(int64_t tokens, int64_t seqs, int channels, int groups, int states, bool grad) {
   const int64_t workgroups = (scan_tiles(channels, groups) + 3) / 4;
-  const int64_t all = scan_slots(tokens, seqs, kScanLeast);
-  int64_t few = scan_few(workgroups, scan_forward_waves(states)), many = scan_slots(tokens, seqs, kScanShort);
-  if (grad) {
-    const int64_t back = scan_few(workgroups, scan_grad_waves(states));
-    if (back > few) few = back;
-    many = scan_slots(tokens, seqs, scan_grad_part(kScanShort));
-  }
-  if (few > all) few = all;
-  return few > many ? few : many;
+  const int64_t most = scan_most_of(tokens, seqs, workgroups, scan_forward_waves(states), kScanShort);
+  if (!grad) return most;
+  const int64_t back = scan_most_of(tokens, seqs, workgroups, scan_grad_waves(states), scan_grad_part(kScanShort));
+  return most > back ? most : back;
 }
 
 struct BlockNormArgs {

@@ -22,6 +22,7 @@ int grad_run(int64_t t, int64_t c) { return conv_grad_run(t, c); }
 int64_t grad_blocks(int64_t t, int64_t run) { return conv_grad_blocks(t, run); }
 int64_t most_blocks(int64_t t) { return conv_grad_most(t); }
 int64_t slots(int64_t t, int64_t s, int chunk) { return scan_slots(t, s, chunk); }
+int64_t most_chunks(int64_t t, int64_t s, int c, int g, int n) { return scan_most_chunks(t, s, c, g, n); }
 int64_t most_slots(int64_t t, int64_t s, int c, int g, int n, int grad) { return scan_most_slots(t, s, c, g, n, grad); }
 }
 """
@@ -43,7 +44,7 @@ def rules(tmp_path_factory):
     for name, args, back in (("forward_chunk", scan, i32), ("grad_chunk", scan, i32), ("grad_part", [i32], i32),
                              ("run_tokens", [i64, i64, i32], i32), ("grad_run", [i64, i64], i32),
                              ("grad_blocks", [i64, i64], i64), ("most_blocks", [i64], i64), ("slots", [i64, i64, i32], i64),
-                             ("most_slots", scan + [i32], i64)):
+                             ("most_slots", scan + [i32], i64), ("most_chunks", scan, i64)):
         f = getattr(lib, name)
         f.argtypes, f.restype = args, back
     return lib
@@ -91,11 +92,12 @@ def test_chunks_fit_the_workspace(rules, states):
                 assert part % 4 == 0 and grad % part == 0 and grad // part <= 2
                 if tokens <= 8:
                     assert forward >= tokens   # one chunk: a forward call needs no workspace
-                only, both = rules.most_slots(*args, 0), rules.most_slots(*args, 1)
+                only, both, whole = rules.most_slots(*args, 0), rules.most_slots(*args, 1), rules.most_chunks(*args)
                 assert rules.slots(tokens, seqs, forward) <= only <= both and rules.slots(tokens, seqs, part) <= both
+                assert rules.slots(tokens, seqs, grad) <= whole <= both
                 for smaller in (v for k, v in last.items() if k[0] <= tokens and k[1] <= seqs):
-                    assert smaller[0] <= only and smaller[1] <= both
-                last[tokens, seqs] = only, both
+                    assert smaller[0] <= only and smaller[1] <= both and smaller[2] <= whole
+                last[tokens, seqs] = only, both, whole
 
 
 @pytest.mark.parametrize("softplus", [True, False])
@@ -117,3 +119,17 @@ def test_sequences_beside_one_another(softplus, plain):
                 assert (b[m] >= a[m] * (1 - 1e-12)).all()
             else:
                 assert torch.allclose(a[m], b[m], rtol=1e-10, atol=1e-12), m
+
+
+def test_workspace_of_a_training_step():
+    """8,192 tokens in 4 sequences, 2,048 channels, 16 states: states kept before every fourth token, states carried and
+    steps summed for chunks from zero of at least 16 tokens, shares of dB and dC of every wave of 64 channels, shares of
+    dA, dD and dbias for chunks of at least 32 tokens."""
+    import recurrent_state_quant_amd as lq
+    T, seqs, c, N = 8192, 4, 2048, 16
+    plan = lq.LeapQuantScan(T, seqs, c, N, device="cpu", save=True)
+    parts, chunks = T // 16 + seqs, T // 32 + seqs
+    kept, carried, sums = (T // 4 + seqs) * c * N * 4, parts * c * N * 4, parts * c * 4
+    shares, weights = c // 64 * T * 2 * N * 4, chunks * (N + 2) * c * 4
+    assert plan.workspace.numel() == kept + carried + sums + shares + weights
+    assert [round(v / 1e6) for v in (kept, carried, sums, shares, weights)] == [269, 68, 4, 34, 38]
