@@ -97,8 +97,12 @@ __device__ __forceinline__ float exp_full(float x) {
 }
 // 1 / (1 + e^-x)
 __device__ __forceinline__ float sigmoid(float x) { return __builtin_amdgcn_rcpf(1.f + exp_full(-x)); }
-// The same for results of type E: where they have 16 bits, without the rest of the
-// exponent's product (|x| 2^-24 of e^-x), at half of the instructions
+// The same of x made of inputs of type E, for results of type E: where these have 16
+// bits, without the rest of the exponent's product (up to 1.25 |x| 2^-24 of e^-x), at
+// half of the instructions.  The half step of a gate's input is 2^13 times that and
+// more, also for the fp32 sums that it enters (gradients of weights and of an fp32
+// stream).  Kernels that wait for memory anyway keep the full form: the norm forward
+// and the single tokens' gate.
 template <class E>
 __device__ __forceinline__ float sigmoid_for(float x) {
   if constexpr (sizeof(E) == 4) return sigmoid(x);

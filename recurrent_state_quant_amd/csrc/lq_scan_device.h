@@ -19,9 +19,11 @@ __device__ __forceinline__ float softplus_of(float v, float e) {
   p = fmaf(p * q, r, r);
   return fmaf(2.f, p, fmaxf(v, 0.f));
 }
-// e^-|v|.  For inputs of 16 bits without the rest of the exponent's product, |v|
-// 2^-24 of it: their own steps are 2^15 times that, and the sum with the bias in v
-// rounds by as much.
+// e^-|v|.  For inputs of 16 bits without the rest of the exponent's product, which
+// with that of log2 e itself is up to 1.25 |v| 2^-24 of the result (5e-7 at v = -7),
+// and so are the fp32 states and gradients that the steps enter.  With a bias the sum
+// v = dt + bias has rounded by up to |v| 2^-24 already, which leaves as much; without
+// one v is the input, whose own half step is 2^13 (fp16) or 2^16 (bf16) times that.
 template <class E>
 __device__ __forceinline__ float scan_exp(float v) {
   if constexpr (sizeof(E) == 4) return exp_full(-fabsf(v));

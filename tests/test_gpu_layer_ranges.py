@@ -55,3 +55,38 @@ def test_norms_of_the_largest_values(dim, dtype, of):
         if out_norm:
             check(dwo, grads[2], 4 * dim + 128 + T, "dwo")
         check(dwi, grads[3], 4 * dim + 128 + T, "dwi")
+
+
+@pytest.mark.parametrize("bias", [True, False])
+@pytest.mark.parametrize("v", [-60.0, -24.0, -12.0, -7.0, -3.0, 3.0, 12.0])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_steps_of_16_bit_inputs(dtype, v, bias):
+    """Their states and the fp32 gradients keep the accuracy of fp32 sums: a step log(1 + e^v) is off by the 16
+    roundings of tests/layer_reference.py and by three of |v|: the sum of dt and its bias, the exponent's product with
+    log2 e (of which calls with 16-bit inputs leave the rest out) and log2 e itself, a quarter."""
+    cu, c, N = [0, 1, 3], 64, 8
+    g = torch.Generator().manual_seed(9)
+    r = lambda *s: torch.randn(s, generator=g)  # noqa: E731
+    x = {m: r(3, c).to(dtype) for m in ("x", "dy")} | {m: r(3, 1, N).to(dtype) for m in ("B", "C")}
+    x["dt"] = (0.3 * r(3, c) if bias else v * (1 + 0.1 * torch.rand((3, c), generator=g))).to(dtype)
+    x["A"], x["bias"] = -torch.rand((c, N), generator=g) - 0.1, v + 0.1 * r(c) if bias else None
+    far = float((x["dt"].float() + (0 if x["bias"] is None else x["bias"])).abs().max())
+    d = {m: None if t is None else t.to(DEV) for m, t in x.items()}
+    plan = lq.LeapQuantScan(3, 2, c, N, dtype=dtype, save=True)
+    where = torch.tensor(cu, dtype=torch.int32, device=DEV)
+    y, S = torch.empty_like(d["x"]), torch.empty((2, c, N), device=DEV)
+    lq.leapquant_scan_forward(plan, where, d["x"], d["dt"], d["A"], d["B"], d["C"], y, dt_bias=d["bias"], S=S)
+    out = {m: torch.empty_like(d[m]) for m in ("x", "dt", "A", "B", "C")}
+    db = None if x["bias"] is None else torch.empty_like(d["bias"])
+    lq.leapquant_scan_backward(plan, where, d["x"], d["dt"], d["A"], d["B"], d["C"], d["dy"], out["x"], out["dt"], out["A"],
+                               out["B"], out["C"], dt_bias=d["bias"], ddt_bias=db)
+    w = {m: None if t is None else t.double() for m, t in x.items()}
+    zero = torch.zeros((2, c, N), dtype=torch.float64)
+    args = [w["x"], w["dt"], w["A"], w["B"], w["C"], None, w["bias"], None, zero, w["dy"], zero]
+    ref, top = (R.scan_adjoint(cu, *args, absolute=a) for a in (False, True))
+    # of each entry's own terms; a gradient of A has two steps in a term, a step's slope is off by as much as the step
+    for got, m, n in ((S, "S", 4 * 2 + 32 + 3 * far), (out["A"], "A", 9 * 2 + 2 * N + c + 160 + 3 + 6 * far),
+                      (db, "bias", 9 * 2 + 2 * N + c + 160 + 3 + 6 * far)):
+        if got is not None:
+            off = (got.cpu().double() - ref[m]).abs()
+            assert (off <= n * 2.0 ** -24 * top[m] + 2.0 ** -120).all(), m
