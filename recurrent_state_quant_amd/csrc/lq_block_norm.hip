@@ -11,8 +11,8 @@
 // LANES lanes hold a row, R pieces of eight values each (16-byte accesses in
 // 16-bit types), so that every value is read and written once; statistics are
 // in fp32.  Bound by memory traffic: 16,384 x 32 rows of 128 in bf16, normed and
-// gated, 82 us (4.9 TB/s); 8,192 rows of 4,096 with gate, fp32 stream and both
-// norms 87 us (5.4 TB/s, part of it from cache), backward 172 + 5 (4.3 TB/s).
+// gated, 80 to 86 us (4.7 to 5.0 TB/s); 8,192 rows of 4,096 with gate, fp32 stream and
+// both norms 87 us (5.4 TB/s, part of it from cache), backward 165 + 5 (4.5 TB/s).
 #include "lq_layer_device.h"
 
 namespace lq {
@@ -171,8 +171,10 @@ __global__ __launch_bounds__(norm_threads<LANES>()) void block_norm_kernel(const
 // in LDS, each lane's own columns for each row of a workgroup: in registers they
 // would take the room of a third wave a SIMD.
 // Three workgroups of 256 threads a CU where a lane has one piece, two with two
-// pieces, one of 512 threads.  Of 8,192 rows of 4,096: 172 us; three of two pieces
-// spill (327 us), 512 lanes with one piece each, one workgroup a CU, 222 for 198.
+// pieces, one of 512 threads.  Of 8,192 rows of 4,096: 165 us; three of two pieces
+// spill (327 us for 172), 512 lanes with one piece each, one workgroup a CU, 222 for 198.
+// Two pieces of fp32 rows spill 7 to 10 registers a lane also at two workgroups (both
+// calls of 8,192 rows of 4,096 take 366 us, at the copy's rate 270).
 static int64_t norm_most_blocks(int dim) {
   return dim <= 512 ? 768 : dim <= 1024 ? 512 : dim <= 2048 ? 768 : dim <= 4096 ? 512 : 256;
 }

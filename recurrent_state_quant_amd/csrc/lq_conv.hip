@@ -10,7 +10,7 @@
 // 16 bytes of channels in registers and walks a run of tokens, so that every input
 // is read once but for the K - 1 around a run.  With width 4 in bf16, 16,384 tokens
 // x 8,192 channels of 24 sequences take 118 us (4.6 TB/s of input and output), 8,192
-// x 6,144 43 us forward (4.7 TB/s) and 72 + 5 backward (4.2 TB/s of two inputs and an
+// x 6,144 43 us forward (4.7 TB/s) and 69 + 5 backward (4.4 TB/s of two inputs and an
 // output).  Loads and stores past the caches gain nothing
 // (48 us for 43 of inputs that are cached).
 #include "lq_layer_device.h"

@@ -99,10 +99,13 @@ inline int64_t scan_slots(int64_t tokens, int64_t seqs, int chunk) { return toke
 // what w waves leave unhidden; 1.4 measured forward, 0.7 in the gradient, whose
 // instructions are three times as many).  `most` workgroups fit a CU; more run in
 // rounds.  So the time is (chunk + what a wave's beginning takes, in tokens) times
-// the rounds' w + stall, and the best length one that fills the CUs evenly: 4,096
-// tokens x 64 waves took 98 us forward in chunks of 72 (3.6 waves a SIMD), 105 of
-// 80 (3.3); the gradient of 8,192 tokens x 32 waves of four sequences takes 251 us in
-// chunks of 136, 261 of 40 or 144, 296 of 96, 328 of 128.
+// the rounds' w + stall, and the best length one that fills the CUs evenly.  All three
+// forward launches of 4,096 tokens x 64 waves take 136 us in the chunks of 88 that are
+// taken (2.9 waves a SIMD), 133 of 64 (4.0), 141 of 56 (4.6) and of 72 (3.6), 155 of 80
+// (3.3), 178 of 120 (2.2); of 16,384 x 64 waves in 24 sequences 463 in chunks of 112,
+// 453 of 72, 479 of 56, 471 of 104, 508 of 160.  The gradient's main launch of 8,192
+// tokens x 32 waves in four sequences takes 220 us in chunks of 136, 225 of 40, 232 of
+// 144, 266 of 96, 308 of 128.
 // A call whose sequences may have several chunks takes two launches more, 25 tokens'
 // time, and every chunk of a sequence lengthens the chain between them by 0.3
 // of a token's; one that needs no chunks from zero takes 0.6 of the rest.  (200 tokens x
@@ -129,7 +132,8 @@ inline int scan_chunk_tokens(int64_t tokens, int64_t seqs, int64_t workgroups, i
   if (tokens <= kScanMost) look(tokens <= kScanLeast ? kScanLeast : (int)(tokens + 7) / 8 * 8);
   return best;
 }
-// Waves of the forward kernel that a SIMD holds
+// Waves of the forward kernel that a SIMD holds: of the chunks from zero, which take
+// more registers than the outputs, of which one to three waves more fit
 constexpr int scan_forward_waves(int states) { return states > 16 ? 3 : states > 8 ? 5 : 6; }
 inline int scan_forward_chunk(int64_t tokens, int64_t seqs, int channels, int groups, int states) {
   return scan_chunk_tokens(tokens, seqs, (scan_tiles(channels, groups) + 3) / 4, scan_forward_waves(states), 1.4);

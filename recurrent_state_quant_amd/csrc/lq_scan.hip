@@ -10,12 +10,14 @@
 // steps (the whole chunk decays by e^(A sum)), the states before every chunk
 // from these, and the tokens again from there.
 //
-// Bound by vector instructions in the first and the third launch (82 % of the issue
-// slots taken): with 16 states a token and channel take 16 exponentials, of two slots
+// Bound by vector instructions in the first and the third launch (of one prompt, with
+// three waves a SIMD, they take 77 and 71 % of the issue slots while the chip is busy):
+// with 16 states a token and channel take 16 exponentials, of two slots
 // each, in both, and 32 to 48 products and sums.  One prompt of 4,096
-// tokens x 4,096 channels in bf16: 59 + 8 + 82 us.  16,384 tokens x 4,096 of 24
-// sequences in fp16: 204 + 28 + 298.  8,192 x 2,048 of four, states kept for the
-// gradient: 63 + 14 + 98.  One launch that hands the states from chunk to chunk
+// tokens x 4,096 channels in bf16: 54 + 7 + 75 us.  16,384 tokens x 4,096 of 24
+// sequences in fp16: 179 + 25 + 260.  8,192 x 2,048 of four, states kept for the
+// gradient: 55 + 13 + 93.  (These with a warm chip; pairs of figures further down were
+// measured one against the other, most of them without.)  One launch that hands the states from chunk to chunk
 // would halve the exponentials of a chunk only where the chunks ran one after the
 // other, and so few waves do not fill the chip.  Keeping the steps of the first
 // launch for the third would save it 7 us of the 89 it then took of the prompt,
@@ -181,7 +183,7 @@ __global__ __launch_bounds__(256) void scan_carry_kernel(const ScanArgs A, int s
 // One token of each row.  Four states a lane, the lanes of a channel side by
 // side, so that the states move in whole lines.  Bound by reading and writing
 // them, past the caches, as a step's states are not read again before the next: 256
-// rows x 4,096 channels x 16 states 30 to 33 us, 4.3 to 4.7 TB/s.
+// rows x 4,096 channels x 16 states 32 to 34 us, 4.2 to 4.5 TB/s.
 template <class E, int N>
 __global__ __launch_bounds__(256) void scan_step_kernel(const ScanArgs A, int64_t blocks_row) {
   constexpr int lanes = N / 4;

@@ -14,12 +14,17 @@
 // is computed again from them, its states stay in registers, and it is taken
 // backwards.
 //
-// Bound by vector instructions (of the time that waves are resident, 93 % of the
-// issue slots are taken, at two waves a SIMD with 16 states): each token's decays
+// Bound by vector instructions (of the time that its waves run, two a SIMD with 16
+// states, they take 89 % of the issue slots; of the whole launch, as some waves end
+// before others, 72 %): each token's decays
 // are computed twice, and with the sums over the channels a state takes some 20
 // instructions.  8,192 tokens x 2,048 channels x 16 states in bf16: chunks from zero
-// 69 us, between them 11, main kernel 252, the sums of its waves 9.  1,021 tokens x
-// 1,111 channels x 8 states in fp32: 10 + 5 + 22 + 4.
+// 61 us, between them 10, main kernel 220, the sums of its waves 9.  1,021 tokens x
+// 1,111 channels x 8 states in fp32: 9 + 5 + 22 + 4.  (As forward: with a warm chip;
+// pairs of figures below were measured one against the other, most of them without.)
+// With 32 states a lane's arrays do not fit the 256 registers that vector instructions
+// take: 84 to 105 of them lie in accumulator registers and are copied, and up to 275
+// scalars (fp32 with a gate; 13 to 47 otherwise) in lanes of vector registers.
 #include "lq_scan_device.h"
 
 namespace lq {
@@ -138,7 +143,10 @@ __global__ __launch_bounds__(256) void scan_grad_carry_kernel(const ScanArgs A, 
 // four sums over eight channels, 302 for 290: fewer instructions, but waits that two
 // waves a SIMD do not hide.
 // Lanes with bits 3 and 2 of (0, 0), (1, 0), (0, 1), (1, 1) come to hold the sums of
-// v[0], v[1], v[2], v[3] over the four lanes with the same bits 1 and 0.  (All lanes
+// v[0], v[1], v[2], v[3] over four lanes: those of either bit 3 with this lane's bits 2
+// to 0, and those with all three of them inverted (the half row mirrored).  So the lanes
+// with one pair of bits 3 and 2, whose bits 1 and 0 differ, share the sixteen out among
+// them, and the sum over the four of them is the whole.  (All lanes
 // are active; the s_nops keep the two cycles between writing a register and
 // reading it across lanes.)
 __device__ __forceinline__ float fold4(const float (&v)[4]) {
